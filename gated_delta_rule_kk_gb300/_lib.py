@@ -122,6 +122,76 @@ class GdnStateBwdArgs(ctypes.Structure):
     ]
 
 
+c_int64 = ctypes.c_int64
+
+
+class ShortConvArgs(ctypes.Structure):
+    _fields_ = [
+        ("dtype", c_int32), ("weight_dtype", c_int32),
+        ("x", c_void_p), ("weight", c_void_p), ("bias", c_void_p), ("h0", c_void_p),
+        ("ht", c_void_p), ("y", c_void_p), ("cu_seqlens", c_void_p),
+        ("x_stride", c_int64), ("x_batch_stride", c_int64),
+        ("y_stride", c_int64), ("y_batch_stride", c_int64),
+        ("B", c_int32), ("T", c_int32), ("D", c_int32), ("W", c_int32), ("N", c_int32),
+        ("silu", c_int32),
+    ]
+
+
+class ShortConvBwdArgs(ctypes.Structure):
+    _fields_ = [
+        ("dtype", c_int32), ("weight_dtype", c_int32),
+        ("dy", c_void_p), ("x", c_void_p), ("weight", c_void_p), ("bias", c_void_p),
+        ("h0", c_void_p), ("dht", c_void_p), ("dx", c_void_p),
+        ("dweight", c_void_p), ("dbias", c_void_p), ("dh0", c_void_p), ("cu_seqlens", c_void_p),
+        ("dy_stride", c_int64), ("dy_batch_stride", c_int64),
+        ("x_stride", c_int64), ("x_batch_stride", c_int64),
+        ("dx_stride", c_int64), ("dx_batch_stride", c_int64),
+        ("B", c_int32), ("T", c_int32), ("D", c_int32), ("W", c_int32), ("N", c_int32),
+        ("silu", c_int32),
+        ("workspace", c_void_p), ("workspace_bytes", c_size_t),
+    ]
+
+
+class ShortConvDecodeArgs(ctypes.Structure):
+    _fields_ = [
+        ("dtype", c_int32), ("weight_dtype", c_int32),
+        ("x", c_void_p), ("weight", c_void_p), ("bias", c_void_p), ("state", c_void_p),
+        ("slot_indices", c_void_p), ("y", c_void_p),
+        ("x_stride", c_int64), ("x_batch_stride", c_int64),
+        ("y_stride", c_int64), ("y_batch_stride", c_int64),
+        ("B", c_int32), ("T", c_int32), ("D", c_int32), ("W", c_int32), ("pool", c_int32),
+        ("silu", c_int32),
+    ]
+
+
+_SSM_TOKENS = [
+    ("x", c_void_p), ("z", c_void_p), ("Bm", c_void_p), ("Cm", c_void_p), ("dt", c_void_p),
+    ("A_log", c_void_p), ("D", c_void_p), ("dt_bias", c_void_p),
+]
+_SSM_STRIDES = [(f"{t}{kind}", c_int64) for t in ("x", "z", "Bm", "Cm", "dt", "y")
+                for kind in ("_stride", "_batch_stride")]
+_SSM_SIZES = [(n, c_int32) for n in ("B", "T", "H", "Hg", "K", "V")]
+
+
+class SsmChunkArgs(ctypes.Structure):
+    _fields_ = [
+        ("dtype", c_int32), ("dt_dtype", c_int32), *_SSM_TOKENS,
+        ("h0", c_void_p), ("ht", c_void_p), ("y", c_void_p), ("cu_seqlens", c_void_p),
+        *_SSM_STRIDES, *_SSM_SIZES, ("N", c_int32),
+        ("dt_softplus", c_int32), ("y_fp32", c_int32), ("segment_tokens", c_int32),
+        ("workspace", c_void_p), ("workspace_bytes", c_size_t),
+    ]
+
+
+class SsmDecodeArgs(ctypes.Structure):
+    _fields_ = [
+        ("dtype", c_int32), ("dt_dtype", c_int32), ("state_dtype", c_int32), *_SSM_TOKENS,
+        ("state", c_void_p), ("slot_indices", c_void_p), ("y", c_void_p),
+        *_SSM_STRIDES, *_SSM_SIZES, ("pool", c_int32),
+        ("dt_softplus", c_int32), ("y_fp32", c_int32),
+    ]
+
+
 # name -> (argtypes, restype); exactly the functions include/gdn.h declares
 SIGNATURES = {
     "gdn_chunk_workspace_size": ([ctypes.POINTER(GdnChunkArgs), ctypes.POINTER(c_size_t)], c_int32),
@@ -137,6 +207,14 @@ SIGNATURES = {
     "gdn_chunk_state_bwd": ([ctypes.POINTER(GdnStateBwdArgs), c_void_p], c_int32),
     "gdn_chunk_fwd_noalloc": ([ctypes.POINTER(GdnChunkArgs), c_void_p], c_int32),
     "gdn_noalloc_scratch_bytes": ([], c_size_t),
+    "short_conv_fwd": ([ctypes.POINTER(ShortConvArgs), c_void_p], c_int32),
+    "short_conv_bwd_workspace_size": ([ctypes.POINTER(ShortConvBwdArgs), ctypes.POINTER(c_size_t)],
+                                      c_int32),
+    "short_conv_bwd": ([ctypes.POINTER(ShortConvBwdArgs), c_void_p], c_int32),
+    "short_conv_decode": ([ctypes.POINTER(ShortConvDecodeArgs), c_void_p], c_int32),
+    "ssm_chunk_workspace_size": ([ctypes.POINTER(SsmChunkArgs), ctypes.POINTER(c_size_t)], c_int32),
+    "ssm_chunk_fwd": ([ctypes.POINTER(SsmChunkArgs), c_void_p], c_int32),
+    "ssm_decode": ([ctypes.POINTER(SsmDecodeArgs), c_void_p], c_int32),
     "gdn_self_test_wait": ([c_int32, c_int32, c_void_p], c_int32),
     "gdn_self_test_bounds": ([c_int32, c_int32, ctypes.POINTER(c_int32), c_void_p], c_int32),
     "gdn_check_device_error": ([c_void_p, ctypes.POINTER(c_int32)], c_int32),

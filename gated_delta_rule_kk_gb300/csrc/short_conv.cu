@@ -1,0 +1,718 @@
+// Short causal depthwise convolution: over prompts, its gradient, and for
+// single tokens against pooled states.
+//
+// Per channel, p_t = bias + sum_{i<W} w_i x_{t-W+1+i} and y = act(p), W <= 4:
+// 2 W operations for one element read and one written, so every form is bound
+// by memory.  A thread owns the channels of one 16-byte piece of a token row
+// (8-byte in the gradient, which keeps W + 1 sums per channel) and walks a run
+// of tokens with the last W - 1 rows in registers, so a row is read once but
+// for the W - 1 rows before each run.  Sums are float32.
+#include <initializer_list>
+#include <type_traits>
+
+#include "abi_check.h"
+#include "gdn_common.cuh"
+#include "rows.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int CV_BATCH = 4;      // rows a thread has on the way at a time
+constexpr int CV_MAX_THREADS = 256;
+
+// Weights of channels c .. c + VEC as w[tap][channel]: their VEC * W values are
+// consecutive and, for VEC > 1, a multiple of 16 bytes at a 16-byte boundary.
+template <int VEC, int W>
+__device__ __forceinline__ void load_weights(float (&w)[W][VEC], float (&bias)[VEC],
+                                             const void *weight, const void *b, bool f32, int c) {
+  auto read = [&](auto tag) {
+    using TW = decltype(tag);
+    const TW *src = static_cast<const TW *>(weight) + (size_t)c * W;
+    constexpr int PIECE = VEC == 1 ? 1 : 16 / (int)sizeof(TW);
+    if constexpr (VEC * W % PIECE == 0) {
+      float f[VEC * W];
+#pragma unroll
+      for (int i = 0; i < VEC * W; i += PIECE) {
+        Row<TW, PIECE> r;
+        r.load(src + i);
+        r.widen(f + i);
+      }
+#pragma unroll
+      for (int i = 0; i < VEC * W; ++i) w[i % W][i / W] = f[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC * W; ++i) w[i % W][i / W] = to_f32(src[i]);
+    }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) bias[e] = b ? to_f32(static_cast<const TW *>(b)[c + e]) : 0.f;
+  };
+  if (f32)
+    read(0.f);
+  else
+    read(__nv_bfloat16());
+}
+
+struct ConvSeqs {
+  const int32_t *cu;
+  int B, T, N;
+};
+
+// The sequence that token t of batch row b belongs to: the last one that does
+// not start after it (0 <= t < T, offsets checked).
+__device__ __forceinline__ int conv_sequence_of(const ConvSeqs &q, int b, int t) {
+  if (q.cu == nullptr) return b;
+  int lo = 0, hi = q.N;  // cu[lo] <= t < cu[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (q.cu[mid] <= t)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+struct ConvParams {
+  const void *x, *weight, *bias, *h0;
+  void *ht, *y;
+  int *err;
+  ConvSeqs q;
+  int64_t xs, xb, ys, yb;
+  int D, silu, w_f32;
+  int run, tiles;  // tokens of a run, runs of a batch row
+};
+
+// The rows before token t of a sequence that starts at bos: x's own, or the
+// state's (zeros without one).  `xr` is the sequence's batch row.
+template <typename T, int VEC, int W>
+__device__ __forceinline__ void load_before(float (*win)[VEC], const T *xr, int64_t xs,
+                                            const T *state, int D, int bos, int t) {
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) {
+    const int pos = t - (W - 1) + j - bos;
+    Row<T, VEC> r;
+    if (pos >= 0)
+      r.load(xr + (int64_t)(bos + pos) * xs);
+    else if (state)
+      r.load(state + (int64_t)(pos + W - 1) * D);
+    else
+      r.zero();
+    r.widen(win[j]);
+  }
+}
+
+// grid: x = runs of every batch row, then (with ht) one block per sequence;
+// y = channel blocks.
+template <typename T, int VEC, int W>
+__global__ void __launch_bounds__(CV_MAX_THREADS) conv_fwd_kernel(ConvParams p) {
+  if (!offsets_ok(p.q.cu, p.q.N, p.q.T, p.err)) return;
+  const int c = (blockIdx.y * blockDim.x + threadIdx.x) * VEC;
+  if (c >= p.D) return;
+  const int runs = p.q.B * p.tiles;
+  const T *x = static_cast<const T *>(p.x) + c;
+  const T *h0 = p.h0 ? static_cast<const T *>(p.h0) + c : nullptr;
+  if ((int)blockIdx.x >= runs) {
+    // the last W - 1 rows of sequence n
+    const int n = blockIdx.x - runs;
+    const int bos = p.q.cu ? p.q.cu[n] : 0, eos = p.q.cu ? p.q.cu[n + 1] : p.q.T;
+    if (!bounds_ok(n < p.q.N && bos >= 0 && bos <= eos && eos <= p.q.T, p.err)) return;
+    const T *xr = x + (p.q.cu ? 0 : n) * p.xb;
+    T *ht = static_cast<T *>(p.ht) + (int64_t)n * (W - 1) * p.D + c;
+    for (int j = 0; j < W - 1; ++j) {
+      const int pos = eos - bos - (W - 1) + j;
+      Row<T, VEC> r;
+      if (pos >= 0)
+        r.load(xr + (int64_t)(bos + pos) * p.xs);
+      else if (h0)
+        r.load(h0 + ((int64_t)n * (W - 1) + pos + W - 1) * p.D);
+      else
+        r.zero();
+      r.store(ht + (int64_t)j * p.D);
+    }
+    return;
+  }
+  const int b = blockIdx.x / p.tiles;
+  int t = (blockIdx.x % p.tiles) * p.run;
+  const int t1 = min(p.q.T, t + p.run);
+  if (!bounds_ok(b < p.q.B && t < t1, p.err)) return;
+  const T *xr = x + b * p.xb;
+  T *yr = static_cast<T *>(p.y) + b * p.yb + c;
+  float w[W][VEC], bias[VEC];
+  load_weights<VEC, W>(w, bias, p.weight, p.bias, p.w_f32, c);
+  for (int n = conv_sequence_of(p.q, b, t); t < t1; ++n) {
+    const int bos = p.q.cu ? p.q.cu[n] : 0, end = min(t1, p.q.cu ? p.q.cu[n + 1] : p.q.T);
+    if (t >= end) continue;  // an empty sequence
+    Row<T, VEC> next[CV_BATCH];
+    auto fetch = [&](int at) {
+#pragma unroll
+      for (int k = 0; k < CV_BATCH; ++k)
+        if (at + k < end) next[k].load(xr + (int64_t)(at + k) * p.xs);
+    };
+    fetch(t);
+    float f[W - 1 + CV_BATCH][VEC];
+    load_before<T, VEC, W>(f, xr, p.xs, h0 ? h0 + (int64_t)n * (W - 1) * p.D : nullptr, p.D, bos, t);
+    for (; t < end; t += CV_BATCH) {
+#pragma unroll
+      for (int k = 0; k < CV_BATCH; ++k) next[k].widen(f[W - 1 + k]);
+      fetch(t + CV_BATCH);
+#pragma unroll
+      for (int k = 0; k < CV_BATCH; ++k) {
+        if (t + k >= end) break;
+        float acc[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) acc[e] = bias[e];
+#pragma unroll
+        for (int i = 0; i < W; ++i) fma_row<VEC>(acc, w[i], f[k + i]);
+        if (p.silu) {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) acc[e] = silu(acc[e]);
+        }
+        Row<T, VEC> out;
+        out.round(acc);
+        out.store(yr + (int64_t)(t + k) * p.ys);
+      }
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) f[j][e] = f[CV_BATCH + j][e];
+    }
+    t = end;
+  }
+}
+
+// ---------------------------------------------------------------- gradient
+
+constexpr int CB_RUNS = 8;  // runs (warps) of a block
+
+struct ConvBwdParams {
+  const void *dy, *x, *weight, *bias, *h0, *dht;
+  void *dx, *dh0;
+  float *part;  // [blocks along time][W + 1][D], or NULL
+  int *err;
+  ConvSeqs q;
+  int64_t gs, gb, xs, xb, ds, db;
+  int D, silu, w_f32;
+  int run, tiles;  // tokens of a warp's run, blocks (of CB_RUNS runs) of a batch row
+};
+
+// Warp y of a block walks one run [lo, hi) of tokens for 32 * VEC channels.
+// dx_t = sum_i w_i dp_{t+W-1-i} needs dp of the W - 1 tokens after t, so the
+// walk goes W - 1 tokens past the run's (or the sequence's) end, where dp past
+// the sequence is zero, and row u - (W - 1) is written as token u is taken.
+// The run that holds a sequence's first token writes its dh0.  dweight and
+// dbias sums of the run's own tokens stay in registers, are added over the
+// block's runs in shared memory and leave as one partial sum per block.
+template <typename T, int VEC, int W>
+__global__ void __launch_bounds__(32 * CB_RUNS) conv_bwd_kernel(ConvBwdParams p) {
+  __shared__ float red[CB_RUNS][32 * VEC + 4];
+  if (!offsets_ok(p.q.cu, p.q.N, p.q.T, p.err)) return;
+  const int lane = threadIdx.x;
+  const int c = (blockIdx.y * 32 + lane) * VEC;
+  const bool live = c < p.D;
+  const int blocks = p.q.B * p.tiles;
+  if ((int)blockIdx.x >= blocks) {
+    // a sequence without tokens: its final state is its initial state
+    const int n = blockIdx.x - blocks;
+    if (!bounds_ok(n < p.q.N, p.err)) return;
+    const int len = p.q.cu ? p.q.cu[n + 1] - p.q.cu[n] : p.q.T;
+    if (len > 0 || !live || threadIdx.y) return;
+    for (int j = 0; j < W - 1; ++j) {
+      const int64_t at = ((int64_t)n * (W - 1) + j) * p.D + c;
+      Row<T, VEC> r;
+      if (p.dht)
+        r.load(static_cast<const T *>(p.dht) + at);
+      else
+        r.zero();
+      r.store(static_cast<T *>(p.dh0) + at);
+    }
+    return;
+  }
+  float w[W][VEC], bias[VEC], dw[W][VEC], db[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    db[e] = 0.f;
+#pragma unroll
+    for (int i = 0; i < W; ++i) dw[i][e] = 0.f;
+  }
+  const int b = blockIdx.x / p.tiles;
+  if (!bounds_ok(b < p.q.B, p.err)) return;
+  const int lo = ((blockIdx.x % p.tiles) * CB_RUNS + threadIdx.y) * p.run;
+  const int hi = min(p.q.T, lo + p.run);
+  if (live && lo < hi) {
+    load_weights<VEC, W>(w, bias, p.weight, p.bias, p.w_f32, c);
+    const T *xr = static_cast<const T *>(p.x) + b * p.xb + c;
+    const T *gr = static_cast<const T *>(p.dy) + b * p.gb + c;
+    T *dxr = static_cast<T *>(p.dx) + b * p.db + c;
+    int t0 = lo;
+    for (int n = conv_sequence_of(p.q, b, lo); t0 < hi; ++n) {
+      const int bos = p.q.cu ? p.q.cu[n] : 0, eos = p.q.cu ? p.q.cu[n + 1] : p.q.T;
+      if (t0 >= eos) continue;  // an empty sequence
+      const int own = min(eos, hi), last = min(eos, hi + W - 1);
+      const int64_t st = (int64_t)n * (W - 1) * p.D + c;
+      Row<T, VEC> nx[CV_BATCH], ng[CV_BATCH];
+      auto fetch = [&](int at) {
+#pragma unroll
+        for (int k = 0; k < CV_BATCH; ++k)
+          if (at + k < last) {
+            nx[k].load(xr + (int64_t)(at + k) * p.xs);
+            ng[k].load(gr + (int64_t)(at + k) * p.gs);
+          }
+      };
+      fetch(t0);
+      float f[W - 1 + CV_BATCH][VEC], d[W - 1 + CV_BATCH][VEC];
+      load_before<T, VEC, W>(f, xr, p.xs, p.h0 ? static_cast<const T *>(p.h0) + st : nullptr, p.D,
+                             bos, t0);
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) d[j][e] = 0.f;
+      for (int u = t0; u < own + W - 1; u += CV_BATCH) {
+#pragma unroll
+        for (int k = 0; k < CV_BATCH; ++k) {
+          nx[k].widen(f[W - 1 + k]);
+          ng[k].widen(d[W - 1 + k]);
+        }
+        fetch(u + CV_BATCH);
+#pragma unroll
+        for (int k = 0; k < CV_BATCH; ++k) {
+          float *dp = d[W - 1 + k];
+          if (u + k < last) {
+            if (p.silu) {
+              float acc[VEC];
+#pragma unroll
+              for (int e = 0; e < VEC; ++e) acc[e] = bias[e];
+#pragma unroll
+              for (int i = 0; i < W; ++i) fma_row<VEC>(acc, w[i], f[k + i]);
+#pragma unroll
+              for (int e = 0; e < VEC; ++e) {
+                // silu'(p) = s (1 + p (1 - s)), s = 1 / (1 + e^-p)
+                const float s = __fdividef(1.f, 1.f + __expf(-acc[e]));
+                dp[e] *= s * fmaf(acc[e], 1.f - s, 1.f);
+              }
+            }
+            if (u + k < own) {
+#pragma unroll
+              for (int i = 0; i < W; ++i) fma_row<VEC>(dw[i], dp, f[k + i]);
+#pragma unroll
+              for (int e = 0; e < VEC; ++e) db[e] += dp[e];
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) dp[e] = 0.f;
+          }
+          const int t = u + k - (W - 1);
+          const bool token = t >= t0 && t < own, state = t < bos && t0 == bos && p.dh0 != nullptr;
+          if (!token && !state) continue;
+          float acc[VEC];
+          const int back = t - eos + W - 1;  // the row of dht that row t became
+          if (p.dht && back >= 0) {
+            Row<T, VEC> r;
+            r.load(static_cast<const T *>(p.dht) + st + (int64_t)back * p.D);
+            r.widen(acc);
+          } else {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
+          }
+#pragma unroll
+          for (int i = 0; i < W; ++i) fma_row<VEC>(acc, w[i], d[W - 1 + k - i]);
+          Row<T, VEC> out;
+          out.round(acc);
+          if (token)
+            out.store(dxr + (int64_t)t * p.ds);
+          else
+            out.store(static_cast<T *>(p.dh0) + st + (int64_t)(t - bos + W - 1) * p.D);
+        }
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            f[j][e] = f[CV_BATCH + j][e];
+            d[j][e] = d[CV_BATCH + j][e];
+          }
+      }
+      t0 = own;
+    }
+  }
+  if (p.part == nullptr) return;
+  float *part = p.part + (int64_t)blockIdx.x * (W + 1) * p.D;
+#pragma unroll
+  for (int i = 0; i <= W; ++i) {
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) red[threadIdx.y][lane * VEC + e] = i < W ? dw[i < W ? i : 0][e] : db[e];
+    __syncthreads();
+    for (int e = threadIdx.y * 32 + lane; e < 32 * VEC; e += 32 * CB_RUNS) {
+      const int ch = blockIdx.y * 32 * VEC + e;
+      if (ch >= p.D) continue;
+      float s = 0.f;
+#pragma unroll
+      for (int r = 0; r < CB_RUNS; ++r) s += red[r][e];
+      part[(int64_t)i * p.D + ch] = s;
+    }
+  }
+}
+
+// dweight and dbias from the blocks' partial sums: block (32 channels, one tap
+// or the bias), warp y adds every 8th partial sum, then the warps in order.
+template <int W>
+__global__ void __launch_bounds__(256) conv_bwd_sum_kernel(const float *part, int blocks, int D,
+                                                           float *dweight, float *dbias, ConvSeqs q,
+                                                           int *err) {
+  __shared__ float red[8][32];
+  if (!offsets_ok(q.cu, q.N, q.T, err)) return;
+  const int c = blockIdx.x * 32 + threadIdx.x, i = blockIdx.y;
+  float s = 0.f;
+  if (c < D) {
+#pragma unroll 4
+    for (int k = threadIdx.y; k < blocks; k += 8) s += part[((int64_t)k * (W + 1) + i) * D + c];
+  }
+  red[threadIdx.y][threadIdx.x] = s;
+  __syncthreads();
+  if (threadIdx.y != 0 || c >= D) return;
+#pragma unroll
+  for (int k = 1; k < 8; ++k) s += red[k][threadIdx.x];
+  if (i < W) {
+    if (dweight) dweight[(int64_t)c * W + i] = s;
+  } else if (dbias) {
+    dbias[c] = s;
+  }
+}
+
+// ---------------------------------------------------------------- single tokens
+
+struct ConvDecodeParams {
+  const void *x, *weight, *bias;
+  void *state, *y;
+  const int32_t *slots;
+  int *err;
+  int64_t xs, xb, ys, yb;
+  int B, T, D, pool, silu, w_f32;
+};
+
+// grid: x = batch entries, y = channel blocks.  Everything a thread needs is
+// asked for before anything is used: the call is a few microseconds long and
+// bound by that one trip to memory.
+template <typename T, int VEC, int W>
+__global__ void __launch_bounds__(CV_MAX_THREADS) conv_decode_kernel(ConvDecodeParams p) {
+  constexpr int TM = 4;
+  const int c = (blockIdx.y * blockDim.x + threadIdx.x) * VEC;
+  if (c >= p.D) return;
+  const int b = blockIdx.x;
+  if (!bounds_ok(b < p.B, p.err)) return;
+  const T *x = static_cast<const T *>(p.x) + b * p.xb + c;
+  T *y = static_cast<T *>(p.y) + b * p.yb + c;
+  const int slot = p.slots ? p.slots[b] : b;
+  Row<T, VEC> rows[W - 1 + TM];
+#pragma unroll
+  for (int t = 0; t < TM; ++t)
+    if (t < p.T) rows[W - 1 + t].load(x + t * p.xs);
+  float w[W][VEC], bias[VEC];
+  load_weights<VEC, W>(w, bias, p.weight, p.bias, p.w_f32, c);
+  if (slot < 0 || slot >= p.pool) {
+    if (threadIdx.x == 0) record_error(p.err, GDN_ERR_BAD_SLOT);
+    Row<T, VEC> r;
+    r.zero();
+    for (int t = 0; t < p.T; ++t) r.store(y + t * p.ys);
+    return;
+  }
+  T *state = static_cast<T *>(p.state) + (int64_t)slot * (W - 1) * p.D + c;
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) rows[j].load(state + (int64_t)j * p.D);
+#pragma unroll
+  for (int t = 0; t < TM; ++t) {
+    if (t >= p.T) break;
+    float acc[VEC], f[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) acc[e] = bias[e];
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      rows[t + i].widen(f);
+      fma_row<VEC>(acc, w[i], f);
+    }
+    if (p.silu) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) acc[e] = silu(acc[e]);
+    }
+    Row<T, VEC> out;
+    out.round(acc);
+    out.store(y + t * p.ys);
+  }
+#pragma unroll
+  for (int t = 1; t <= TM; ++t) {
+    if (t != p.T) continue;
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) rows[t + j].store(state + (int64_t)j * p.D);
+  }
+}
+
+// ---------------------------------------------------------------- host
+
+// Threads of a block (a multiple of 32) that spread `pieces` evenly over the
+// fewest blocks of at most 256.
+int even_block(int64_t pieces) {
+  const int64_t blocks = (pieces + CV_MAX_THREADS - 1) / CV_MAX_THREADS;
+  const int64_t each = (pieces + blocks - 1) / blocks;
+  return (int)((each + 31) / 32 * 32);
+}
+
+// Whether the rows of tensors with these addresses and strides can be taken in
+// pieces of `vec` elements, each on a boundary of its size.
+bool whole_pieces(int64_t D, int vec, int32_t dtype, std::initializer_list<const void *> tensors,
+                  std::initializer_list<int64_t> strides) {
+  if (D % vec != 0) return false;
+  for (const void *t : tensors)
+    if (!aligned_to(t, vec * dtype_bytes(dtype))) return false;
+  for (int64_t s : strides)
+    if (s % vec != 0) return false;
+  return true;
+}
+
+// Tokens of a run: the longest of 32, 16, 8, 4 that still gives every SM 1024
+// threads.  A run reads W - 1 rows twice (from L2), so long ones move less,
+// but a short call needs its threads.
+int run_tokens(int64_t tokens, int64_t pieces, int longest) {
+  const int64_t want = (int64_t)sm_count() * 1024;
+  int run = longest;
+  while (run > 4 && (tokens + run - 1) / run * pieces < want) run /= 2;
+  return run;
+}
+
+// Calls `f` with the element type and tap count as compile-time values.
+template <typename F>
+cudaError_t with_types(int32_t dtype, int W, F &&f) {
+  auto taps = [&](auto t) {
+    using T = decltype(t);
+    if (W == 2) return f(T(), std::integral_constant<int, 2>());
+    if (W == 3) return f(T(), std::integral_constant<int, 3>());
+    return f(T(), std::integral_constant<int, 4>());
+  };
+  return dtype == GDN_BF16 ? taps(__nv_bfloat16()) : taps(0.f);
+}
+
+gdn_status_t check_conv(int32_t dtype, int32_t w_dtype, int B, int T, int D, int W, int N,
+                        int silu, const void *cu) {
+  CHECK_DTYPE(dtype, "dtype");
+  CHECK_DTYPE(w_dtype, "weight_dtype");
+  CHECK_THAT(w_dtype == GDN_F32 || w_dtype == dtype, GDN_ERR_INVALID_ARG,
+             "weight_dtype must be GDN_F32 or dtype");
+  CHECK_THAT(B >= 1 && T >= 0 && D >= 1 && N >= 1, GDN_ERR_INVALID_ARG,
+             "sizes must be positive (B=%d T=%d D=%d N=%d)", B, T, D, N);
+  CHECK_THAT(W >= 2 && W <= 4, GDN_ERR_UNSUPPORTED, "W must be 2..4 (got %d)", W);
+  CHECK_FLAG(silu, "silu");
+  if (cu == nullptr) {
+    CHECK_THAT(N == B, GDN_ERR_INVALID_ARG, "without cu_seqlens N (%d) must equal B (%d)", N, B);
+  } else {
+    CHECK_THAT(B == 1, GDN_ERR_INVALID_ARG, "with cu_seqlens B must be 1 (got %d)", B);
+    CHECK_OPT_PTR(cu, "cu_seqlens");
+  }
+  // one launch index counts the runs of all batch rows and the sequences
+  CHECK_THAT((int64_t)B * (T / 4 + 1) + N <= 0x7fffffff, GDN_ERR_UNSUPPORTED,
+             "B * T (%lld) is too long for one call", (long long)B * T);
+  CHECK_THAT(D <= 32 * 65535, GDN_ERR_UNSUPPORTED, "D (%d) must be at most %d", D, 32 * 65535);
+  return GDN_OK;
+}
+
+#define CHECK_STRIDE(s, name) \
+  CHECK_THAT((s) >= a->D, GDN_ERR_INVALID_ARG, "%s (%lld) is less than D (%d)", name, (long long)(s), a->D)
+
+// Shape of the gradient's launch: elements of a piece, tokens of a run and
+// blocks along time.
+struct BwdShape {
+  int vec, run, tiles;
+  int64_t blocks;
+};
+BwdShape bwd_shape(const short_conv_bwd_args &a) {
+  BwdShape s;
+  const bool many = a.B > 1;
+  const bool whole = whole_pieces(a.D, 4, a.dtype, {a.dy, a.x, a.dx},
+                                  {a.dy_stride, a.x_stride, a.dx_stride,
+                                   many ? a.dy_batch_stride : 0, many ? a.x_batch_stride : 0,
+                                   many ? a.dx_batch_stride : 0});
+  s.vec = whole ? 4 : 1;
+  s.run = run_tokens((int64_t)a.B * a.T, a.D / s.vec, 64);
+  s.tiles = (a.T + s.run * CB_RUNS - 1) / (s.run * CB_RUNS);
+  s.blocks = (int64_t)a.B * s.tiles;
+  return s;
+}
+
+}  // namespace
+}  // namespace gdn
+
+using namespace gdn;
+
+extern "C" {
+
+gdn_status_t short_conv_fwd(const short_conv_args *a, gdn_stream_t stream) {
+  (void)set_host_error(GDN_OK, "");
+  CHECK_THAT(a != nullptr, GDN_ERR_INVALID_ARG, "args is NULL");
+  gdn_status_t st = check_conv(a->dtype, a->weight_dtype, a->B, a->T, a->D, a->W, a->N, a->silu,
+                               a->cu_seqlens);
+  if (st != GDN_OK) return st;
+  if (a->T > 0) {
+    CHECK_TOKENS(a->x, "x", a->dtype);
+    CHECK_TOKENS(a->y, "y", a->dtype);
+    CHECK_STRIDE(a->x_stride, "x_stride");
+    CHECK_STRIDE(a->y_stride, "y_stride");
+  }
+  CHECK_PTR(a->weight, "weight");
+  CHECK_OPT_PTR(a->bias, "bias");
+  CHECK_OPT_PTR(a->h0, "h0");
+  CHECK_OPT_PTR(a->ht, "ht");
+  ConvParams p{};
+  p.x = a->x; p.weight = a->weight; p.bias = a->bias; p.h0 = a->h0; p.ht = a->ht; p.y = a->y;
+  p.q = {a->cu_seqlens, a->B, a->T, a->N};
+  p.xs = a->x_stride; p.xb = a->B > 1 ? a->x_batch_stride : 0;
+  p.ys = a->y_stride; p.yb = a->B > 1 ? a->y_batch_stride : 0;
+  p.D = a->D; p.silu = a->silu; p.w_f32 = a->weight_dtype == GDN_F32;
+  p.err = device_error_word();
+  if (p.err == nullptr) return launch_status(cudaGetLastError(), "device error word");
+  const int wide = 16 / (int)dtype_bytes(a->dtype);
+  const bool whole = whole_pieces(a->D, wide, a->dtype, {a->x, a->y}, {p.xs, p.xb, p.ys, p.yb});
+  const int vec = whole ? wide : 1;
+  const int64_t pieces = a->D / vec;
+  p.run = run_tokens((int64_t)a->B * a->T, pieces, 32);
+  p.tiles = (a->T + p.run - 1) / p.run;
+  const int block = even_block(pieces);
+  const int64_t gx = (int64_t)a->B * p.tiles + (a->ht ? a->N : 0);
+  if (gx == 0) return GDN_OK;
+  const dim3 grid((unsigned)gx, (unsigned)((pieces + block - 1) / block));
+  return launch_status(
+      with_types(a->dtype, a->W,
+                 [&](auto t, auto w) {
+                   using T = decltype(t);
+                   constexpr int W = decltype(w)::value;
+                   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+                   if (whole)
+                     conv_fwd_kernel<T, 16 / sizeof(T), W><<<grid, block, 0, s>>>(p);
+                   else
+                     conv_fwd_kernel<T, 1, W><<<grid, block, 0, s>>>(p);
+                   return cudaGetLastError();
+                 }),
+      "short convolution launch");
+}
+
+gdn_status_t short_conv_bwd_workspace_size(const short_conv_bwd_args *a, size_t *bytes) {
+  CHECK_THAT(a != nullptr && bytes != nullptr, GDN_ERR_INVALID_ARG, "NULL argument");
+  *bytes = 0;
+  gdn_status_t st = check_conv(a->dtype, a->weight_dtype, a->B, a->T, a->D, a->W, a->N, a->silu,
+                               a->cu_seqlens);
+  if (st != GDN_OK) return st;
+  if (a->dweight || a->dbias)
+    *bytes = (size_t)bwd_shape(*a).blocks * (a->W + 1) * a->D * sizeof(float);
+  return GDN_OK;
+}
+
+gdn_status_t short_conv_bwd(const short_conv_bwd_args *a, gdn_stream_t stream) {
+  (void)set_host_error(GDN_OK, "");
+  CHECK_THAT(a != nullptr, GDN_ERR_INVALID_ARG, "args is NULL");
+  gdn_status_t st = check_conv(a->dtype, a->weight_dtype, a->B, a->T, a->D, a->W, a->N, a->silu,
+                               a->cu_seqlens);
+  if (st != GDN_OK) return st;
+  if (a->T > 0) {
+    CHECK_TOKENS(a->dy, "dy", a->dtype);
+    CHECK_TOKENS(a->x, "x", a->dtype);
+    CHECK_TOKENS(a->dx, "dx", a->dtype);
+    CHECK_STRIDE(a->dy_stride, "dy_stride");
+    CHECK_STRIDE(a->x_stride, "x_stride");
+    CHECK_STRIDE(a->dx_stride, "dx_stride");
+  }
+  CHECK_PTR(a->weight, "weight");
+  CHECK_OPT_PTR(a->bias, "bias");
+  CHECK_OPT_PTR(a->h0, "h0");
+  CHECK_OPT_PTR(a->dht, "dht");
+  CHECK_OPT_PTR(a->dh0, "dh0");
+  CHECK_OPT_PTR(a->dweight, "dweight");
+  CHECK_OPT_PTR(a->dbias, "dbias");
+  const BwdShape shape = bwd_shape(*a);
+  const bool sums = a->dweight || a->dbias;
+  if (sums && shape.blocks > 0) {
+    const size_t need = (size_t)shape.blocks * (a->W + 1) * a->D * sizeof(float);
+    CHECK_THAT(a->workspace != nullptr && a->workspace_bytes >= need, GDN_ERR_WORKSPACE,
+               "workspace of %zu bytes needed (got %zu)", need, a->workspace_bytes);
+    CHECK_OPT_PTR(a->workspace, "workspace");
+  }
+  ConvBwdParams p{};
+  p.dy = a->dy; p.x = a->x; p.weight = a->weight; p.bias = a->bias; p.h0 = a->h0; p.dht = a->dht;
+  p.dx = a->dx; p.dh0 = a->dh0;
+  p.part = sums ? static_cast<float *>(a->workspace) : nullptr;
+  p.q = {a->cu_seqlens, a->B, a->T, a->N};
+  p.gs = a->dy_stride; p.gb = a->B > 1 ? a->dy_batch_stride : 0;
+  p.xs = a->x_stride; p.xb = a->B > 1 ? a->x_batch_stride : 0;
+  p.ds = a->dx_stride; p.db = a->B > 1 ? a->dx_batch_stride : 0;
+  p.D = a->D; p.silu = a->silu; p.w_f32 = a->weight_dtype == GDN_F32;
+  p.run = shape.run; p.tiles = shape.tiles;
+  p.err = device_error_word();
+  if (p.err == nullptr) return launch_status(cudaGetLastError(), "device error word");
+  const int64_t gx = shape.blocks + (a->dh0 ? a->N : 0);
+  const dim3 grid((unsigned)gx, (unsigned)((a->D + 32 * shape.vec - 1) / (32 * shape.vec)));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return launch_status(
+      with_types(a->dtype, a->W,
+                 [&](auto t, auto w) {
+                   using T = decltype(t);
+                   constexpr int W = decltype(w)::value;
+                   const dim3 block(32, CB_RUNS);
+                   if (gx > 0) {
+                     if (shape.vec == 4)
+                       conv_bwd_kernel<T, 4, W><<<grid, block, 0, s>>>(p);
+                     else
+                       conv_bwd_kernel<T, 1, W><<<grid, block, 0, s>>>(p);
+                     const cudaError_t e = cudaGetLastError();
+                     if (e != cudaSuccess) return e;
+                   }
+                   if (sums)
+                     conv_bwd_sum_kernel<W><<<dim3((a->D + 31) / 32, W + 1), dim3(32, 8), 0, s>>>(
+                         p.part, (int)shape.blocks, a->D, a->dweight, a->dbias, p.q, p.err);
+                   return cudaGetLastError();
+                 }),
+      "short convolution gradient launch");
+}
+
+gdn_status_t short_conv_decode(const short_conv_decode_args *a, gdn_stream_t stream) {
+  (void)set_host_error(GDN_OK, "");
+  CHECK_THAT(a != nullptr, GDN_ERR_INVALID_ARG, "args is NULL");
+  CHECK_THAT(a->T >= 1 && a->T <= 4, GDN_ERR_UNSUPPORTED, "T must be 1..4 (got %d)", a->T);
+  gdn_status_t st = check_conv(a->dtype, a->weight_dtype, a->B, a->T, a->D, a->W, a->B, a->silu,
+                               nullptr);
+  if (st != GDN_OK) return st;
+  CHECK_THAT(a->pool >= 1, GDN_ERR_INVALID_ARG, "pool must be positive (got %d)", a->pool);
+  CHECK_THAT(a->slot_indices != nullptr || a->pool >= a->B, GDN_ERR_INVALID_ARG,
+             "identity slots need pool (%d) >= B (%d)", a->pool, a->B);
+  CHECK_TOKENS(a->x, "x", a->dtype);
+  CHECK_TOKENS(a->y, "y", a->dtype);
+  CHECK_STRIDE(a->x_stride, "x_stride");
+  CHECK_STRIDE(a->y_stride, "y_stride");
+  CHECK_PTR(a->weight, "weight");
+  CHECK_OPT_PTR(a->bias, "bias");
+  CHECK_PTR(a->state, "state");
+  CHECK_OPT_PTR(a->slot_indices, "slot_indices");
+  ConvDecodeParams p{};
+  p.x = a->x; p.weight = a->weight; p.bias = a->bias; p.state = a->state; p.y = a->y;
+  p.slots = a->slot_indices;
+  p.xs = a->x_stride; p.xb = a->B > 1 ? a->x_batch_stride : 0;
+  p.ys = a->y_stride; p.yb = a->B > 1 ? a->y_batch_stride : 0;
+  p.B = a->B; p.T = a->T; p.D = a->D; p.pool = a->pool; p.silu = a->silu;
+  p.w_f32 = a->weight_dtype == GDN_F32;
+  p.err = device_error_word();
+  if (p.err == nullptr) return launch_status(cudaGetLastError(), "device error word");
+  const int wide = 16 / (int)dtype_bytes(a->dtype);
+  const bool whole = whole_pieces(a->D, wide, a->dtype, {a->x, a->y}, {p.xs, p.xb, p.ys, p.yb});
+  const int64_t pieces = a->D / (whole ? wide : 1);
+  const int block = even_block(pieces);
+  const dim3 grid((unsigned)a->B, (unsigned)((pieces + block - 1) / block));
+  return launch_status(
+      with_types(a->dtype, a->W,
+                 [&](auto t, auto w) {
+                   using T = decltype(t);
+                   constexpr int W = decltype(w)::value;
+                   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+                   if (whole)
+                     conv_decode_kernel<T, 16 / sizeof(T), W><<<grid, block, 0, s>>>(p);
+                   else
+                     conv_decode_kernel<T, 1, W><<<grid, block, 0, s>>>(p);
+                   return cudaGetLastError();
+                 }),
+      "short convolution token launch");
+}
+
+}  // extern "C"

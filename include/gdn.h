@@ -378,6 +378,189 @@ typedef struct gdn_decode_args {
 gdn_status_t gdn_decode(const gdn_decode_args *args, gdn_stream_t stream);
 
 /*
+ * Short causal depthwise convolution, the operator in front of the recurrences:
+ * every channel d of a sequence is filtered along time with W taps,
+ *     p_t[d] = bias[d] + sum_{i<W} weight[d][i] x_{t-W+1+i}[d],   y = act(p),
+ * where the W - 1 rows before the sequence's first token come from h0 (oldest
+ * first; zeros if NULL) and act is the identity or SiLU, p / (1 + e^-p).
+ *   x, y     [B, T, D]       dtype    token rows x_stride / y_stride elements
+ *                                     apart and batch rows x_batch_stride /
+ *                                     y_batch_stride apart (the channels are
+ *                                     dense), so that x may be a column range
+ *                                     of a wider projection (any element may
+ *                                     be its first); y must not overlap x
+ *   weight   [D, W]          weight_dtype (GDN_F32, or dtype)
+ *   bias     [D]             weight_dtype, NULL = none
+ *   h0, ht   [N, W - 1, D]   dtype    rows before the first token / the last
+ *                                     W - 1 rows (of h0 and x together), NULL =
+ *                                     zeros / not returned; ht must not overlap
+ *                                     h0
+ *   cu_seqlens [N + 1]       int32    as gdn_chunk_fwd; with bad offsets
+ *                                     (GDN_ERR_BAD_SEQLENS) nothing is written
+ * Limits: 2 <= W <= 4.  Sums in float32, one rounding at the end.  A stride
+ * must be at least D.
+ */
+typedef struct short_conv_args {
+  int32_t dtype;               /* gdn_dtype_t of x, y, h0, ht */
+  int32_t weight_dtype;        /* gdn_dtype_t of weight, bias */
+  const void *x;
+  const void *weight, *bias;
+  const void *h0;
+  void *ht;
+  void *y;
+  const int32_t *cu_seqlens;
+  int64_t x_stride, x_batch_stride, y_stride, y_batch_stride;
+  int32_t B, T, D, W, N;
+  int32_t silu;                /* 1: SiLU, 0: identity */
+} short_conv_args;
+
+gdn_status_t short_conv_fwd(const short_conv_args *args, gdn_stream_t stream);
+
+/*
+ * Gradient of short_conv_fwd: with dp_t = dy_t act'(p_t),
+ *     dx_t = sum_i weight[i] dp_{t+W-1-i}   (tokens of the same sequence), plus
+ *            the row of dht that x_t became, if it did,
+ *     dh0  = the same sums at the W - 1 rows before the sequence,
+ *     dweight[i] = sum_t dp_t x_{t-W+1+i},   dbias = sum_t dp_t.
+ *   dy, x    [B, T, D]       dtype    strided as x above
+ *   dx       [B, T, D]       dtype    strided; must not overlap x or dy
+ *   h0, dht, dh0 [N, W-1, D] dtype    NULL = zeros / zeros / not returned
+ *   dweight  [D, W], dbias [D] float32, NULL = not returned
+ * The sums over tokens run in a fixed order (float32 partial sums in
+ * `workspace`, 16-byte aligned, short_conv_bwd_workspace_size() bytes), so
+ * results do not change from run to run.  The rest as short_conv_fwd.
+ */
+typedef struct short_conv_bwd_args {
+  int32_t dtype;               /* gdn_dtype_t of dy, x, dx, h0, dht, dh0 */
+  int32_t weight_dtype;        /* gdn_dtype_t of weight, bias */
+  const void *dy, *x;
+  const void *weight, *bias;
+  const void *h0, *dht;
+  void *dx;
+  float *dweight, *dbias;
+  void *dh0;
+  const int32_t *cu_seqlens;
+  int64_t dy_stride, dy_batch_stride, x_stride, x_batch_stride, dx_stride, dx_batch_stride;
+  int32_t B, T, D, W, N;
+  int32_t silu;
+  void *workspace;
+  size_t workspace_bytes;
+} short_conv_bwd_args;
+
+/* Bytes of workspace short_conv_bwd needs; reads sizes, strides, dtype, the
+ * alignment of dy, x and dx, and whether cu_seqlens, dweight and dbias are NULL. */
+gdn_status_t short_conv_bwd_workspace_size(const short_conv_bwd_args *args, size_t *bytes);
+gdn_status_t short_conv_bwd(const short_conv_bwd_args *args, gdn_stream_t stream);
+
+/*
+ * short_conv_fwd for T = 1..4 new tokens per batch entry against pooled
+ * states, updated in place:
+ *   x, y     [B, T, D]          dtype  strided as above
+ *   state    [pool, W - 1, D]   dtype  the last W - 1 rows of each request,
+ *                                      oldest first
+ *   slot_indices [B]            int32  as gdn_decode (NULL = identity; distinct;
+ *                                      a slot outside [0, pool) records
+ *                                      GDN_ERR_BAD_SLOT and that entry's y is
+ *                                      written as zeros)
+ */
+typedef struct short_conv_decode_args {
+  int32_t dtype;               /* gdn_dtype_t of x, y, state */
+  int32_t weight_dtype;        /* gdn_dtype_t of weight, bias */
+  const void *x;
+  const void *weight, *bias;
+  void *state;
+  const int32_t *slot_indices;
+  void *y;
+  int64_t x_stride, x_batch_stride, y_stride, y_batch_stride;
+  int32_t B, T, D, W, pool;
+  int32_t silu;
+} short_conv_decode_args;
+
+gdn_status_t short_conv_decode(const short_conv_decode_args *args, gdn_stream_t stream);
+
+/*
+ * Selective state space scan over prompts, one scalar decay per token and head
+ * (the recurrence of gdn_chunk_fwd without its delta term, with step sizes, a
+ * skip term and a gate).  Per sequence and head, with the state h [V, K]
+ * starting at h0 (or zeros):
+ *     s_t = softplus(dt_t + dt_bias)   (dt_softplus = 1; else dt_t + dt_bias)
+ *     h_t = e^(-e^A_log s_t) h_{t-1} + s_t x_t Bm_t^T
+ *     y_t = h_t Cm_t + D x_t,   then y_t *= silu(z_t) if z is given
+ * with softplus(v) = log(1 + e^v), v itself above 20.
+ *   x, z, y  [B, T, H, V]   dtype    z NULL = no gate; y float32 when
+ *                                    y_fp32 = 1
+ *   Bm, Cm   [B, T, Hg, K]  dtype    head h reads group h / (H / Hg)
+ *   dt       [B, T, H]      dt_dtype (GDN_F32, or dtype)
+ *   A_log, D, dt_bias [H]   float32  D and dt_bias NULL = zeros
+ *   h0, ht   [N, H, V, K]   float32  NULL = zeros / not returned
+ *   cu_seqlens [N + 1]      int32    as gdn_chunk_fwd; with bad offsets nothing
+ *                                    is written
+ * x, z, Bm, Cm, dt and y have token rows *_stride elements apart and batch rows
+ * *_batch_stride apart; within a row the last two dimensions are dense, so all
+ * of them may be column ranges of wider buffers, starting at any element.
+ * Outputs must not overlap inputs.
+ * Limits: 1 <= K <= 256, H % Hg == 0, N and H at most 65535.
+ * Segments: a sequence longer than `segment_tokens` (a multiple of 128; 0 = the
+ * library's choice, whole sequences when their number fills the GPU) is cut
+ * into segments of that many tokens that are processed at once: first each
+ * one's last state from zero, then each from its start state.
+ * Workspace: ssm_chunk_workspace_size() bytes (0 when no sequence is cut),
+ * device memory, 256-byte aligned.
+ */
+typedef struct ssm_chunk_args {
+  int32_t dtype;               /* gdn_dtype_t of x, z, Bm, Cm, y */
+  int32_t dt_dtype;            /* gdn_dtype_t of dt */
+  const void *x, *z, *Bm, *Cm, *dt;
+  const float *A_log, *D, *dt_bias;
+  const float *h0;
+  float *ht;
+  void *y;
+  const int32_t *cu_seqlens;
+  int64_t x_stride, x_batch_stride, z_stride, z_batch_stride;
+  int64_t Bm_stride, Bm_batch_stride, Cm_stride, Cm_batch_stride;
+  int64_t dt_stride, dt_batch_stride, y_stride, y_batch_stride;
+  int32_t B, T, H, Hg, K, V, N;
+  int32_t dt_softplus;
+  int32_t y_fp32;              /* 1: y is float32 whatever dtype is; 0: y has dtype */
+  int32_t segment_tokens;      /* longest run of tokens taken in sequence; 0 = choose */
+  void *workspace;
+  size_t workspace_bytes;
+} ssm_chunk_args;
+
+/* Bytes of workspace ssm_chunk_fwd needs; reads sizes, strides, dtype,
+ * segment_tokens, pointers' alignment and whether cu_seqlens is NULL. */
+gdn_status_t ssm_chunk_workspace_size(const ssm_chunk_args *args, size_t *bytes);
+gdn_status_t ssm_chunk_fwd(const ssm_chunk_args *args, gdn_stream_t stream);
+
+/*
+ * The scan for T = 1..4 new tokens per batch entry against pooled states,
+ * updated in place (float32 arithmetic, one rounding when state_dtype is
+ * GDN_BF16):
+ *   x, z, y  [B, T, H, V], Bm, Cm [B, T, Hg, K], dt [B, T, H]  as above
+ *   state    [pool, H, V, K]   state_dtype   K fastest
+ *   slot_indices [B]           int32         as gdn_decode
+ * Limits: 8 <= K <= 256, K % 8 == 0, H % Hg == 0.
+ */
+typedef struct ssm_decode_args {
+  int32_t dtype;               /* gdn_dtype_t of x, z, Bm, Cm, y */
+  int32_t dt_dtype;            /* gdn_dtype_t of dt */
+  int32_t state_dtype;         /* gdn_dtype_t of state */
+  const void *x, *z, *Bm, *Cm, *dt;
+  const float *A_log, *D, *dt_bias;
+  void *state;
+  const int32_t *slot_indices;
+  void *y;
+  int64_t x_stride, x_batch_stride, z_stride, z_batch_stride;
+  int64_t Bm_stride, Bm_batch_stride, Cm_stride, Cm_batch_stride;
+  int64_t dt_stride, dt_batch_stride, y_stride, y_batch_stride;
+  int32_t B, T, H, Hg, K, V, pool;
+  int32_t dt_softplus;
+  int32_t y_fp32;
+} ssm_decode_args;
+
+gdn_status_t ssm_decode(const ssm_decode_args *args, gdn_stream_t stream);
+
+/*
  * GDN chunked forward without a workspace, for callers that cannot allocate
  * device memory (a host runtime that owns a fixed device-memory budget and
  * forbids cudaMalloc from plugins, or a latency-critical loop that must not
