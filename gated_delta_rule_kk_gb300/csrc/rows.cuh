@@ -88,8 +88,42 @@ __device__ __forceinline__ void fma_row(float *acc, const float *a, const float 
   }
 }
 
+// out = a op b, pairs of lanes an instruction
+#define GDN_ROW_OP(name, op)                                                           \
+  template <int VEC>                                                                   \
+  __device__ __forceinline__ void name(float *out, const float *a, const float *b) {   \
+    static_assert(VEC % 2 == 0, "pairs");                                              \
+    _Pragma("unroll") for (int i = 0; i < VEC; i += 2)                                 \
+        asm("{\n\t.reg .b64 ra, rb;\n\t"                                               \
+            "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t" op                    \
+            ".rn.f32x2 ra, ra, rb;\n\tmov.b64 {%0, %1}, ra;\n\t}"                      \
+            : "=f"(out[i]), "=f"(out[i + 1])                                           \
+            : "f"(a[i]), "f"(a[i + 1]), "f"(b[i]), "f"(b[i + 1]));                     \
+  }
+GDN_ROW_OP(mul_row, "mul")
+GDN_ROW_OP(add_row, "add")
+GDN_ROW_OP(sub_row, "sub")
+#undef GDN_ROW_OP
+
 // p / (1 + e^-p); e^-p overflows to infinity below -88 and the quotient is 0
 __device__ __forceinline__ float silu(float p) { return __fdividef(p, 1.f + __expf(-p)); }
+
+// silu of VEC values
+template <int VEC>
+__device__ __forceinline__ void silu_row(float *out, const float *z) {
+  const float k[2] = {-1.442695041f, -1.442695041f}, one[2] = {1.f, 1.f};
+#pragma unroll
+  for (int i = 0; i < VEC; i += 2) {
+    float e[2];
+    mul_row<2>(e, z + i, k);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e[j]));
+    add_row<2>(e, e, one);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e[j]));
+    mul_row<2>(out + i, z + i, e);
+  }
+}
 
 // log(1 + e^v), v itself above 20
 __device__ __forceinline__ float softplus(float v) { return v > 20.f ? v : log1pf(expf(v)); }

@@ -322,12 +322,14 @@ gdn_status_t check_chunk_args(const ssm_chunk_args &a) {
   return GDN_OK;
 }
 
-// Segment length when the caller leaves it open: as long as still gives every
-// SM four blocks of the kernel, but at most 64 to a sequence (each block reads
-// the states of the segments before its own).  Cutting costs a second pass over
-// x, B and dt, so sequences stay whole when they fill the GPU by themselves.
-int choose_segment(const SsmParams &p) {
-  const int64_t chains = (int64_t)p.H * ((p.V + 31) / 32), want = 4 * (int64_t)sm_count();
+// Segment length when the caller leaves it open.  Cutting costs a second pass
+// over x, B and dt and a block reads the states of the segments before its own,
+// so sequences stay whole when they give half the blocks the GPU holds; else
+// segments are as long as still fills it, at most 64 to a sequence.
+int choose_segment(const SsmParams &p, bool tc) {
+  const int cols = tc ? 64 : 32;  // of a block's state tile; one block an SM, or four
+  const int64_t chains = (int64_t)p.H * ((p.V + cols - 1) / cols);
+  const int64_t want = (tc ? 1 : 4) * (int64_t)sm_count();
   if (p.cu == nullptr && chains * p.N >= want / 2) return SSM_WHOLE;
   const int64_t tokens = p.cu ? p.T : (int64_t)p.T * p.N;
   int64_t seg = tokens * chains / want;
@@ -341,7 +343,8 @@ SsmParams chunk_params(const ssm_chunk_args &a) {
   set_tokens(p, a);
   p.N = a.N;
   p.h0 = a.h0; p.ht = a.ht; p.cu = a.cu_seqlens;
-  p.seg = a.segment_tokens > 0 ? a.segment_tokens : choose_segment(p);
+  p.seg = a.segment_tokens > 0 ? a.segment_tokens
+                               : choose_segment(p, ssm_tc_supported(p, a.dtype == GDN_BF16));
   const int64_t longest = a.T;  // no sequence has more tokens
   const int64_t per = longest > p.seg ? (longest + p.seg - 1) / p.seg : 1;
   p.items = (int)(a.cu_seqlens ? (a.N + (longest > p.seg ? longest / p.seg : 0)) : a.N * per);
@@ -389,7 +392,9 @@ gdn_status_t ssm_chunk_fwd(const ssm_chunk_args *a, gdn_stream_t stream) {
   p.err = device_error_word();
   if (p.err == nullptr) return launch_status(cudaGetLastError(), "device error word");
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return launch_status(launch_ssm_simt(p, a->dtype == GDN_BF16, s), "scan launch");
+  const bool bf16 = a->dtype == GDN_BF16;
+  return launch_status(ssm_tc_supported(p, bf16) ? launch_ssm_tc(p, s) : launch_ssm_simt(p, bf16, s),
+                       "scan launch");
 }
 
 gdn_status_t ssm_decode(const ssm_decode_args *a, gdn_stream_t stream) {

@@ -30,6 +30,9 @@ struct SsmParams {
   float *seg_state, *seg_decay;
 };
 
+// The scan on the tensor cores: whether it serves p, and its launch.
+bool ssm_tc_supported(const SsmParams &p, bool bf16);
+cudaError_t launch_ssm_tc(const SsmParams &p, cudaStream_t stream);
 // The scan in float32 on the CUDA cores: any type and size.
 cudaError_t launch_ssm_simt(const SsmParams &p, bool bf16, cudaStream_t stream);
 

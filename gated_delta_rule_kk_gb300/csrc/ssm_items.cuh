@@ -62,13 +62,20 @@ __device__ __forceinline__ SsmItem ssm_item(const SsmParams &p, int item) {
   return r;
 }
 
-// Step size of a token and head from dt and its bias.
+// dt at element `at`, and the step size from dt with its bias.
+template <typename Params>
+__device__ __forceinline__ float ssm_dt(const Params &p, int64_t at) {
+  return p.dt_f32 ? static_cast<const float *>(p.dt)[at]
+                  : to_f32(static_cast<const __nv_bfloat16 *>(p.dt)[at]);
+}
+template <typename Params>
+__device__ __forceinline__ float ssm_softplus(const Params &p, float v) {
+  return p.softplus ? softplus(v) : v;
+}
+// Step size of a token and head.
 template <typename Params>
 __device__ __forceinline__ float ssm_step(const Params &p, int64_t row, int h, float bias) {
-  const float v = (p.dt_f32 ? static_cast<const float *>(p.dt)[row + h]
-                            : to_f32(static_cast<const __nv_bfloat16 *>(p.dt)[row + h])) +
-                  bias;
-  return p.softplus ? softplus(v) : v;
+  return ssm_softplus(p, ssm_dt(p, row + h) + bias);
 }
 
 }  // namespace gdn

@@ -219,6 +219,7 @@ def test_scan_in_segments(dtype, lens):
     i = ssm_inputs(5, 1, 1000, 2, 1, 64, 128, dtype, lens)
     check_scan(i, segment_tokens=128)
     check_scan(i, segment_tokens=384)
+    check_scan(i, segment_tokens=1024)
 
 
 def test_scan_step_sizes_as_given_and_in_float32():
