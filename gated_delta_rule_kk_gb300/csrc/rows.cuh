@@ -88,6 +88,20 @@ __device__ __forceinline__ void fma_row(float *acc, const float *a, const float 
   }
 }
 
+// out = a * b + c
+template <int VEC>
+__device__ __forceinline__ void fma_rows(float *out, const float *a, const float *b,
+                                         const float *c) {
+  static_assert(VEC % 2 == 0, "pairs");
+#pragma unroll
+  for (int i = 0; i < VEC; i += 2)
+    asm("{\n\t.reg .b64 ra, rb, rc;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+        "fma.rn.f32x2 rc, ra, rb, rc;\n\tmov.b64 {%0, %1}, rc;\n\t}"
+        : "=f"(out[i]), "=f"(out[i + 1])
+        : "f"(a[i]), "f"(a[i + 1]), "f"(b[i]), "f"(b[i + 1]), "f"(c[i]), "f"(c[i + 1]));
+}
+
 // out = a op b, pairs of lanes an instruction
 #define GDN_ROW_OP(name, op)                                                           \
   template <int VEC>                                                                   \
@@ -108,9 +122,9 @@ GDN_ROW_OP(sub_row, "sub")
 // p / (1 + e^-p); e^-p overflows to infinity below -88 and the quotient is 0
 __device__ __forceinline__ float silu(float p) { return __fdividef(p, 1.f + __expf(-p)); }
 
-// silu of VEC values
+// 1 / (1 + e^-z) of VEC values, and silu
 template <int VEC>
-__device__ __forceinline__ void silu_row(float *out, const float *z) {
+__device__ __forceinline__ void sigmoid_row(float *out, const float *z) {
   const float k[2] = {-1.442695041f, -1.442695041f}, one[2] = {1.f, 1.f};
 #pragma unroll
   for (int i = 0; i < VEC; i += 2) {
@@ -120,9 +134,14 @@ __device__ __forceinline__ void silu_row(float *out, const float *z) {
     for (int j = 0; j < 2; ++j) asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e[j]));
     add_row<2>(e, e, one);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e[j]));
-    mul_row<2>(out + i, z + i, e);
+    for (int j = 0; j < 2; ++j) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(out[i + j]) : "f"(e[j]));
   }
+}
+template <int VEC>
+__device__ __forceinline__ void silu_row(float *out, const float *z) {
+  float s[VEC];
+  sigmoid_row<VEC>(s, z);
+  mul_row<VEC>(out, z, s);
 }
 
 // log(1 + e^v), v itself above 20

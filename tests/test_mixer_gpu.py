@@ -71,6 +71,42 @@ def test_conv(B, T, D, W, dtype, lens, gap, silu, bias, state):
         assert_each_close(dh0, rh, "dh0", CONV_TOL)
 
 
+# long enough for the ring of tiles: runs that end inside a sequence and at its
+# end, sequences shorter than the taps, channels that end inside a box
+@pytest.mark.parametrize("B,T,D,W,dtype,lens,gap,silu", [
+    (1, 3001, 4100, 4, BF16, [1000, 0, 1, 2, 3, 1995], 36, True),
+    (2, 1601, 4104, 3, BF16, None, 0, False),
+    (1, 5003, 1156, 4, F32, [7, 4000, 2, 994], 0, True),
+    (1, 14000, 520, 2, BF16, None, 8, True),
+    # the last token(s) on a run of their own, or just before a run's end
+    (1, 3000, 1160, 4, F32, [500, 2500], 0, True),
+    (1, 3001, 1160, 4, F32, [500, 2501], 0, True),
+    (1, 3002, 1160, 4, F32, [500, 2502], 0, True),
+    (1, 3003, 1160, 3, F32, [500, 2503], 0, True),
+    (1, 3001, 1160, 2, F32, [2999, 2], 0, False),
+])
+def test_conv_of_long_prompts(B, T, D, W, dtype, lens, gap, silu):
+    i = conv_inputs(T, B, T, D, W, dtype, True, lens, True, gap)
+    d = cuda(i)
+    act = "silu" if silu else None
+    y, ht = gdn.short_conv_fwd(d["x"], d["weight"], bias=d["bias"], initial_state=d["h0"],
+                               cu_seqlens=d["cu"], activation=act)
+    ok()
+    ry, rht = M.short_conv(i["x"], i["weight"], i["bias"], i["h0"], i["cu"], silu)
+    assert_each_close(y, ry, "y", CONV_TOL)
+    assert_each_close(ht, rht, "ht", CONV_TOL)
+    out = gdn.short_conv_bwd(d["dy"], d["x"], d["weight"], bias=d["bias"], initial_state=d["h0"],
+                             dfinal_state=d["dht"], cu_seqlens=d["cu"], activation=act)
+    ok()
+    ref = M.short_conv_grad(i["dy"], i["x"], i["weight"], i["bias"], i["h0"], i["dht"], i["cu"], silu)
+    for got, want, name in zip(out, ref, ("dx", "dw", "db", "dh0")):
+        assert_each_close(got, want, name, CONV_TOL)
+    again = gdn.short_conv_bwd(d["dy"], d["x"], d["weight"], bias=d["bias"],
+                               initial_state=d["h0"], dfinal_state=d["dht"], cu_seqlens=d["cu"],
+                               activation=act)
+    assert all(torch.equal(a, b) for a, b in zip(out, again))
+
+
 def test_conv_float32_weights_beside_bfloat16_rows():
     i = conv_inputs(5, 2, 50, 24, 4, BF16)
     i["weight"], i["bias"] = i["weight"].float() * 1.001, i["bias"].float() * 1.001
@@ -276,6 +312,34 @@ def test_scan_tokens(T, dtype, sdtype, H, Hg, V, K):
     assert_each_close(state[slots.long().cuda()], rht, "state", 1e-5)
     others = torch.tensor([1, 2])
     assert torch.equal(state[others.cuda()].cpu(), pool[others])
+
+
+@pytest.mark.parametrize("T,dtype,sdtype,B,H,V,K", [
+    (1, BF16, BF16, 70, 32, 64, 128), (3, BF16, F32, 70, 16, 100, 64), (2, F32, F32, 40, 13, 80, 136),
+    (4, BF16, BF16, 100, 31, 33, 248)])
+def test_scan_tokens_of_many_requests(T, dtype, sdtype, B, H, V, K):
+    """Enough states to stream through the ring: checked on some requests, two
+    of them with bad slots."""
+    i = ssm_inputs(T + K, B, T, H, 1, V, K, dtype, h0=False)
+    slots = torch.randperm(B + 20)[:B].to(torch.int32)
+    slots[3], slots[B - 1] = -1, B + 20
+    d = cuda(i)
+    state = torch.randn(B + 20, H, V, K, device="cuda").to(sdtype)
+    before = state.clone()
+    y = gdn.ssm_decode(d["x"], d["dt"], d["A_log"], d["Bm"], d["Cm"], state, D=d["D"], z=d["z"],
+                       dt_bias=d["dt_bias"], slot_indices=slots.cuda(), out_dtype=F32)
+    assert gdn.gdn_check_device_error() == Status.BAD_SLOT
+    assert not y[3].any() and not y[B - 1].any()
+    some = [0, 1, 2, 4, B // 2, B - 3, B - 2]
+    at = slots[some].long()
+    sub = {k: v[some] if k in ("x", "dt", "Bm", "Cm", "z") else v for k, v in i.items()}
+    ry, rht = M.ssm_scan(sub["x"], sub["dt"], sub["A_log"], sub["Bm"], sub["Cm"], sub["D"], sub["z"],
+                         sub["dt_bias"], h0=before[at.cuda()])
+    assert_close(y[some], ry, TOL_F32, "y")
+    assert_each_close(state[at.cuda()], rht, "state", 1e-5)
+    rest = torch.ones(B + 20, dtype=torch.bool)
+    rest[slots[(slots >= 0) & (slots < B + 20)].long()] = False
+    assert torch.equal(state[rest.cuda()], before[rest.cuda()])
 
 
 def test_tokens_continue_prompts():
