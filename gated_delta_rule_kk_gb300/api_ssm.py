@@ -118,7 +118,7 @@ def _activation(activation):
 
 
 def _call(name, args, stream, device):
-    lib = _lib.load()
+    lib = _lib._lib or _lib.load()
     st = getattr(lib, name)(ctypes.byref(args), _stream_handle(stream, device))
     if st:
         _lib.check(st, name)
@@ -201,7 +201,7 @@ def _workspace(args, size_fn, workspace, device, stream):
     caching allocator, which keeps it valid for the work enqueued on its stream,
     unless the caller passes one)."""
     n = ctypes.c_size_t(0)
-    st = getattr(_lib.load(), size_fn)(ctypes.byref(args), ctypes.byref(n))
+    st = getattr(_lib._lib or _lib.load(), size_fn)(ctypes.byref(args), ctypes.byref(n))
     if st:
         _lib.check(st, size_fn)
     if n.value == 0:

@@ -6,6 +6,8 @@
 #include <stdint.h>
 #include <stdio.h>
 
+#include <atomic>
+
 #include "gdn_internal.h"
 
 namespace gdn {
@@ -33,14 +35,22 @@ inline gdn_status_t launch_status(cudaError_t e, const char *what) {
 
 inline size_t dtype_bytes(int32_t dtype) { return dtype == GDN_BF16 ? 2 : 4; }
 
-// SMs of the current device (a GB300's count if it cannot be read).
+// SMs of the current device, read once for each (a GB300's count if it cannot
+// be read).
 inline int sm_count() {
+  static std::atomic<int> known[64];
   int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
     (void)cudaGetLastError();
     return 152;
   }
+  n = known[dev].load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
+    (void)cudaGetLastError();
+    return 152;
+  }
+  known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 

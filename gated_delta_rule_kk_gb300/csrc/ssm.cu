@@ -800,8 +800,9 @@ int choose_segment(const SsmParams &p, bool tc) {
   const int64_t tokens = p.cu ? p.T : (int64_t)p.T * p.N;
   int64_t seg = tokens * chains / want;
   if (seg < p.T / 64) seg = p.T / 64;
-  seg = (seg + SSM_UNIT - 1) / SSM_UNIT * SSM_UNIT;
-  return seg < SSM_UNIT ? SSM_UNIT : seg < p.T ? (int)seg : SSM_WHOLE;
+  const int64_t unit = tc ? SSM_UNIT : SSM_UNIT / 2;
+  seg = std::max(unit, (seg + unit - 1) / unit * unit);
+  return seg < p.T ? (int)seg : SSM_WHOLE;
 }
 
 SsmParams chunk_params(const ssm_chunk_args &a) {

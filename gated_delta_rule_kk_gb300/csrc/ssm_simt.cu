@@ -89,10 +89,13 @@ __global__ void __launch_bounds__(SS_THREADS) ssm_simt_kernel(SsmParams p) {
     (&sm.B[0][0])[i] = 0.f;
     (&sm.C[0][0])[i] = 0.f;
   }
+  for (int i = tid; i < SS_TB * SS_ROWS; i += SS_THREADS) (&sm.x[0][0])[i] = 0.f;
   float total = 0.f;
   for (int t0 = q.lo; t0 < q.hi; t0 += SS_TB) {
     const int n = min(SS_TB, q.hi - t0);
     __syncthreads();
+    // rows past the last token, up to a whole four, are left as they are: finite,
+    // and taken with factors of zero
     for (int i = warp; i < n; i += 4) {
       const T *bt = static_cast<const T *>(p.Bm) + bat + (int64_t)(t0 + i) * p.bs;
       const T *ct = static_cast<const T *>(p.Cm) + cat + (int64_t)(t0 + i) * p.cs;
@@ -126,46 +129,61 @@ __global__ void __launch_bounds__(SS_THREADS) ssm_simt_kernel(SsmParams p) {
     }
     __syncthreads();
     total += sm.total;
+    // Four tokens at a time: their eight partial outputs (of two rows) are summed
+    // over the row's eight lanes together, halving values and lanes at each step,
+    // and lane kl ends with token kl / 2's row kl % 2.  Tokens past the block's
+    // last have factors of zero and a decay of one.
     auto tokens = [&](auto scaled) {
-      for (int i = 0; i < n; ++i) {
-        float acc[2][4] = {}, in[2];
-        const float d = sm.decay[i];
-        const float dd[4] = {d, d, d, d};
+#pragma unroll 1
+      for (int i = 0; i < n; i += 4) {
+        float sum[8];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) in[r] = sm.in[i] * sm.x[i][r0 + 16 * r];
+        for (int t = 0; t < 4; ++t) {
+          float acc[2][4] = {}, in[2];
+          const float d = sm.decay[i + t];
+          const float dd[4] = {d, d, d, d};
 #pragma unroll
-        for (int j = 0; j < KJ; ++j) {
-          const float4 b4 = *reinterpret_cast<const float4 *>(&sm.B[i][32 * j + 4 * kl]);
-          const float bv[4] = {b4.x, b4.y, b4.z, b4.w};
-          float cv[4];
-          if (!STATES) {
-            const float4 c4 = *reinterpret_cast<const float4 *>(&sm.C[i][32 * j + 4 * kl]);
-            cv[0] = c4.x; cv[1] = c4.y; cv[2] = c4.z; cv[3] = c4.w;
-          }
+          for (int r = 0; r < 2; ++r) in[r] = sm.in[i + t] * sm.x[i + t][r0 + 16 * r];
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            float *h4 = &s[r][4 * j];
-            if constexpr (decltype(scaled)::value) {
-              const float ii[4] = {in[r], in[r], in[r], in[r]};
-              fma_row<4>(h4, ii, bv);
-            } else {
-              float add[4] = {in[r] * bv[0], in[r] * bv[1], in[r] * bv[2], in[r] * bv[3]};
-              fma_row<4>(add, dd, h4);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) h4[e] = add[e];
+          for (int j = 0; j < KJ; ++j) {
+            const float4 b4 = *reinterpret_cast<const float4 *>(&sm.B[i + t][32 * j + 4 * kl]);
+            const float bv[4] = {b4.x, b4.y, b4.z, b4.w};
+            float cv[4];
+            if (!STATES) {
+              const float4 c4 = *reinterpret_cast<const float4 *>(&sm.C[i + t][32 * j + 4 * kl]);
+              cv[0] = c4.x; cv[1] = c4.y; cv[2] = c4.z; cv[3] = c4.w;
             }
-            if (!STATES) fma_row<4>(acc[r], h4, cv);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              float *h4 = &s[r][4 * j];
+              if constexpr (decltype(scaled)::value) {
+                const float ii[4] = {in[r], in[r], in[r], in[r]};
+                fma_row<4>(h4, ii, bv);
+              } else {
+                float add[4] = {in[r] * bv[0], in[r] * bv[1], in[r] * bv[2], in[r] * bv[3]};
+                fma_row<4>(add, dd, h4);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) h4[e] = add[e];
+              }
+              if (!STATES) fma_row<4>(acc[r], h4, cv);
+            }
           }
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            sum[2 * t + r] = (acc[r][0] + acc[r][1]) + (acc[r][2] + acc[r][3]);
         }
         if (!STATES) {
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            float v = (acc[r][0] + acc[r][1]) + (acc[r][2] + acc[r][3]);
-            v += __shfl_xor_sync(~0u, v, 1);
-            v += __shfl_xor_sync(~0u, v, 2);
-            v += __shfl_xor_sync(~0u, v, 4);
-            if (kl == 0) sm.y[i][r0 + 16 * r] = sm.out[i] * v;
+          for (int m = 4, o = 4; o > 0; m /= 2, o /= 2) {
+            const bool up = kl & o;
+#pragma unroll
+            for (int j = 0; j < m; ++j) {
+              const float send = up ? sum[j] : sum[j + m], keep = up ? sum[j + m] : sum[j];
+              sum[j] = keep + __shfl_xor_sync(~0u, send, o);
+            }
           }
+          const int t = i + kl / 2;
+          sm.y[t][r0 + 16 * (kl & 1)] = sm.out[t] * sum[0];
         }
       }
     };

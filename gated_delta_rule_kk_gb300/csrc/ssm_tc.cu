@@ -53,10 +53,10 @@ constexpr int ST_Q = 128, ST_VT = 64;
 constexpr int ST_W_OUT = 8, ST_W_STATE = 16, ST_W_W = 24, ST_W_LOAD = 28, ST_W_MMA = 29,
               ST_W_SCALARS = 30, ST_THREADS = 32 * 32;
 // Registers of a thread of each role.  The block starts with 64 a thread, and
-// 64 + 64 + 64 + 64 + 72 + 72 + 48 + 56, the warpgroups' shares, is what 8
+// 64 + 64 + 56 + 56 + 80 + 80 + 48 + 56, the warpgroups' shares, is what 8
 // warpgroups have at 64: no role spills.
-constexpr int ST_R_STATE = 72, ST_R_W = 48, ST_R_REST = 56;
-static_assert(4 * 64 + 2 * ST_R_STATE + ST_R_W + ST_R_REST <= 8 * 64, "registers");
+constexpr int ST_R_OUT = 56, ST_R_STATE = 80, ST_R_W = 48, ST_R_REST = 56;
+static_assert(2 * 64 + 2 * ST_R_OUT + 2 * ST_R_STATE + ST_R_W + ST_R_REST <= 8 * 64, "registers");
 constexpr uint32_t ST_TILE = 16384;  // 128 rows of 128 bytes, 128-byte swizzle
 // TMEM columns: two of S, then M over it (16 columns of S hold 8 of M's high and
 // 8 of its low pieces, bf16 pairs); C h^T; y; B^T W, the first piece and the sum
@@ -383,6 +383,7 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
     }
   } else if (warp < ST_W_STATE) {
     // ---------------- output
+    regs_down<ST_R_OUT>();
     const int i = 32 * (warp & 3) + lane, c0 = 32 * ((warp - ST_W_OUT) >> 2);
     unsigned char *zt = sm + L::Z;
 #pragma unroll 1
@@ -394,27 +395,25 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
       wait(&bar.y_full, it);
       ptx::tc_fence_after();
 #pragma unroll 1
-      for (int c = c0; c < c0 + 32; c += 16) {
-        uint32_t acc[16];
-        tmem_ld16_async(tmem + ST_Y + c + lanes, acc);
-        float y[16];
+      for (int c = c0; c < c0 + 32; c += 8) {
+        uint32_t acc[8];
+        tmem_ld8_async(tmem + ST_Y + c + lanes, acc);
+        unsigned char *piece = zt + swz(i, c / 8);
+        float y[8];
         if (p.z) {
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            Row<__nv_bfloat16, 8> zr;
-            zr.load(reinterpret_cast<const __nv_bfloat16 *>(zt + swz(i, c / 8 + k)));
-            zr.widen(y + 8 * k);
-          }
-          silu_row<16>(y, y);
+          Row<__nv_bfloat16, 8> zr;
+          zr.load(reinterpret_cast<const __nv_bfloat16 *>(piece));
+          zr.widen(y);
+          silu_row<8>(y, y);
         }
         tmem_wait_ld();
-        pin_regs<16>(acc);
-        if (c > c0) {
+        pin_regs<8>(acc);
+        if (c == c0 + 24) {
           ptx::tc_fence_before();
           arrive(&bar.y_read);
         }
 #pragma unroll
-        for (int j = 0; j < 16; j += 2) {
+        for (int j = 0; j < 8; j += 2) {
           const float x[2] = {__uint_as_float(acc[j]), __uint_as_float(acc[j + 1])};
           if (p.z) {
             mul_row<2>(y + j, y + j, x);
@@ -423,23 +422,19 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
             y[j + 1] = x[1];
           }
         }
+        Row<__nv_bfloat16, 8> out;
+        out.round(y);
+        if (whole) {
+          out.store(reinterpret_cast<__nv_bfloat16 *>(piece));
+        } else if (i < n && c < width) {
+          const int64_t at = q.b * p.yb + (q.lo + it * ST_Q + i) * p.ys + (int64_t)h * V + v0 + c;
+          if (!p.y_f32) {
+            out.store(static_cast<__nv_bfloat16 *>(p.y) + at);
+          } else {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          Row<__nv_bfloat16, 8> out;
-          out.round(y + 8 * k);
-          if (whole) {
-            out.store(reinterpret_cast<__nv_bfloat16 *>(zt + swz(i, c / 8 + k)));
-          } else if (i < n && c + 8 * k < width) {
-            const int64_t at = q.b * p.yb + (q.lo + it * ST_Q + i) * p.ys + (int64_t)h * V + v0 +
-                               c + 8 * k;
-            if (!p.y_f32) {
-              out.store(static_cast<__nv_bfloat16 *>(p.y) + at);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 8; j += 4)
-                *reinterpret_cast<float4 *>(static_cast<float *>(p.y) + at + j) =
-                    make_float4(y[8 * k + j], y[8 * k + j + 1], y[8 * k + j + 2], y[8 * k + j + 3]);
-            }
+            for (int j = 0; j < 8; j += 4)
+              *reinterpret_cast<float4 *>(static_cast<float *>(p.y) + at + j) =
+                  make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
           }
         }
       }
