@@ -7,11 +7,16 @@ output's own rounding.  Its weight gradients sum up to 2000 products, in
 float32 partial sums: 1e-5 RMS as well.  Scan: the library's bounds, 1e-4 RMS
 in float32 and for float32 states, 2e-2 RMS for bfloat16 inputs.
 """
+import importlib.util
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
 import gated_delta_rule_kk_gb300 as gdn
-from gated_delta_rule_kk_gb300 import GdnError, Status
+from gated_delta_rule_kk_gb300 import GdnError, Status, build_lib
 from oracle import mixer as M
 
 from _mixer import assert_each_close, conv_inputs, cuda, ssm_inputs
@@ -370,6 +375,141 @@ def test_tokens_continue_prompts():
                                   z=d["z"][:, lo:hi], **kw))
     ok()
     assert_close(torch.cat(got, 1), whole.cpu().double().numpy(), TOL_BF16, "y")
+
+
+def test_offsets_past_32_bits():
+    """The last rows of buffers of more than 2^31 elements."""
+    T, D = 263000, 8192
+    x = torch.zeros((1, T, D), dtype=BF16, device="cuda")
+    i = conv_inputs(21, 1, 300, D, 4, BF16, state=False)
+    c = cuda(i)
+    x[:, -300:] = c["x"]
+    y, ht = gdn.short_conv_fwd(x, c["weight"], c["bias"])
+    y_ref, _ = M.short_conv(i["x"], i["weight"], i["bias"])
+    assert_each_close(y[:, -300:], y_ref, "y", CONV_TOL)
+    assert torch.equal(ht, c["x"][:, -3:])
+    dx = gdn.short_conv_bwd(x, x, c["weight"], c["bias"])[0]
+    dx_ref = M.short_conv_grad(i["x"], i["x"], i["weight"], i["bias"])[0]
+    assert_each_close(dx[:, -300:], dx_ref, "dx", CONV_TOL)
+    ok()
+    del x, y, dx
+
+    H, V, K, slots = 64, 64, 128, 4200
+    d = cuda(ssm_inputs(22, 2, 1, H, 1, V, K, BF16))
+    pool = torch.zeros((slots, H, V, K), dtype=BF16, device="cuda")
+    at = torch.tensor([slots - 1, 3], dtype=torch.int32, device="cuda")
+    pool[at.long()] = d["h0"].to(BF16)
+    state = d["h0"].to(BF16)
+    args = (d["x"], d["dt"], d["A_log"], d["Bm"], d["Cm"])
+    y = gdn.ssm_decode(*args, pool, slot_indices=at)
+    want = gdn.ssm_decode(*args, state)
+    assert torch.equal(y, want) and torch.equal(pool[at.long()], state)
+    ok()
+
+
+@pytest.mark.parametrize("dtype,H,V,T", [(BF16, 512, 64, 66000), (F32, 16, 64, 2400)])
+def test_scan_over_wide_buffers(dtype, H, V, T):
+    """x, z and y of more than 2^31 elements (or of more than 2^31 bytes between two
+    rows of a batch): the last tokens as a prompt of their own from the state before."""
+    d = cuda(ssm_inputs(23, 1, 300, H, 1, V, 128, dtype))
+    if dtype is F32:
+        base = torch.zeros((2, 2 ** 29 + 64), dtype=dtype, device="cuda")
+        x = base.as_strided((2, T, H, V), (base.stride(0), H * V, V, 1))
+        rep = 2
+    else:
+        x, rep = torch.zeros((1, T, H, V), dtype=dtype, device="cuda"), 1
+    x[:, -300:] = d["x"]
+
+    def grown(t):
+        out = torch.zeros((rep, T, *t.shape[2:]), dtype=dtype, device="cuda")
+        out[:, -300:] = t
+        return out
+
+    kw = dict(A_log=d["A_log"], D=d["D"], dt_bias=d["dt_bias"], out_dtype=F32)
+    y, ht = gdn.ssm_chunk_fwd(x, grown(d["dt"]), Bm=grown(d["Bm"]), Cm=grown(d["Cm"]), z=x, **kw)
+    want, h = gdn.ssm_chunk_fwd(d["x"], d["dt"], Bm=d["Bm"], Cm=d["Cm"], z=d["x"], **kw)
+    ok()
+    tol = TOL_F32 if dtype is F32 else TOL_BF16
+    for b in range(rep):
+        assert_close(y[b:b + 1, -300:], want.double().cpu().numpy(), tol, "y")
+        assert_close(ht[b:b + 1], h.double().cpu().numpy(), TOL_F32, "ht")
+
+
+def test_example():
+    """Both sides round to bfloat16 in four places (the two projections, the
+    convolution, the scan), of values summed in different orders: four units of
+    2^-8 of a value of up to six RMS."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    spec = importlib.util.spec_from_file_location("ssm_block",
+                                                  os.path.join(root, "examples", "ssm_block.py"))
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    assert example.main(steps=5) < 4 * 6 * 2 ** -8
+
+
+CHECKED = """
+import sys
+sys.path[:0] = sys.argv[1:3]
+import torch
+from gated_delta_rule_kk_gb300 import _lib
+import gated_delta_rule_kk_gb300 as gdn
+from _mixer import conv_inputs, cuda, ssm_inputs
+
+checked, release = _lib.load(), _lib.load(sys.argv[3])
+
+
+def conv(T, dtype, lens=None):
+    d = cuda(conv_inputs(1, 1, T, 520, 4, dtype, lens=lens))
+    y = gdn.short_conv_fwd(d["x"], d["weight"], d["bias"], d["h0"], d["cu"])
+    g = gdn.short_conv_bwd(d["dy"], d["x"], d["weight"], d["bias"], d["h0"], d["dht"], d["cu"])
+    return *y, *g
+
+
+def conv_token():
+    d = cuda(conv_inputs(2, 3, 2, 520, 4, torch.bfloat16))
+    return gdn.short_conv_decode(d["x"], d["weight"], d["h0"], d["bias"]), d["h0"]
+
+
+def scan(T, dtype, lens=None, segment=0):
+    d = cuda(ssm_inputs(3, 1, T, 4, 2, 72, 128, dtype, lens=lens))
+    return gdn.ssm_chunk_fwd(d["x"], d["dt"], d["A_log"], d["Bm"], d["Cm"], D=d["D"], z=d["z"],
+                             dt_bias=d["dt_bias"], initial_state=d["h0"], cu_seqlens=d["cu"],
+                             segment_tokens=segment)
+
+
+def token(B, T, state):
+    d = cuda(ssm_inputs(4, B, T, 16, 2, 72, 128, torch.bfloat16))
+    h = d["h0"].to(state)
+    return gdn.ssm_decode(d["x"], d["dt"], d["A_log"], d["Bm"], d["Cm"], h, D=d["D"], z=d["z"],
+                          dt_bias=d["dt_bias"]), h
+
+
+cases = [lambda: conv_token()]
+for dt in (torch.bfloat16, torch.float32):
+    cases += [lambda dt=dt: conv(1, dt), lambda dt=dt: conv(37, dt, [0, 1, 36]),
+              lambda dt=dt: conv(3001, dt, [1500, 0, 1501]), lambda dt=dt: scan(1, dt),
+              lambda dt=dt: scan(300, dt, [129, 0, 1, 170]), lambda dt=dt: scan(300, dt, None, 128),
+              lambda dt=dt: token(1, 1, dt), lambda dt=dt: token(100, 3, dt)]
+for i, case in enumerate(cases):
+    results = []
+    for lib in (checked, release):
+        _lib._lib = lib
+        results.append(case())
+        status = gdn.gdn_check_device_error()
+        assert status == 0, (i, status)
+    for a, b in zip(*results):
+        assert (a is None) == (b is None) and (a is None or torch.equal(a, b)), i
+"""
+
+
+def test_checked_build():
+    """The bounds-checked build records nothing on valid calls and computes the same."""
+    tests = os.path.dirname(os.path.abspath(__file__))
+    build_lib.build(checked=True)
+    r = subprocess.run([sys.executable, "-c", CHECKED, os.path.dirname(tests), tests,
+                        build_lib.build()], env=dict(os.environ, GDN_CHECKED="1"),
+                       capture_output=True, text=True, timeout=900)
+    assert r.returncode == 0, r.stdout + r.stderr
 
 
 def test_calls_on_another_stream():
