@@ -5,10 +5,11 @@
 // log-decays a s_t inside the chunk and h the state at its start,
 //   Y = diag(e^(G_i)) (C h^T) + M X,   M_ij = (C B^T)_ij e^(G_i - G_j) s_j, j <= i
 //   h^T <- e^(G_Q) h^T + B^T W,        W_j = s_j e^(G_Q - G_j) x_j
-// that is four products with 128 rows: S = C B^T (N = 128), C h^T (N = 128: h as
-// two bf16 pieces), M X (N = 64, M as two pieces) and B^T W (N = 192: W as three
-// pieces, so that the float32 state gains no rounding from the operands).  x, B
-// and C are bf16 themselves and enter exactly.
+// that is four products with 128 rows: S = C B^T (N = 128), C h^T (N = 64, h as two
+// bf16 pieces along the keys), M X (N = 64, M as two pieces) and B^T W (N = 128 +
+// 64: W as three pieces, so that the float32 state gains no rounding from the
+// operands).  x, B and C are bf16 themselves and enter exactly.  One piece each of
+// h and M left y up to 3e-2 of its RMS off, two some 5e-5.
 //
 // One CTA per (64-column V tile, head, segment of a sequence) walks the
 // segment's chunks; h stays in registers in float32.  S, M and W do not depend
@@ -16,11 +17,11 @@
 //   0-7    M      thread (row i, 16 of every 32 columns): S from TMEM, times
 //                 e^(G_i - G_j) s_j, plus D on the diagonal, back over S as the two
 //                 bf16 A operands of M X
-//   8-15   output thread (row i, 32 columns): y times the gate, over z's tile in
-//                 shared memory, from where it leaves by TMA
+//   8-15   output thread (row i, 32 columns): y times the gate (whose z comes
+//                 straight to registers) into a tile that leaves by TMA
 //   16-23  state  thread (key k, 32 columns): h, its bf16 pieces for C h^T; and,
-//                 (row i, 32 columns) of C h^T times e^(G_i) into the accumulator
-//                 that M X adds to
+//                 (row i, 32 columns) of C h^T times e^(G_i) in place, where M X
+//                 adds to it
 //   24-27  W      thread j: row j of the three pieces
 //   28     loads  TMA: two x, two B tiles and one C tile (x, C and z of later
 //                 chunks asked into L2 before their tiles are free)
@@ -28,7 +29,14 @@
 //                 an order in which each product's operands are formed while the
 //                 others run
 //   30     scalars  step sizes, log-decays and their sums
-//   31     store  TMA: y out of z's tile, then the next z into it
+//   31     store  TMA: y
+// What bounds it (2 x 4096 tokens, 64 heads of 64 x 128, B and C shared by all:
+// 100 us, where the bytes alone would take 31 at the copy rate and CUDA cores took
+// 1620): 128 CTAs with some 6000 cycles a chunk, in which every role is busy for
+// 3000 to 5000, waiting the rest for one another; 56 products of 70 to 80 cycles to
+// issue make the longest.  Two y in TMEM (111 us with one, which M X of a chunk
+// shared with the output of the one before) and z past shared memory (its tile
+// waited for y's store) keep the output out of that chain.
 // The decays: every 32-token block b keeps f_j = s_j e^(block end - G_j) and the
 // sums inside the block, so that e^(G_i - G_j) s_j is a product of f_j and one
 // factor per row and block, all exponents sums of negative terms between j and
@@ -36,8 +44,9 @@
 // row's factor could overflow, takes an exponential per element when its decay
 // is below e^-60.
 //
-// Every wait is bounded: a role whose wait runs out goes on without waiting,
-// GDN_ERR_TIMEOUT is recorded and the call ends.
+// Every wait is bounded: a role whose wait runs out issues nothing more and ends
+// after its step, GDN_ERR_TIMEOUT is recorded, the copies and products that are on
+// their way are waited for and the block returns.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -53,15 +62,15 @@ constexpr int ST_Q = 128, ST_VT = 64;
 constexpr int ST_W_OUT = 8, ST_W_STATE = 16, ST_W_W = 24, ST_W_LOAD = 28, ST_W_MMA = 29,
               ST_W_SCALARS = 30, ST_THREADS = 32 * 32;
 // Registers of a thread of each role.  The block starts with 64 a thread, and
-// 64 + 64 + 56 + 56 + 80 + 80 + 48 + 56, the warpgroups' shares, is what 8
+// 64 + 64 + 64 + 64 + 80 + 80 + 48 + 48, the warpgroups' shares, is what 8
 // warpgroups have at 64: no role spills.
-constexpr int ST_R_OUT = 56, ST_R_STATE = 80, ST_R_W = 48, ST_R_REST = 56;
-static_assert(2 * 64 + 2 * ST_R_OUT + 2 * ST_R_STATE + ST_R_W + ST_R_REST <= 8 * 64, "registers");
+constexpr int ST_R_STATE = 80, ST_R_W = 48, ST_R_REST = 48;
+static_assert(4 * 64 + 2 * ST_R_STATE + ST_R_W + ST_R_REST <= 8 * 64, "registers");
 constexpr uint32_t ST_TILE = 16384;  // 128 rows of 128 bytes, 128-byte swizzle
 // TMEM columns: two of S, then M over it (16 columns of S hold 8 of M's high and
-// 8 of its low pieces, bf16 pairs); C h^T; y; B^T W, the first piece and the sum
-// of the others
-constexpr uint32_t ST_S = 0, ST_OFF = 256, ST_Y = 320, ST_DH = 384;
+// 8 of its low pieces, bf16 pairs); two of y, which starts as C h^T; B^T W, the
+// first piece and the sum of the others
+constexpr uint32_t ST_S = 0, ST_Y = 256, ST_DH = 384;
 
 // Per-chunk scalars, two buffers.
 struct StScalars {
@@ -73,15 +82,19 @@ struct StScalars {
   float pad[7];
 };
 
+// A wait sees a phase by its parity, so a barrier may complete a phase only after
+// every role has seen the one before: one barrier for each of two buffers, or one
+// whose next phase needs something of all its waiters first.
 struct StBars {
-  uint64_t x_full[2], x_free[2], b_full[2], b_free[2], sc_full[2], sc_free[2];
-  uint64_t c_full, z_full, z_free, off_full, s_full, m_full, w_full, dh_full, dh_free, h_full,
-      off_read, y_full, y_read, staged;
+  uint64_t x_full[2], x_free[2], b_full[2], b_free[2], sc_full[2], sc_free[2], s_full[2],
+      ready[2], y_full[2], y_read[2];
+  uint64_t y_sent, off_full, w_full, dh_full, dh_free, h_full, staged,
+      drained;
 };
 
 template <int KH>  // 64-key halves of a B or C tile
 struct StLayout {
-  static constexpr uint32_t X = 0, Z = 2 * ST_TILE, B = 3 * ST_TILE, C = B + 2 * KH * ST_TILE;
+  static constexpr uint32_t X = 0, Y = 2 * ST_TILE, B = 3 * ST_TILE, C = B + 2 * KH * ST_TILE;
   static constexpr uint32_t W = C + KH * ST_TILE, H = W + 3 * ST_TILE, SC = H + 2 * ST_TILE;
   static constexpr uint32_t BARS = SC + 2 * sizeof(StScalars);
   static constexpr uint32_t BYTES = BARS + sizeof(StBars) + 16;
@@ -124,21 +137,25 @@ __device__ __forceinline__ uint32_t elect_one() {
   return one;
 }
 // D[tmem] (+)= A * B[smem], bf16 operands, fp32 accumulate; A in shared memory
-// or in tensor memory.
-__device__ __forceinline__ void mma_ss(uint32_t one, uint32_t d_tmem, uint64_t a_desc,
-                                       uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+// or in tensor memory.  Operands in shared memory by the low word of their
+// descriptor (all share the high one): one 32-bit addition leads to the next.
+constexpr uint32_t ST_DESC_HIGH = (1024 >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ void mma_ss(uint32_t one, uint32_t d_tmem, uint32_t a, uint32_t b,
+                                       uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(one)
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\tmov.b64 da, {%1, %6};\n\tmov.b64 db, {%2, %6};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(one), "r"(ST_DESC_HIGH)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t one, uint32_t d_tmem, uint32_t a_tmem,
-                                       uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t one, uint32_t d_tmem, uint32_t a_tmem, uint32_t b,
+                                       uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(one)
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\tmov.b64 db, {%2, %6};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b), "r"(idesc), "r"(accumulate), "r"(one), "r"(ST_DESC_HIGH)
       : "memory");
 }
 __device__ __forceinline__ void commit(uint32_t one, uint64_t *bar) {
@@ -228,16 +245,12 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 __device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-__device__ __forceinline__ uint64_t sw128(const void *smem, uint32_t lbo) {
-  return ptx::sdesc(smem, lbo, 1024) | (2ull << 61);
+// Low word of the descriptor of a 128-byte swizzled operand, `lbo` bytes between
+// its halves, and the word `bytes` further on.
+__device__ __forceinline__ uint32_t sw128(const void *smem, uint32_t lbo) {
+  return (ptx::smem_u32(smem) >> 4) | lbo << 12;
 }
-__device__ __forceinline__ uint64_t ahead(uint64_t desc, uint32_t bytes) {
-  return desc + (uint64_t)(bytes >> 4);
-}
-// Bytes to 16-key step ks of a K-major operand: halves of 64 keys one tile apart.
-__device__ __forceinline__ constexpr uint32_t kstep(int ks) {
-  return (ks >> 2) * ST_TILE + (ks & 3) * 32;
-}
+__device__ __forceinline__ uint32_t ahead(uint32_t desc, uint32_t bytes) { return desc + (bytes >> 4); }
 
 // STATES: the first of two passes, which keeps only every segment's last state.
 template <int KH, bool STATES>
@@ -270,25 +283,23 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
     for (int s = 0; s < 2; ++s) {
       ptx::mbar_init(&bar.x_full[s], 1);
       ptx::mbar_init(&bar.x_free[s], 1);
-      ptx::mbar_init(&bar.b_full[s], 1);
+      ptx::mbar_init(&bar.b_full[s], STATES ? 1 : 2);  // B, and C
       ptx::mbar_init(&bar.b_free[s], 1);
       ptx::mbar_init(&bar.sc_full[s], 1);
+      ptx::mbar_init(&bar.s_full[s], 1);
+      ptx::mbar_init(&bar.ready[s], 16);  // M, and C h^T scaled
+      ptx::mbar_init(&bar.y_full[s], 1);
+      ptx::mbar_init(&bar.y_read[s], 8);
       ptx::mbar_init(&bar.sc_free[s], STATES ? 12 : 20);  // the warps that read them
     }
-    ptx::mbar_init(&bar.c_full, 1);
-    ptx::mbar_init(&bar.z_full, 1);
-    ptx::mbar_init(&bar.z_free, 1);
+    ptx::mbar_init(&bar.y_sent, 1);
     ptx::mbar_init(&bar.off_full, 1);
-    ptx::mbar_init(&bar.s_full, 1);
-    ptx::mbar_init(&bar.m_full, 8);
     ptx::mbar_init(&bar.w_full, 4);
     ptx::mbar_init(&bar.dh_full, 1);
     ptx::mbar_init(&bar.dh_free, 8);
     ptx::mbar_init(&bar.h_full, 8);
-    ptx::mbar_init(&bar.off_read, 8);
-    ptx::mbar_init(&bar.y_full, 1);
-    ptx::mbar_init(&bar.y_read, 8);
     ptx::mbar_init(&bar.staged, 8);
+    ptx::mbar_init(&bar.drained, 1);
     ptx::fence_mbar_init();
   }
   if (warp == 0) ptx::tmem_alloc<512>(tmem_slot);
@@ -301,10 +312,15 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
   auto wait = [&](uint64_t *b, int phase) {
     ok = wait_bounded(b, (uint32_t)(phase & 1), ok ? 1u << 22 : 1u) && ok;
   };
+  // a wait of its own: what it waits for comes whatever went wrong elsewhere
+  auto drain = [&](uint64_t *b, int phase) {
+    ok = wait_bounded(b, (uint32_t)(phase & 1), 1u << 22) && ok;
+  };
   auto arrive = [&](uint64_t *b) {
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(b);
   };
+  auto going = [&] { return __all_sync(~0u, ok) != 0; };
   auto tokens_of = [&](int it) { return min(ST_Q, q.hi - q.lo - it * ST_Q); };
 
   if (warp < ST_W_OUT) {
@@ -312,13 +328,13 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
     const int w4 = warp & 3, i = 32 * w4 + lane, c = 16 * (warp >> 2);
     const float skip = p.D ? p.D[h] : 0.f;
 #pragma unroll 1
-    for (int it = 0; it < (STATES ? 0 : nch); ++it) {
+    for (int it = 0; it < (STATES ? 0 : nch) && going(); ++it) {
       const StScalars &s = sc[it & 1];
       const int n = tokens_of(it);
       wait(&bar.sc_full[it & 1], it >> 1);
       const float pin = s.pin[i], own = s.tb[w4];
       const bool direct = !(fabsf(own) <= 60.f);
-      wait(&bar.s_full, it);
+      wait(&bar.s_full[it & 1], it >> 1);
       ptx::tc_fence_after();
       // blocks from the diagonal back; `between` sums the log-decays from the
       // block's end to row i
@@ -378,54 +394,59 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
       for (int b = w4 + 1; b < 4; ++b) tmem_st16(tmem + ST_S + 128 * (it & 1) + 32 * b + c + lanes, zero);
       tmem_wait_st();
       ptx::tc_fence_before();
-      arrive(&bar.m_full);
+      arrive(&bar.ready[it & 1]);
       arrive(&bar.sc_free[it & 1]);
     }
   } else if (warp < ST_W_STATE) {
     // ---------------- output
-    regs_down<ST_R_OUT>();
     const int i = 32 * (warp & 3) + lane, c0 = 32 * ((warp - ST_W_OUT) >> 2);
-    unsigned char *zt = sm + L::Z;
+    unsigned char *yt = sm + L::Y;
+    // z comes straight to registers, 8 columns on their way (from L2, where the
+    // loads ask for them) while the gate of the 8 before waits for y
+    Row<__nv_bfloat16, 8> z;
+    float gate[8];
+    auto ask = [&](int it, int c) {
+      const int64_t t = q.lo + (int64_t)it * ST_Q + i;
+      if (t < q.hi && c < width)
+        z.load(static_cast<const __nv_bfloat16 *>(p.z) + q.b * p.zb + t * p.zs + (int64_t)h * V +
+               v0 + c);
+    };
+#pragma unroll
+    for (int j = 0; j < 8; ++j) gate[j] = 1.f;
+    z.zero();
+    if (!STATES && p.z) {
+      ask(0, c0);
+      z.widen(gate);
+      silu_row<8>(gate, gate);
+      ask(0, c0 + 8);
+    }
 #pragma unroll 1
-    for (int it = 0; it < (STATES ? 0 : nch); ++it) {
+    for (int it = 0; it < (STATES ? 0 : nch) && going(); ++it) {
       const int n = tokens_of(it);
       const bool whole = n == ST_Q && !p.y_f32;
-      if (p.z) wait(&bar.z_full, it);
-      if (!p.z && it > 0) wait(&bar.z_free, it - 1);
-      wait(&bar.y_full, it);
+      wait(&bar.y_full[it & 1], it >> 1);
       ptx::tc_fence_after();
 #pragma unroll 1
       for (int c = c0; c < c0 + 32; c += 8) {
         uint32_t acc[8];
-        tmem_ld8_async(tmem + ST_Y + c + lanes, acc);
-        unsigned char *piece = zt + swz(i, c / 8);
-        float y[8];
-        if (p.z) {
-          Row<__nv_bfloat16, 8> zr;
-          zr.load(reinterpret_cast<const __nv_bfloat16 *>(piece));
-          zr.widen(y);
-          silu_row<8>(y, y);
-        }
+        tmem_ld8_async(tmem + ST_Y + 64 * (it & 1) + c + lanes, acc);
+        if (c == c0 && it > 0) wait(&bar.y_sent, it - 1);
         tmem_wait_ld();
         pin_regs<8>(acc);
         if (c == c0 + 24) {
           ptx::tc_fence_before();
-          arrive(&bar.y_read);
+          arrive(&bar.y_read[it & 1]);
         }
+        float y[8];
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
           const float x[2] = {__uint_as_float(acc[j]), __uint_as_float(acc[j + 1])};
-          if (p.z) {
-            mul_row<2>(y + j, y + j, x);
-          } else {
-            y[j] = x[0];
-            y[j + 1] = x[1];
-          }
+          mul_row<2>(y + j, gate + j, x);
         }
         Row<__nv_bfloat16, 8> out;
         out.round(y);
         if (whole) {
-          out.store(reinterpret_cast<__nv_bfloat16 *>(piece));
+          out.store(reinterpret_cast<__nv_bfloat16 *>(yt + swz(i, c / 8)));
         } else if (i < n && c < width) {
           const int64_t at = q.b * p.yb + (q.lo + it * ST_Q + i) * p.ys + (int64_t)h * V + v0 + c;
           if (!p.y_f32) {
@@ -437,9 +458,17 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
                   make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
           }
         }
+        if (c == c0 + 24) {
+          ptx::fence_proxy_async_smem();
+          arrive(&bar.staged);
+        }
+        if (p.z) {
+          z.widen(gate);
+          silu_row<8>(gate, gate);
+          const bool later = c >= c0 + 16;
+          ask(it + later, c + (later ? -16 : 16));
+        }
       }
-      ptx::fence_proxy_async_smem();
-      arrive(&bar.staged);
     }
   } else if (warp < ST_W_W) {
     // ---------------- state: key k, columns v .. v + 31
@@ -467,7 +496,7 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
     }
     unsigned char *img = sm + L::H;
 #pragma unroll 1
-    for (int it = 0; it < nch; ++it) {
+    for (int it = 0; it < nch && going(); ++it) {
       if (!STATES) {
         // C h^T of the chunk before has read the pieces: it ran before the
         // product whose result the state now holds
@@ -502,12 +531,12 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
         arrive(&bar.sc_free[it & 1]);
         const float e = __expf(G), ee[2] = {e, e};
         wait(&bar.off_full, it);
-        if (it > 0) wait(&bar.y_read, it - 1);
         ptx::tc_fence_after();
 #pragma unroll 1
         for (int c = v; c < v + 32; c += 8) {
           uint32_t a[8];
-          tmem_ld8_async(tmem + ST_OFF + c + lanes, a);
+          const uint32_t at = tmem + ST_Y + 64 * (it & 1) + c + lanes;
+          tmem_ld8_async(at, a);
           tmem_wait_ld();
           pin_regs<8>(a);
 #pragma unroll
@@ -517,11 +546,11 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
             a[j] = __float_as_uint(x[0]);
             a[j + 1] = __float_as_uint(x[1]);
           }
-          tmem_st8(tmem + ST_Y + c + lanes, a);
+          tmem_st8(at, a);
         }
         tmem_wait_st();
         ptx::tc_fence_before();
-        arrive(&bar.off_read);
+        arrive(&bar.ready[it & 1]);
       }
       wait(&bar.dh_full, it);
       ptx::tc_fence_after();
@@ -561,7 +590,7 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
     const int j = tid - 32 * ST_W_W;
     unsigned char *img = sm + L::W;
 #pragma unroll 1
-    for (int it = 0; it < nch; ++it) {
+    for (int it = 0; it < nch && going(); ++it) {
       unsigned char *xt = sm + L::X + (it & 1) * ST_TILE, *bt = sm + L::B + (it & 1) * KH * ST_TILE;
       const int n = tokens_of(it);
       wait(&bar.sc_full[it & 1], it >> 1);
@@ -619,34 +648,44 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
       ptx::prefetch_tmap(&tm_b);
       if (!STATES) ptx::prefetch_tmap(&tm_c);
     }
+    int xs = 0, bms = 0;  // tiles asked for
 #pragma unroll 1
-    for (int it = 0; it < nch; ++it) {
+    for (int it = 0; it < nch && going(); ++it) {
       const int bs = it & 1, t = q.lo + it * ST_Q;
       // one copy a lane: the copies of one thread complete one after another
-      if (it >= 2) wait(&bar.x_free[bs], (it >> 1) - 1);
-      if (lane == 0) {
-        ptx::mbar_arrive_expect_tx(&bar.x_full[bs], ST_TILE);
-        tma_load_4d(sm + L::X + bs * ST_TILE, &tm_x, v0, h, t, q.b, &bar.x_full[bs]);
-        if (it + 2 < nch) tma_prefetch_4d(&tm_x, v0, h, t + 2 * ST_Q, q.b);
-      }
       if (it >= 2) wait(&bar.b_free[bs], (it >> 1) - 1);
+      if (!going()) break;
       if (lane == 0) ptx::mbar_arrive_expect_tx(&bar.b_full[bs], KH * ST_TILE);
       __syncwarp();
       if (lane >= 1 && lane <= KH)
         tma_load_4d(sm + L::B + (bs * KH + lane - 1) * ST_TILE, &tm_b, 64 * (lane - 1), g, t, q.b,
                     &bar.b_full[bs]);
+      ++bms;
+      if (it >= 2) wait(&bar.x_free[bs], (it >> 1) - 1);
+      if (!going()) break;
+      if (lane == 0) {
+        ptx::mbar_arrive_expect_tx(&bar.x_full[bs], ST_TILE);
+        tma_load_4d(sm + L::X + bs * ST_TILE, &tm_x, v0, h, t, q.b, &bar.x_full[bs]);
+        if (it + 2 < nch) tma_prefetch_4d(&tm_x, v0, h, t + 2 * ST_Q, q.b);
+      }
+      ++xs;
       if (!STATES) {
         if (it >= 1) wait(&bar.off_full, it - 1);  // C h^T, the last to read C
-        if (lane == 0) ptx::mbar_arrive_expect_tx(&bar.c_full, KH * ST_TILE);
+        if (!going()) break;
+        if (lane == 0) ptx::mbar_arrive_expect_tx(&bar.b_full[bs], KH * ST_TILE);
         __syncwarp();
         if (lane > KH && lane <= 2 * KH) {
           const int half = lane - 1 - KH;
-          tma_load_4d(sm + L::C + half * ST_TILE, &tm_c, 64 * half, g, t, q.b, &bar.c_full);
+          tma_load_4d(sm + L::C + half * ST_TILE, &tm_c, 64 * half, g, t, q.b,
+                      &bar.b_full[bs]);
           if (it + 1 < nch) tma_prefetch_4d(&tm_c, 64 * half, g, t + ST_Q, q.b);
         }
         if (p.z && lane == 0 && it + 1 < nch) tma_prefetch_4d(&tm_z, v0, h, t + ST_Q, q.b);
       }
     }
+    // the last copies land before the block ends, whoever else waits for them
+    for (int k = max(0, xs - 2); k < xs; ++k) drain(&bar.x_full[k & 1], k >> 1);
+    for (int k = max(0, bms - 2); k < bms; ++k) drain(&bar.b_full[k & 1], k >> 1);
   } else if (warp == ST_W_MMA) {
     // ---------------- MMA
     regs_down<ST_R_REST>();
@@ -655,30 +694,38 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
     const uint32_t id_dh2 = ptx::idesc_bf16(128, 128, 1, 1);  // B, two pieces of W MN-major
     const uint32_t id_dh1 = ptx::idesc_bf16(128, 64, 1, 1);
     const uint32_t one = elect_one();
-    const uint64_t dc = sw128(sm + L::C, 16), dh = sw128(sm + L::H, ST_TILE);
-    const uint64_t dw = sw128(sm + L::W, ST_TILE);
+    const uint32_t dc = sw128(sm + L::C, 16), dh = sw128(sm + L::H, ST_TILE);
+    const uint32_t dw = sw128(sm + L::W, ST_TILE);
     auto b_of = [&](int it) { return (uint32_t)(L::B + (it & 1) * KH * ST_TILE); };
+    // (S goes where M was two chunks before: M X of that chunk is behind the
+    // C h^T whose scaled rows `ready` has announced since)
     auto scores = [&](int it) {
-      const uint64_t db = sw128(sm + b_of(it), 16);
-      wait(&bar.c_full, it);
+      const uint32_t db = sw128(sm + b_of(it), 16), d = tmem + ST_S + 128 * (it & 1);
       wait(&bar.b_full[it & 1], it >> 1);
-      if (it > 1) wait(&bar.y_full, it - 2);  // M X, which reads M out of S's columns
+      if (!going()) return;
       ptx::tc_fence_after();
+#pragma unroll 1
+      for (int half = 0; half < KH; ++half)
 #pragma unroll 2
-      for (int ks = 0; ks < 4 * KH; ++ks)
-        mma_ss(one, tmem + ST_S + 128 * (it & 1), ahead(dc, kstep(ks)), ahead(db, kstep(ks)), id_s,
-               ks > 0);
-      commit(one, &bar.s_full);
+        for (int ks = 0; ks < 4; ++ks)
+          mma_ss(one, d, ahead(dc, half * ST_TILE + ks * 32), ahead(db, half * ST_TILE + ks * 32),
+                 id_s, half + ks > 0);
+      commit(one, &bar.s_full[it & 1]);
     };
     auto carried = [&](int it) {  // C h^T
       wait(&bar.h_full, it);
-      if (it > 0) wait(&bar.off_read, it - 1);
+      if (it > 1) wait(&bar.y_read[it & 1], (it >> 1) - 1);
+      if (!going()) return;
       ptx::tc_fence_after();
+      const uint32_t d = tmem + ST_Y + 64 * (it & 1);
+#pragma unroll 1
+      for (int half = 0; half < KH; ++half)
 #pragma unroll 2
-      for (int ks = 0; ks < 4 * KH; ++ks) {
-        mma_ss(one, tmem + ST_OFF, ahead(dc, kstep(ks)), ahead(dh, ks * 2048), id_y, ks > 0);
-        mma_ss(one, tmem + ST_OFF, ahead(dc, kstep(ks)), ahead(dh, ST_TILE + ks * 2048), id_y, 1);
-      }
+        for (int ks = 0; ks < 4; ++ks) {
+          const uint32_t a = ahead(dc, half * ST_TILE + ks * 32), b = ahead(dh, (4 * half + ks) * 2048);
+          mma_ss(one, d, a, b, id_y, half + ks > 0);
+          mma_ss(one, d, a, ahead(b, ST_TILE), id_y, 1);
+        }
       commit(one, &bar.off_full);
     };
     if (!STATES && nch > 0) {
@@ -686,39 +733,48 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
       carried(0);
     }
 #pragma unroll 1
-    for (int it = 0; it < nch; ++it) {
+    for (int it = 0; it < nch && going(); ++it) {
       // with one half of keys the product's upper 64 rows are of the tile after
       // B, and are not read
-      const uint64_t db = sw128(sm + b_of(it), ST_TILE);
-      wait(&bar.b_full[it & 1], it >> 1);
+      const uint32_t db = sw128(sm + b_of(it), ST_TILE);
       wait(&bar.w_full, it);
-      if (it > 0) wait(&bar.dh_free, it - 1);
-      ptx::tc_fence_after();
-#pragma unroll 2
-      for (int ks = 0; ks < 8; ++ks) {
-        mma_ss(one, tmem + ST_DH, ahead(db, ks * 2048), ahead(dw, ks * 2048), id_dh2, ks > 0);
-        mma_ss(one, tmem + ST_DH + 64, ahead(db, ks * 2048), ahead(dw, 2 * ST_TILE + ks * 2048),
-               id_dh1, 1);
+      if (STATES) {  // else the scores' b_full and C h^T's h_full said so
+        wait(&bar.b_full[it & 1], it >> 1);
+        if (it > 0) wait(&bar.dh_free, it - 1);
       }
+      if (!going()) break;
+      ptx::tc_fence_after();
+#pragma unroll 1
+      for (int k4 = 0; k4 < 8; k4 += 2)
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          const uint32_t a = ahead(db, (k4 + ks) * 2048), b = ahead(dw, (k4 + ks) * 2048);
+          mma_ss(one, tmem + ST_DH, a, b, id_dh2, k4 + ks > 0);
+          mma_ss(one, tmem + ST_DH + 64, a, ahead(b, 2 * ST_TILE), id_dh1, 1);
+        }
       commit(one, &bar.dh_full);
       commit(one, &bar.b_free[it & 1]);
       if (STATES) {
         commit(one, &bar.x_free[it & 1]);
         continue;
       }
+      wait(&bar.ready[it & 1], it >> 1);
+      if (!going()) break;
       if (it + 1 < nch) scores(it + 1);
-      const uint64_t dx = sw128(sm + L::X + (it & 1) * ST_TILE, ST_TILE);
-      wait(&bar.m_full, it);
-      wait(&bar.off_read, it);
       ptx::tc_fence_after();
-#pragma unroll 2
-      for (int ks = 0; ks < 16; ++ks)
-        mma_ts(one, tmem + ST_Y, tmem + ST_S + 128 * (it & 1) + 8 * ks,
-               ahead(dx, (ks >> 1) * 2048), id_y, 1);
-      commit(one, &bar.y_full);
+      const uint32_t dx = sw128(sm + L::X + (it & 1) * ST_TILE, ST_TILE);
+      const uint32_t dm = tmem + ST_S + 128 * (it & 1), dy = tmem + ST_Y + 64 * (it & 1);
+#pragma unroll 1
+      for (int k4 = 0; k4 < 16; k4 += 2)
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+          mma_ts(one, dy, dm + 8 * (k4 + ks), ahead(dx, ((k4 + ks) >> 1) * 2048), id_y, 1);
+      commit(one, &bar.y_full[it & 1]);
       commit(one, &bar.x_free[it & 1]);
       if (it + 1 < nch) carried(it + 1);
     }
+    commit(one, &bar.drained);
+    drain(&bar.drained, 0);
   } else if (warp == ST_W_SCALARS) {
     // ---------------- scalars
     regs_down<ST_R_REST>();
@@ -740,42 +796,46 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
     };
     auto put = [&](int it, const uint32_t (&raw)[4]) {
       StScalars &s = sc[it & 1];
-      float tail = 0.f, total = 0.f;
-#pragma unroll 1
-      for (int b = 3; b >= 0; --b) {
-        uint32_t bits = raw[0];
+      // the four blocks side by side: their sums are long chains of shuffles
+      float step[4], before[4], after[4];  // sums up to and from this token
 #pragma unroll
-        for (int j = 1; j < 4; ++j) bits = b == j ? raw[j] : bits;
-        const float v = __uint_as_float(p.dt_f32 ? bits : bits << 16) + bias;
+      for (int b = 0; b < 4; ++b) {
+        const float v = __uint_as_float(p.dt_f32 ? raw[b] : raw[b] << 16) + bias;
         const float soft = log1pf(expf(fminf(v, 20.f)));
-        float step = !p.softplus || !(v <= 20.f) ? v : soft;
-        if (q.lo + it * ST_Q + 32 * b + lane >= q.hi) step = 0.f;
-        float before = a * step, after = before;  // sums up to and from this token
+        step[b] = !p.softplus || !(v <= 20.f) ? v : soft;
+        if (q.lo + it * ST_Q + 32 * b + lane >= q.hi) step[b] = 0.f;
+        before[b] = after[b] = a * step[b];
+      }
+#pragma unroll 1
+      for (int o = 1; o < 32; o <<= 1) {
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const float u = __shfl_up_sync(~0u, before, o), d = __shfl_down_sync(~0u, after, o);
-          if (lane >= o) before += u;
-          if (lane + o < 32) after += d;
+        for (int b = 0; b < 4; ++b) {
+          const float u = __shfl_up_sync(~0u, before[b], o), d = __shfl_down_sync(~0u, after[b], o);
+          if (lane >= o) before[b] += u;
+          if (lane + o < 32) after[b] += d;
         }
-        const float all = __shfl_sync(~0u, before, 31);
-        const float rest = __shfl_down_sync(~0u, after, 1);
-        s.pin[32 * b + lane] = before;
-        s.f[32 * b + lane] = step * expf(lane < 31 ? rest : 0.f);
+      }
+      float tail = 0.f;
+#pragma unroll
+      for (int b = 3; b >= 0; --b) {
+        const float all = __shfl_sync(~0u, before[b], 31);
+        const float rest = __shfl_down_sync(~0u, after[b], 1);
+        s.pin[32 * b + lane] = before[b];
+        s.f[32 * b + lane] = step[b] * expf(lane < 31 ? rest : 0.f);
         if (lane == 0) {
           s.tb[b] = all;
           s.sfx[b] = expf(tail);
         }
         tail += all;
       }
-      total = tail;
-      if (lane == 0) s.total = total;
-      sum += total;
+      if (lane == 0) s.total = tail;
+      sum += tail;
       arrive(&bar.sc_full[it & 1]);
     };
     uint32_t raw[4];
     fetch(0, raw);
 #pragma unroll 1
-    for (int it = 0; it < nch; ++it) {
+    for (int it = 0; it < nch && going(); ++it) {
       uint32_t next[4];
       fetch(it + 1, next);
       if (it >= 2) wait(&bar.sc_free[it & 1], (it >> 1) - 1);
@@ -787,22 +847,17 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
   } else if (!STATES) {
     // ---------------- store
     regs_down<ST_R_REST>();
-    auto load_z = [&](int it) {
-      ptx::mbar_arrive_expect_tx(&bar.z_full, ST_TILE);
-      tma_load_4d(sm + L::Z, &tm_z, v0, h, q.lo + it * ST_Q, q.b, &bar.z_full);
-    };
-    if (p.z && nch > 0 && lane == 0) load_z(0);
 #pragma unroll 1
-    for (int it = 0; it < nch; ++it) {
+    for (int it = 0; it < nch && going(); ++it) {
       wait(&bar.staged, it);
+      if (!going()) break;
       if (lane == 0) {
         if (tokens_of(it) == ST_Q && !p.y_f32) {
-          tma_store_4d(&tm_y, v0, h, q.lo + it * ST_Q, q.b, sm + L::Z);
+          tma_store_4d(&tm_y, v0, h, q.lo + it * ST_Q, q.b, sm + L::Y);
           ptx::bulk_commit();
           ptx::bulk_wait_read<0>();
         }
-        ptx::mbar_arrive(&bar.z_free);
-        if (p.z && it + 1 < nch) load_z(it + 1);
+        ptx::mbar_arrive(&bar.y_sent);
       }
       __syncwarp();
     }
