@@ -16,6 +16,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "abi_check.h"
 #include "ptx.cuh"
@@ -677,13 +678,14 @@ ssm_decode_ring_kernel(SsmDecodeParams p, int items) {
 template <typename S, int LPR, int PP, int TM>
 cudaError_t launch_decode(SsmDecodeParams &p, cudaStream_t stream) {
   constexpr int ROWS = SD_WARPS * SD_ROWS * 32 / LPR;
-  const int64_t bh = (int64_t)p.B * p.H, bytes = (int64_t)p.V * p.K * sizeof(S);
-  // The ring pays once every block has several items: below, its start and end
-  // are not hidden (B = 256, H = 64, bf16 states of 64 x 128: 92.9 us against 152.5).
+  const int64_t bh = (int64_t)p.B * p.H;
+  // The ring pays once every block has an item (requests of 64 heads, bf16 states of
+  // 64 x 128, ring / direct, us: 8 requests 6.2 / 6.3, 16 8.0 / 9.3, 64 20.3 / 28.9,
+  // 256 92.9 / 152.5).
   const int blocks = sd_blocks(TM) * sm_count();
   const int rows = std::min(ROWS, (int)(SD_TILE / (p.K * sizeof(S))));
   const int vblocks = (p.V + rows - 1) / rows;
-  if (bh * bytes >= (int64_t)SD_STAGES * SD_TILE * blocks && bh * vblocks <= 0x7fffffff) {
+  if (bh * vblocks >= blocks && bh * vblocks <= 0x7fffffff) {
     p.vblocks = vblocks;
     p.rows = (p.V + vblocks - 1) / vblocks;
     const int smem = SD_STAGES * ((int)SD_TILE + SdCoef(p.K, p.rows, p.T).bytes());
@@ -788,21 +790,46 @@ gdn_status_t check_chunk_args(const ssm_chunk_args &a) {
   return GDN_OK;
 }
 
-// Segment length when the caller leaves it open.  Cutting costs a second pass
-// over x, B and dt and a block reads the states of the segments before its own,
-// so sequences stay whole when they give half the blocks the GPU holds; else
-// segments are as long as still fills it, at most 64 to a sequence.
+// Segment length when the caller leaves it open: the one of least estimated time,
+// in tokens that are walked one after another.  Whole sequences are walked in one
+// pass.  Segments are walked in two, the first without y (together 1.4 times one on
+// the tensor cores, 1.85 times on CUDA cores), and cost a second start and, for the
+// later ones, the states of all segments before; on the tensor cores once for every
+// block that an SM takes after another, on CUDA cores behind the three other blocks
+// of the SM.  `held` blocks run at a time:
+// sequences of one length take whole waves of them; packed ones, whose lengths the
+// host does not know, queue, with half a block's walk left idle at the end (the
+// longest is taken to be half as long again as the mean).
+// One sequence of 4096 tokens (states of 64 x 128), whole / segments, us: bf16
+// 8 heads 80 / 35, 32 heads 81 / 47, 64 heads 82 / 77, 80 heads 82 / 116;
+// float32 8 heads 1019 / 115, 64 heads 1398 / 619, 120 heads 1470 / 1063.  Eight
+// packed prompts (bf16), 32068 tokens and 32 heads 277 / 274 to 310, 12001 tokens
+// and 16 heads 55 / 60 to 109.
 int choose_segment(const SsmParams &p, bool tc) {
   const int cols = tc ? 64 : 32;  // of a block's state tile; one block an SM, or four
-  const int64_t chains = (int64_t)p.H * ((p.V + cols - 1) / cols);
-  const int64_t want = (tc ? 1 : 4) * (int64_t)sm_count();
-  if (p.cu == nullptr && chains * p.N >= want / 2) return SSM_WHOLE;
-  const int64_t tokens = p.cu ? p.T : (int64_t)p.T * p.N;
-  int64_t seg = tokens * chains / want;
-  if (seg < p.T / 64) seg = p.T / 64;
-  const int64_t unit = tc ? SSM_UNIT : SSM_UNIT / 2;
-  seg = std::max(unit, (seg + unit - 1) / unit * unit);
-  return seg < p.T ? (int)seg : SSM_WHOLE;
+  const double chains = (double)p.H * ((p.V + cols - 1) / cols);
+  const double held = (tc ? 1 : 4) * sm_count();
+  const double passes = tc ? 1.4 : 1.85, start = tc ? 400 : 64, state = tc ? 50 : 8;
+  const int longest = p.cu ? (int)std::min<int64_t>(p.T, (int64_t)p.T * 3 / (2 * p.N)) : p.T;
+  auto walked = [&](int seg, int pieces) {
+    return p.cu ? std::max<double>(seg, p.T * chains / held + seg / 2)
+                : std::ceil(chains * p.N * pieces / held) * seg;
+  };
+  const int unit = tc ? SSM_UNIT : SSM_UNIT / 2;
+  int best = SSM_WHOLE;
+  double least = walked(longest, 1) + start / 2;
+  for (int n = 2; n <= 64; ++n) {
+    const int seg = ((longest + n - 1) / n + unit - 1) / unit * unit;
+    const int pieces = (longest + seg - 1) / seg;
+    if (pieces < 2) break;
+    const double tokens = walked(seg, pieces), starts = tc ? tokens / seg : 1;
+    const double cost = passes * tokens + starts * (start + state * pieces);
+    if (cost < least) {
+      least = cost;
+      best = seg;
+    }
+  }
+  return best;
 }
 
 SsmParams chunk_params(const ssm_chunk_args &a) {
