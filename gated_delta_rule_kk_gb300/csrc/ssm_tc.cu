@@ -33,8 +33,9 @@
 // What bounds it (2 x 4096 tokens, 64 heads of 64 x 128, B and C shared by all:
 // 100 us, where the bytes alone would take 31 at the copy rate and CUDA cores took
 // 1620): 128 CTAs with some 6000 cycles a chunk, in which every role is busy for
-// 3000 to 5000, waiting the rest for one another; 56 products of 70 to 80 cycles to
-// issue make the longest.  Two y in TMEM (111 us with one, which M X of a chunk
+// 3000 to 5000, waiting the rest for one another.  The warps' 14000 instructions a
+// chunk take 65% of an SM's issue slots, the products 42% of the tensor pipe, HBM
+// 22% of its rate: fewer instructions a chunk would be the next step.  Two y in TMEM (111 us with one, which M X of a chunk
 // shared with the output of the one before) and z past shared memory (its tile
 // waited for y's store) keep the output out of that chain.
 // The decays: every 32-token block b keeps f_j = s_j e^(block end - G_j) and the
