@@ -481,9 +481,11 @@ conv_ring_kernel(const __grid_constant__ CUtensorMap tm_x,
   };
   if (tid >= R::THREADS) {
     const int boxes = p.D - c0 > CR_BOX ? R::BOXES : 1;
-    for (int u = lo, m = 0; u < stop; u += CR_STAGE, ++m) {
+    int m = 0;  // stages asked for
+    for (int u = lo; u < stop; u += CR_STAGE, ++m) {
       const int s = m % S;
       if (m >= S) wait(&empty[s], m / S - 1);
+      if (!__all_sync(~0u, ok)) break;
       if (lane == 0) ptx::mbar_arrive_expect_tx(&full[s], boxes * R::BOX * (BWD ? 2 : 1));
       __syncwarp();
       // one copy a lane: the copies of one thread complete one after another
@@ -493,6 +495,9 @@ conv_ring_kernel(const __grid_constant__ CUtensorMap tm_x,
                          g ? (const void *)&tm_g : (const void *)&tm_x, c0 + box * CR_BOX, u, b,
                          &full[s]);
     }
+    // the last copies land before the warp ends, whoever else waits for them
+    for (int k = max(0, m - S); k < m; ++k)
+      ok = ptx::mbar_wait_bounded(&full[k % S], (uint32_t)(k / S & 1), 1u << 22) && ok;
     if (!ok && lane == 0) record_error(p.err, GDN_ERR_TIMEOUT);
     return;
   }

@@ -647,6 +647,7 @@ ssm_decode_ring_kernel(SsmDecodeParams p, int items) {
       const int s = n % SD_STAGES;
       const SdItem it = item_at(i);
       if (n >= SD_STAGES) wait(&empty[s], n / SD_STAGES - 1);
+      if (!__all_sync(~0u, ok)) break;
       if (lane == 0) {
         if (good(it)) {
           const uint32_t bytes = bytes_of(it);
@@ -658,6 +659,9 @@ ssm_decode_ring_kernel(SsmDecodeParams p, int items) {
       }
       __syncwarp();
     }
+    // the last copies land before the warp ends, whoever else waits for them
+    for (int k = max(0, n - SD_STAGES); k < n; ++k)
+      ok = ptx::mbar_wait_bounded(&full[k % SD_STAGES], (uint32_t)(k / SD_STAGES & 1), 1u << 22) && ok;
   } else {
     for (int i = blockIdx.x; i < items; i += gridDim.x, ++n) {
       const int s = n % SD_STAGES;
@@ -688,7 +692,7 @@ cudaError_t launch_decode(SsmDecodeParams &p, cudaStream_t stream) {
   const int blocks = sd_blocks(TM) * sm_count();
   const int rows = std::min(ROWS, (int)(SD_TILE / (p.K * sizeof(S))));
   const int vblocks = (p.V + rows - 1) / rows;
-  if (bh * vblocks >= blocks && bh * vblocks <= 0x7fffffff) {
+  if (bh * vblocks >= blocks && bh * vblocks <= 0x7fff0000) {
     p.vblocks = vblocks;
     p.rows = (p.V + vblocks - 1) / vblocks;
     const int smem = SD_STAGES * ((int)SD_TILE + SdCoef(p.K, p.rows, p.T).bytes());
