@@ -823,6 +823,8 @@ int choose_segment(const SsmParams &p, bool tc) {
                 : std::ceil(chains * p.N * pieces / held) * seg;
   };
   const int unit = tc ? SSM_UNIT : SSM_UNIT / 2;
+  // (one unit holds it whole; no tokens, or a mean of less than one, too)
+  if (longest <= unit) return SSM_WHOLE;
   int best = SSM_WHOLE;
   double least = walked(longest, 1) + start / 2;
   for (int n = 2; n <= 64; ++n) {
