@@ -788,10 +788,11 @@ bool whole_pieces(int64_t D, int vec, int32_t dtype, std::initializer_list<const
 
 // Tokens of a run: as few as let the whole call be on the GPU at once (with
 // `threads` resident threads on an SM), so that no second wave is left
-// half-empty.  A run reads W - 1 rows twice, from L2.
+// half-empty.  A run reads W - 1 rows twice, from L2.  At least a batch, also of no
+// tokens: runs are divided by.
 int run_tokens(int64_t tokens, int64_t pieces, int threads) {
   const int64_t resident = (int64_t)sm_count() * threads;
-  const int64_t run = (tokens * pieces + resident - 1) / resident;
+  const int64_t run = std::max<int64_t>(1, (tokens * pieces + resident - 1) / resident);
   return (int)((run + CV_BATCH - 1) / CV_BATCH * CV_BATCH);
 }
 
@@ -971,10 +972,18 @@ gdn_status_t short_conv_fwd(const short_conv_args *a, gdn_stream_t stream) {
   p.xs = a->x_stride; p.xb = a->B > 1 ? a->x_batch_stride : 0;
   p.ys = a->y_stride; p.yb = a->B > 1 ? a->y_batch_stride : 0;
   p.D = a->D; p.silu = a->silu; p.w_f32 = a->weight_dtype == GDN_F32;
-  p.err = device_error_word();
-  if (p.err == nullptr) return launch_status(cudaGetLastError(), "device error word");
   const RingShape r = ring_shape(a->dtype, a->B, a->T, a->D, false, {a->x}, a->y, {p.xs, p.xb},
                                  {p.ys, p.yb});
+  const int wide = CV_PIECE / 2;
+  const bool whole = whole_pieces(a->D, wide, a->dtype, {a->x, a->y}, {p.xs, p.xb, p.ys, p.yb});
+  const int64_t pieces = a->D / (whole ? wide : 1);
+  p.run = run_tokens((int64_t)a->B * a->T, pieces, CV_MAX_THREADS * CV_BLOCKS);
+  p.tiles = (a->T + p.run - 1) / p.run;
+  const int block = even_block(pieces);
+  const int64_t gx = (int64_t)a->B * p.tiles + (a->ht ? a->N : 0);
+  if (gx == 0) return GDN_OK;
+  p.err = device_error_word();
+  if (p.err == nullptr) return launch_status(cudaGetLastError(), "device error word");
   if (r.use) {
     ConvRingParams rp{};
     rp.weight = a->weight; rp.bias = a->bias; rp.h0 = a->h0; rp.out = a->y; rp.ht = a->ht;
@@ -989,15 +998,6 @@ gdn_status_t short_conv_fwd(const short_conv_args *a, gdn_stream_t stream) {
                                     }),
                          "short convolution launch");
   }
-  const int wide = CV_PIECE / 2;
-  const bool whole = whole_pieces(a->D, wide, a->dtype, {a->x, a->y}, {p.xs, p.xb, p.ys, p.yb});
-  const int vec = whole ? wide : 1;
-  const int64_t pieces = a->D / vec;
-  p.run = run_tokens((int64_t)a->B * a->T, pieces, CV_MAX_THREADS * CV_BLOCKS);
-  p.tiles = (a->T + p.run - 1) / p.run;
-  const int block = even_block(pieces);
-  const int64_t gx = (int64_t)a->B * p.tiles + (a->ht ? a->N : 0);
-  if (gx == 0) return GDN_OK;
   const dim3 grid((unsigned)gx, (unsigned)((pieces + block - 1) / block));
   return launch_status(
       with_types(a->dtype, a->W,

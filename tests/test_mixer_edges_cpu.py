@@ -44,3 +44,19 @@ n = ctypes.c_size_t(9)
 assert lib.ssm_chunk_workspace_size(ctypes.byref(a), ctypes.byref(n)) == Status.OK
 assert n.value == 0
 """)
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_convolution_without_tokens(lib, dtype):
+    """Without a state to return there is nothing to launch; with one, the launch's shape
+    (formed before the device is asked for) has no length of zero to divide by."""
+    in_a_process(f"""
+a = conv_args(dtype={dtype}, weight_dtype={dtype}, T=0, x=None, y=None)
+assert lib.short_conv_fwd(ctypes.byref(a), None) == Status.OK
+a = conv_args(dtype={dtype}, weight_dtype={dtype}, T=0, B=1, N=3, cu_seqlens=FAKE)
+assert lib.short_conv_fwd(ctypes.byref(a), None) == Status.OK
+import torch
+if not torch.cuda.is_available():
+    a = conv_args(dtype={dtype}, weight_dtype={dtype}, T=0, ht=FAKE)
+    assert lib.short_conv_fwd(ctypes.byref(a), None) == Status.CUDA
+""")
