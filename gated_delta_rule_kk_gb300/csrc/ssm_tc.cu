@@ -93,12 +93,22 @@ struct StBars {
       drained;
 };
 
+// The first token of the segment, counted from its start, whose x is not finite in
+// each of the tile's columns, and the least of them.  The zeros of M past the
+// diagonal would carry such an x to the tokens before it (0 x Inf = NaN), so it
+// enters M X as zero and the output writes NaN from its token on.
+struct StBad {
+  int first[ST_VT], any;
+};
+constexpr int ST_NEVER = 0x7fffffff;
+
 template <int KH>  // 64-key halves of a B or C tile
 struct StLayout {
   static constexpr uint32_t X = 0, Y = 2 * ST_TILE, B = 3 * ST_TILE, C = B + 2 * KH * ST_TILE;
   static constexpr uint32_t W = C + KH * ST_TILE, H = W + 3 * ST_TILE, SC = H + 2 * ST_TILE;
   static constexpr uint32_t BARS = SC + 2 * sizeof(StScalars);
-  static constexpr uint32_t BYTES = BARS + sizeof(StBars) + 16;
+  static constexpr uint32_t BAD = BARS + sizeof(StBars) + 16;
+  static constexpr uint32_t BYTES = BAD + sizeof(StBad);
 };
 static_assert(StLayout<2>::BYTES <= 232448, "shared memory of one CTA");
 
@@ -264,6 +274,7 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
   StScalars *sc = reinterpret_cast<StScalars *>(sm + L::SC);
   StBars &bar = *reinterpret_cast<StBars *>(sm + L::BARS);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::BARS + sizeof(StBars));
+  StBad &bad = *reinterpret_cast<StBad *>(sm + L::BAD);
   // (a warp's index the compiler knows to be the same in all its lanes, so that
   // each role's addresses and descriptors live in uniform registers)
   const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
@@ -303,6 +314,7 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
     ptx::mbar_init(&bar.drained, 1);
     ptx::fence_mbar_init();
   }
+  if (!STATES && tid <= ST_VT) (tid < ST_VT ? bad.first[tid] : bad.any) = ST_NEVER;
   if (warp == 0) ptx::tmem_alloc<512>(tmem_slot);
   ptx::tc_fence_before();
   __syncthreads();
@@ -427,6 +439,7 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
       const bool whole = n == ST_Q && !p.y_f32;
       wait(&bar.y_full[it & 1], it >> 1);
       ptx::tc_fence_after();
+      const bool poisoned = it * ST_Q + i >= *const_cast<volatile int *>(&bad.any);
 #pragma unroll 1
       for (int c = c0; c < c0 + 32; c += 8) {
         uint32_t acc[8];
@@ -443,6 +456,11 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
         for (int j = 0; j < 8; j += 2) {
           const float x[2] = {__uint_as_float(acc[j]), __uint_as_float(acc[j + 1])};
           mul_row<2>(y + j, gate + j, x);
+        }
+        if (poisoned) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (it * ST_Q + i >= bad.first[c + j]) y[j] = __uint_as_float(0x7fffffffu);
         }
         Row<__nv_bfloat16, 8> out;
         out.round(y);
@@ -602,6 +620,8 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
       if (it > 0) wait(&bar.dh_full, it - 1);  // the product before has read W
       if (j < n) {
         const float ww[2] = {w, w};
+        // NaNs once an x of the row is not finite: its last piece is NaN
+        __nv_bfloat162 odd = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll 1
         for (int c = 0; c < 8; ++c) {
           const uint4 u = *reinterpret_cast<const uint4 *>(xt + swz(j, c));
@@ -619,11 +639,23 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
             d[0] = low(b[k]); d[1] = high(b[k]);
             sub_row<2>(v, v, d);
             e[k] = pack2(v[0], v[1]);
+            odd = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&e[k]),
+                          __floats2bfloat162_rn(0.f, 0.f), odd);
           }
           *reinterpret_cast<uint4 *>(img + swz(j, c)) = make_uint4(a[0], a[1], a[2], a[3]);
           *reinterpret_cast<uint4 *>(img + ST_TILE + swz(j, c)) = make_uint4(b[0], b[1], b[2], b[3]);
           *reinterpret_cast<uint4 *>(img + 2 * ST_TILE + swz(j, c)) =
               make_uint4(e[0], e[1], e[2], e[3]);
+        }
+        if (!STATES && !__hbeq2(odd, odd)) {
+#pragma unroll 1
+          for (int c = 0; c < ST_VT; ++c) {
+            uint16_t *x = reinterpret_cast<uint16_t *>(xt + swz(j, c / 8)) + c % 8;
+            if ((*x & 0x7f80) != 0x7f80) continue;
+            *x = 0;
+            atomicMin(&bad.first[c], it * ST_Q + j);
+            atomicMin(&bad.any, it * ST_Q + j);
+          }
         }
       } else {
         // past the sequence's end: what the loads brought is another sequence's

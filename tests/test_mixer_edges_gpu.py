@@ -1,0 +1,72 @@
+"""Edges of the short convolution and the state space scan on the GPU."""
+import pytest
+import torch
+
+import gated_delta_rule_kk_gb300 as gdn
+from gated_delta_rule_kk_gb300 import Status
+
+from _mixer import cuda, ssm_inputs
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def ok():
+    assert gdn.gdn_check_device_error() == Status.OK
+
+
+def scan(d, **kw):
+    return gdn.ssm_chunk_fwd(d["x"], d["dt"], d["A_log"], d["Bm"], d["Cm"], D=d["D"], z=d["z"],
+                             dt_bias=d["dt_bias"], initial_state=d["h0"], cu_seqlens=d["cu"], **kw)
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("dtype,T,V,K,lens,segment,at", [
+    (BF16, 300, 64, 128, None, 0, [(5, 1, 3)]),
+    (BF16, 300, 64, 128, None, 0, [(127, 0, 63), (128, 0, 0), (299, 1, 33)]),
+    (BF16, 300, 64, 64, None, 128, [(200, 1, 17), (140, 1, 17), (256, 0, 5)]),
+    (BF16, 300, 72, 128, [100, 0, 200], 0, [(50, 0, 71), (120, 1, 64), (299, 0, 2)]),
+    (F32, 100, 40, 48, None, 0, [(5, 1, 3), (70, 0, 39)]),
+])
+@pytest.mark.parametrize("out", [BF16, F32])
+def test_scan_keeps_the_tokens_before_a_value_that_is_not_finite(value, dtype, T, V, K, lens,
+                                                                 segment, at, out):
+    """x of one token and state row reaches that row's outputs from the token on, and no other.
+    The others are the same arithmetic: the same bits."""
+    if dtype == F32 and out == BF16:
+        out = None
+    d = cuda(ssm_inputs(31, 1, T, 2, 1, V, K, dtype, lens))
+    kw = dict(segment_tokens=segment, out_dtype=out)
+    y, ht = scan(d, **kw)
+    bad = {**d, "x": d["x"].clone()}
+    clean = torch.ones((1, T, 2, V), dtype=torch.bool, device="cuda")
+    kept = torch.ones(ht.shape, dtype=torch.bool, device="cuda")
+    ends = [0, T] if lens is None else [0, lens[0], lens[0] + lens[1], T]
+    for t, h, v in at:
+        bad["x"][0, t, h, v] = value
+        n = next(n for n in range(len(ends) - 1) if ends[n] <= t < ends[n + 1])
+        clean[0, t:ends[n + 1], h, v] = False
+        kept[n, h, v] = False
+    y2, ht2 = scan(bad, **kw)
+    ok()
+    assert torch.equal(y2[clean], y[clean])
+    assert not y2[~clean].isfinite().any()
+    assert torch.equal(ht2[kept], ht[kept])
+    assert not ht2[~kept].isfinite().any()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("name", ["Bm", "Cm", "z"])
+def test_scan_keeps_the_tokens_before_nan_in_the_other_inputs(dtype, name):
+    d = cuda(ssm_inputs(32, 1, 300, 2, 1, 64, 128, dtype))
+    y, _ = scan(d)
+    for t in (0, 77, 130, 299):
+        bad = {**d, name: d[name].clone()}
+        bad[name][:, t] = float("nan")
+        y2, _ = scan(bad)
+        ok()
+        assert torch.equal(y2[:, :t], y[:, :t]), t
+        if name != "Bm":  # B lives on in the state, C and z only in their own token
+            assert torch.equal(y2[:, t + 1:], y[:, t + 1:]), t
+        assert y2[:, t].isnan().all(), t
