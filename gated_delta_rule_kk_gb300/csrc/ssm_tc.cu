@@ -620,7 +620,7 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
       if (it > 0) wait(&bar.dh_full, it - 1);  // the product before has read W
       if (j < n) {
         const float ww[2] = {w, w};
-        // NaNs once an x of the row is not finite: its last piece is NaN
+        // NaNs once an element of the row is not finite: its last piece is NaN
         __nv_bfloat162 odd = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll 1
         for (int c = 0; c < 8; ++c) {
@@ -647,12 +647,16 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
           *reinterpret_cast<uint4 *>(img + 2 * ST_TILE + swz(j, c)) =
               make_uint4(e[0], e[1], e[2], e[3]);
         }
-        if (!STATES && !__hbeq2(odd, odd)) {
+        if (!__hbeq2(odd, odd)) {
 #pragma unroll 1
           for (int c = 0; c < ST_VT; ++c) {
-            uint16_t *x = reinterpret_cast<uint16_t *>(xt + swz(j, c / 8)) + c % 8;
-            if ((*x & 0x7f80) != 0x7f80) continue;
-            *x = 0;
+            const uint32_t at = swz(j, c / 8) + 2 * (c % 8);
+            auto half = [&](unsigned char *tile) { return reinterpret_cast<uint16_t *>(tile + at); };
+            auto finite = [](const uint16_t *v) { return (*v & 0x7f80) != 0x7f80; };
+            // an infinite first piece is the whole value: Inf - Inf left no others
+            if (!finite(half(img))) *half(img + ST_TILE) = *half(img + 2 * ST_TILE) = 0;
+            if (STATES || finite(half(xt))) continue;
+            *half(xt) = 0;
             atomicMin(&bad.first[c], it * ST_Q + j);
             atomicMin(&bad.any, it * ST_Q + j);
           }

@@ -1,9 +1,11 @@
 """Edges of the short convolution and the state space scan on the GPU."""
+import numpy as np
 import pytest
 import torch
 
 import gated_delta_rule_kk_gb300 as gdn
 from gated_delta_rule_kk_gb300 import Status
+from oracle import mixer as M
 
 from _mixer import cuda, ssm_inputs
 
@@ -70,3 +72,26 @@ def test_scan_keeps_the_tokens_before_nan_in_the_other_inputs(dtype, name):
         if name != "Bm":  # B lives on in the state, C and z only in their own token
             assert torch.equal(y2[:, t + 1:], y[:, t + 1:]), t
         assert y2[:, t].isnan().all(), t
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("segment", [0, 128])
+def test_scan_states_keep_an_infinite_value(dtype, segment):
+    """An infinite x leaves infinities of B's signs in its row of the state, two of opposite
+    signs NaN, as the recurrence does (few enough tokens after it that no decay is zero)."""
+    i = ssm_inputs(33, 1, 300, 2, 1, 64, 128, dtype)
+    i["x"] = i["x"].clone()
+    i["x"][0, 290, 0, 7] = i["x"][0, 280, 1, 63] = i["x"][0, 299, 1, 0] = float("inf")
+    i["x"][0, 288, 1, 20] = float("-inf")
+    i["x"][0, 285, 0, 50], i["x"][0, 295, 0, 50] = float("inf"), float("-inf")
+    _, ht = scan(cuda(i), segment_tokens=segment)
+    ok()
+    with np.errstate(invalid="ignore"):
+        _, ref = M.ssm_scan(i["x"], i["dt"], i["A_log"], i["Bm"], i["Cm"], i["D"], i["z"],
+                            i["dt_bias"], h0=i["h0"])
+    ref = torch.from_numpy(ref)
+    there = ~ref.isfinite()
+    assert there.sum() >= 4 * 128 and ref[there].isinf().any() and ref[there].isnan().any()
+    got = ht.cpu().double()
+    assert torch.equal(got.isfinite(), ~there)
+    assert torch.equal(got[there].nan_to_num(0.5, 1, -1), ref[there].nan_to_num(0.5, 1, -1))
