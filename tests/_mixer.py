@@ -2,6 +2,8 @@
 import numpy as np
 import torch
 
+from oracle import mixer
+
 from _util import RECORDS, CURRENT_TEST, _np
 
 
@@ -77,3 +79,51 @@ def cuda(d):
         else:
             out[k] = v.cuda() if isinstance(v, torch.Tensor) else v
     return out
+
+
+def scan_rooms(i, pieces=2):
+    """What y may be off by where the scan runs on the tensor cores, element for element.
+
+    A 128-token chunk from state h is y = e^G (C h) + M x with M and h in two bfloat16 pieces,
+    each to 2^-8 of what it is taken from: at most 2^-16 of |M| |x| + e^G |C| |h| (2^-8 with one).
+    M's own sums over K, the products' (16 terms at a time, some 20 partial sums of float32) and
+    the decays' exponentials: 2^-18 of the same with the magnitudes taken inside M and h."""
+    x, Bm, Cm, dt = (_np(i[k]) for k in ("x", "Bm", "Cm", "dt"))
+    H, V = x.shape[2:]
+    head = np.arange(H) // (H // Bm.shape[2])
+    a, bias = -np.exp(_np(i["A_log"])), _np(i["dt_bias"])
+    step = mixer.softplus(dt + bias)
+    skip = np.zeros(H) if i["D"] is None else _np(i["D"])
+    room = np.zeros_like(x)
+    for n, (b, lo, hi) in enumerate(mixer.bounds(x.shape[0], x.shape[1], i["cu"])):
+        h = np.zeros((H, V, Bm.shape[3])) if i["h0"] is None else _np(i["h0"])[n]
+        most = np.abs(h)  # h's magnitudes, summed without cancelling
+        for t in range(lo, hi, 128):
+            e = min(t + 128, hi)
+            s, xc = step[b, t:e].T, x[b, t:e].transpose(1, 0, 2)  # heads first
+            G = np.cumsum(a[:, None] * s, 1)
+            low = np.tril(np.ones((e - t, e - t), bool))
+            L = np.exp(np.where(low, G[:, :, None] - G[:, None, :], -np.inf)) * s[:, None, :]
+            B, C = (v[b, t:e].transpose(1, 0, 2)[head] for v in (Bm, Cm))
+            eye = skip[:, None, None] * np.eye(e - t)
+            M, most_M = C @ B.transpose(0, 2, 1) * L + eye, \
+                np.abs(C) @ np.abs(B).transpose(0, 2, 1) * L + np.abs(eye)
+            eG = np.exp(G)[:, :, None]
+            near = np.abs(M) @ np.abs(xc) + eG * (np.abs(C) @ np.abs(h).transpose(0, 2, 1))
+            sums = most_M @ np.abs(xc) + eG * (np.abs(C) @ most.transpose(0, 2, 1))
+            room[b, t:e] = (2.0 ** (-8 * pieces) * near + 2.0 ** -18 * sums).transpose(1, 0, 2)
+            W = (s * np.exp(G[:, -1:] - G))[:, :, None] * xc
+            end = np.exp(G[:, -1])[:, None, None]
+            h = end * h + W.transpose(0, 2, 1) @ B
+            most = end * most + np.abs(W).transpose(0, 2, 1) @ np.abs(B)
+    if i["z"] is not None:
+        z = _np(i["z"])
+        room *= np.abs(z * mixer.sigmoid(z))
+    return room
+
+
+def assert_inside(got, ref, room, what):
+    """|got - ref| <= room for every element."""
+    worst = float(np.max(np.abs(_np(got) - ref) / np.maximum(room, 1e-300)))
+    RECORDS.append((CURRENT_TEST[0], what, worst, worst, 1.0))
+    assert np.isfinite(worst) and worst <= 1.0, f"{what}: {worst:.2f} times the allowed error"

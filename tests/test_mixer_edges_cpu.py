@@ -4,10 +4,14 @@ import os
 import subprocess
 import sys
 
+import numpy as np
 import pytest
+import torch
 
 from gated_delta_rule_kk_gb300 import _lib, build_lib
+from oracle import mixer as M
 
+from _mixer import scan_rooms, ssm_inputs
 from test_mixer_cpu import FAKE
 
 TESTS = os.path.dirname(os.path.abspath(__file__))
@@ -60,3 +64,48 @@ if not torch.cuda.is_available():
     a = conv_args(dtype={dtype}, weight_dtype={dtype}, T=0, ht=FAKE)
     assert lib.short_conv_fwd(ctypes.byref(a), None) == Status.CUDA
 """)
+
+
+def pieces(v, n):
+    """The sum of v's first n bfloat16 pieces, each the nearest to what is left."""
+    v = torch.from_numpy(np.asarray(v))
+    total = torch.zeros_like(v)
+    for _ in range(n):
+        total = total + (v - total).to(torch.bfloat16).double()
+    return total.numpy()
+
+
+def chunked_scan(i, of_m, of_h):
+    """y in 128-token chunks with M and h in so many bfloat16 pieces, all else exact."""
+    x, Bm, Cm, dt, A_log, bias, D, z, h0 = (
+        None if i[k] is None else i[k].double().numpy()
+        for k in ("x", "Bm", "Cm", "dt", "A_log", "dt_bias", "D", "z", "h0"))
+    H = x.shape[2]
+    head = np.arange(H) // (H // Bm.shape[2])
+    s = M.softplus(dt + bias)
+    y = np.zeros_like(x)
+    for n, (b, lo, hi) in enumerate(M.bounds(x.shape[0], x.shape[1], i["cu"])):
+        h = h0[n].copy()
+        for t in range(lo, hi, 128):
+            e = min(t + 128, hi)
+            for k in range(H):
+                G = np.cumsum(-np.exp(A_log[k]) * s[b, t:e, k])
+                L = np.tril(np.exp(np.minimum(G[:, None] - G[None], 0)))
+                B, C, X = Bm[b, t:e, head[k]], Cm[b, t:e, head[k]], x[b, t:e, k]
+                m = C @ B.T * L * s[b, t:e, k] + D[k] * np.eye(e - t)
+                y[b, t:e, k] = np.exp(G)[:, None] * (C @ pieces(h[k], of_h).T) + pieces(m, of_m) @ X
+                w = (s[b, t:e, k] * np.exp(G[-1] - G))[:, None] * X
+                h[k] = np.exp(G[-1]) * h[k] + w.T @ B
+    return y * z * M.sigmoid(z)
+
+
+@pytest.mark.parametrize("T,lens", [(1, None), (129, None), (300, [0, 1, 130, 0, 41, 128, 0])])
+def test_the_scan_bound_sees_a_lost_piece(T, lens):
+    """What y may be off by on the tensor cores (test_mixer_edges_gpu.py) holds for two pieces of
+    M and h, and for neither of them with one."""
+    i = ssm_inputs(41, 1, T, 2, 1, 64, 128, torch.bfloat16, lens)
+    ref, _ = M.ssm_scan(i["x"], i["dt"], i["A_log"], i["Bm"], i["Cm"], i["D"], i["z"], i["dt_bias"],
+                        h0=i["h0"], cu_seqlens=i["cu"])
+    room = scan_rooms(i)
+    worst = {k: np.max(np.abs(chunked_scan(i, *k) - ref) / room) for k in ((2, 2), (1, 2), (2, 1))}
+    assert worst[2, 2] < 1 < min(worst[1, 2], worst[2, 1]), worst

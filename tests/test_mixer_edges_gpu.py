@@ -7,7 +7,8 @@ import gated_delta_rule_kk_gb300 as gdn
 from gated_delta_rule_kk_gb300 import Status
 from oracle import mixer as M
 
-from _mixer import cuda, ssm_inputs
+from _mixer import assert_inside, cuda, scan_rooms, ssm_inputs
+from _util import TOL_F32, assert_close
 
 pytestmark = pytest.mark.gpu
 
@@ -95,3 +96,36 @@ def test_scan_states_keep_an_infinite_value(dtype, segment):
     got = ht.cpu().double()
     assert torch.equal(got.isfinite(), ~there)
     assert torch.equal(got[there].nan_to_num(0.5, 1, -1), ref[there].nan_to_num(0.5, 1, -1))
+
+
+def check_inside(i, **kw):
+    """y of the tensor cores within what their roundings allow, element for element, and the
+    states within the float32 bound."""
+    y, ht = scan(cuda(i), out_dtype=F32, **kw)
+    ok()
+    ref, rht = M.ssm_scan(i["x"], i["dt"], i["A_log"], i["Bm"], i["Cm"], i["D"], i["z"],
+                          i["dt_bias"], h0=i["h0"], cu_seqlens=i["cu"])
+    assert_inside(y, ref, scan_rooms(i), "y")
+    assert_close(ht, rht, TOL_F32, "ht")
+
+
+@pytest.mark.parametrize("B,T,H,Hg,V,K,lens,segment", [
+    (1, 1, 2, 1, 64, 128, None, 0),
+    (2, 63, 4, 2, 64, 128, None, 0),
+    (1, 128, 2, 2, 64, 64, None, 0),
+    (1, 129, 3, 1, 64, 128, None, 0),
+    (2, 257, 2, 1, 128, 128, None, 0),
+    (1, 300, 4, 2, 64, 128, [0, 1, 130, 0, 41, 128, 0], 0),
+    (1, 200, 3, 3, 40, 48, [77, 123], 0),
+    (1, 1000, 2, 1, 64, 128, None, 128),
+    (1, 1000, 2, 1, 64, 128, [700, 0, 1, 128, 171], 384),
+])
+def test_scan_within_its_roundings(B, T, H, Hg, V, K, lens, segment):
+    check_inside(ssm_inputs(T + K + 1, B, T, H, Hg, V, K, BF16, lens), segment_tokens=segment)
+
+
+@pytest.mark.parametrize("fast", [False, True])
+def test_scan_within_its_roundings_bare_and_with_strong_decays(fast):
+    check_inside(ssm_inputs(42, 1, 400, 4, 1, 64, 128, BF16, fast=fast))
+    check_inside(ssm_inputs(43, 2, 200, 2, 1, 64, 128, BF16, h0=False, z=False, skip=False,
+                            fast=fast))
