@@ -40,10 +40,13 @@
 // waited for y's store) keep the output out of that chain.
 // The decays: every 32-token block b keeps f_j = s_j e^(block end - G_j) and the
 // sums inside the block, so that e^(G_i - G_j) s_j is a product of f_j and one
-// factor per row and block, all exponents sums of negative terms between j and
-// i (no difference of long sums), and only the block on the diagonal, where the
-// row's factor could overflow, takes an exponential per element when its decay
-// is below e^-60.
+// factor per row and block, all exponents sums of the terms between j and i.  Only on
+// the diagonal does the row's factor take what f_j has past i off again: a difference
+// of sums of at most 80, of which some 1e-5 is lost at worst.  Where a block decays by
+// more, so that the factor could overflow, its elements take an exponential each, of
+// sums in fixed point: differences of float32 sums of 1e5 (one token that resets the
+// state) had y off by a percent.  (80 or 60 as the limit, us: 98 / 105, 283 / 317 for
+// eight packed prompts: the heads of the strongest decays set the pace.)
 //
 // Every wait is bounded: a role whose wait runs out issues nothing more and ends
 // after its step, GDN_ERR_TIMEOUT is recorded, the copies and products that are on
@@ -346,7 +349,7 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
       const int n = tokens_of(it);
       wait(&bar.sc_full[it & 1], it >> 1);
       const float pin = s.pin[i], own = s.tb[w4];
-      const bool direct = !(fabsf(own) <= 60.f);
+      const bool direct = !(fabsf(own) <= 80.f);
       wait(&bar.s_full[it & 1], it >> 1);
       ptx::tc_fence_after();
       // blocks from the diagonal back; `between` sums the log-decays from the
@@ -373,9 +376,18 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
               i < n ? ssm_step(p, q.b * p.dtb + (int64_t)(q.lo + it * ST_Q + i) * p.dts, h,
                                p.dt_bias ? p.dt_bias[h] : 0.f)
                     : 0.f;
+          // log-decays up to row i, each rounded to 2^-19, so that their differences are
+          // exact; e^-104 is zero in float32, and 32 of it stay below 2^31
+          int sum = __float2int_rn(fmaxf(-expf(p.A_log[h]) * step, -104.f) * 524288.f);
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(~0u, sum, o);
+            if (lane >= o) sum += u;
+          }
 #pragma unroll
           for (int j = 0; j < 16; ++j)
-            v[j] = __expf(pin - __shfl_sync(~0u, pin, c + j)) * __shfl_sync(~0u, step, c + j);
+            v[j] = __expf((float)(sum - __shfl_sync(~0u, sum, c + j)) * 0x1p-19f) *
+                   __shfl_sync(~0u, step, c + j);
         }
         tmem_wait_ld();
         pin_regs<16>(r);

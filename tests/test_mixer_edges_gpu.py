@@ -129,3 +129,13 @@ def test_scan_within_its_roundings_bare_and_with_strong_decays(fast):
     check_inside(ssm_inputs(42, 1, 400, 4, 1, 64, 128, BF16, fast=fast))
     check_inside(ssm_inputs(43, 2, 200, 2, 1, 64, 128, BF16, h0=False, z=False, skip=False,
                             fast=fast))
+
+
+@pytest.mark.parametrize("resets", [[40], [0, 31, 32], [100, 101, 110, 250]])
+def test_scan_after_a_token_that_resets_the_state(resets):
+    """A step size of 6e4 (log-decays of down to -1e6) in one token: the tokens after it in its
+    block differ by decays near one, which no difference of such sums gives."""
+    i = ssm_inputs(44, 1, 300, 4, 2, 64, 128, BF16)
+    i["dt"] = i["dt"].clone()
+    i["dt"][:, resets] = 6e4
+    check_inside(i)
