@@ -64,6 +64,17 @@ struct SdItem {
   int v, end;  // rows v .. end - 1
 };
 
+// The log-decays after token r up to token t, from the tokens' own: no difference of
+// running sums, of which little is left after a token that resets the state.
+template <int TM>
+__device__ __forceinline__ float decay_between(const float (&g)[TM], int r, int t) {
+  float sum = 0.f;
+#pragma unroll
+  for (int q = 1; q < TM; ++q)
+    if (q > r && q <= t) sum = __fadd_rn(sum, g[q]);
+  return sum;
+}
+
 // What a thread needs of an item's tokens, asked for before the item's state is
 // waited for.  Raw bits, so that nothing waits for them either; B and C of one
 // token (of more they are read where they are used).
@@ -228,14 +239,15 @@ struct SdRows {
           raw[j][q].zero();
       }
     const float a = -expf(tok.A_log);
-    float step[TM], G[TM], total = 0.f;
+    float step[TM], g[TM], G[TM], total = 0.f;
 #pragma unroll
     for (int t = 0; t < TM; ++t) {
-      step[t] = 0.f;
+      step[t] = g[t] = 0.f;
       if (t < p.T) {
         const float dt = __uint_as_float(p.dt_f32 ? tok.dt[t] : tok.dt[t] << 16);
         step[t] = ssm_softplus(p, __fadd_rn(dt, tok.bias));
-        total = __fadd_rn(total, __fmul_rn(a, step[t]));
+        g[t] = __fmul_rn(a, step[t]);
+        total = __fadd_rn(total, g[t]);
       }
       G[t] = total;
     }
@@ -288,7 +300,7 @@ struct SdRows {
       float y = expf(G[t]) * sum[0];
 #pragma unroll
       for (int r = 0; r <= t; ++r)
-        y = fmaf(expf(G[t] - G[r]) * dots[r], step[r] * value(tok.xown[r]), y);
+        y = fmaf(expf(decay_between(g, r, t)) * dots[r], step[r] * value(tok.xown[r]), y);
       if (p.D) y = fmaf(tok.skip, value(tok.xown[t]), y);
       if (p.z) y *= silu(value(tok.zown[t]));
       put(t, y);
@@ -296,7 +308,7 @@ struct SdRows {
     const float keep = expf(total);
     float e[TM];
 #pragma unroll
-    for (int t = 0; t < TM; ++t) e[t] = expf(total - G[t]);
+    for (int t = 0; t < TM; ++t) e[t] = expf(decay_between(g, t, TM - 1));
 #pragma unroll
     for (int q = 0; q < PP; ++q) {
       float bv[TM][VEC];
@@ -390,7 +402,7 @@ struct SdCoef {
 template <int TM>
 __device__ __forceinline__ void ssm_decode_prepare(const SsmDecodeParams &p, const SdItem &it,
                                                    float *f) {
-  const int lane = threadIdx.x & 31, g = it.h / (p.H / p.Hg);
+  const int lane = threadIdx.x & 31, group = it.h / (p.H / p.Hg);
   const SdCoef c(p.K, p.rows, p.T);
   auto token = [&](const void *base, int64_t at) {
     return p.tok_f32 ? static_cast<const float *>(base)[at]
@@ -398,17 +410,18 @@ __device__ __forceinline__ void ssm_decode_prepare(const SsmDecodeParams &p, con
   };
   const int64_t xat = it.b * p.xb + (int64_t)it.h * p.V + it.v;
   const int64_t zat = it.b * p.zb + (int64_t)it.h * p.V + it.v;
-  const int64_t bat = it.b * p.bb + (int64_t)g * p.K, cat = it.b * p.cb + (int64_t)g * p.K;
+  const int64_t bat = it.b * p.bb + (int64_t)group * p.K, cat = it.b * p.cb + (int64_t)group * p.K;
   const float a = -expf(p.A_log[it.h]), bias = p.dt_bias ? p.dt_bias[it.h] : 0.f;
   const float D = p.D ? p.D[it.h] : 0.f;
-  float step[TM], G[TM], total = 0.f;
+  float step[TM], g[TM], G[TM], total = 0.f;
 #pragma unroll
   for (int t = 0; t < TM; ++t) {
-    step[t] = 0.f;
+    step[t] = g[t] = 0.f;
     if (t < p.T) {
       step[t] = ssm_softplus(
           p, __fadd_rn(ssm_dt(p, it.b * p.dtb + t * p.dts + it.h), bias));
-      total = __fadd_rn(total, __fmul_rn(a, step[t]));
+      g[t] = __fmul_rn(a, step[t]);
+      total = __fadd_rn(total, g[t]);
     }
     G[t] = total;
   }
@@ -438,7 +451,7 @@ __device__ __forceinline__ void ssm_decode_prepare(const SsmDecodeParams &p, con
       const float z = p.z ? token(p.z, zat + t * p.zs + r) : 0.f;
       const float u = __fmul_rn(x, step[t]);
       f[c.u(t) + r] = u;
-      f[c.w(t) + r] = __fmul_rn(u, expf(total - G[t]));
+      f[c.w(t) + r] = __fmul_rn(u, expf(decay_between(g, t, TM - 1)));
       f[c.skip(t) + r] = D * x;
       f[c.gate(t) + r] = p.z ? silu(z) : 1.f;
     }
@@ -449,7 +462,7 @@ __device__ __forceinline__ void ssm_decode_prepare(const SsmDecodeParams &p, con
     for (int r = 0; r <= t; ++r) {
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) dots[t][r] += __shfl_xor_sync(~0u, dots[t][r], o);
-      if (lane == 0 && t < p.T) f[c.mix(t, r)] = expf(G[t] - G[r]) * dots[t][r];
+      if (lane == 0 && t < p.T) f[c.mix(t, r)] = expf(decay_between(g, r, t)) * dots[t][r];
     }
   if (lane == 0) {
 #pragma unroll

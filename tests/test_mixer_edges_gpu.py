@@ -139,3 +139,21 @@ def test_scan_after_a_token_that_resets_the_state(resets):
     i["dt"] = i["dt"].clone()
     i["dt"][:, resets] = 6e4
     check_inside(i)
+
+
+@pytest.mark.parametrize("T,resets", [(2, [0]), (3, [1]), (4, [0, 2]), (4, [3])])
+@pytest.mark.parametrize("B,H", [(2, 4), (60, 32)])  # straight from memory, and through the ring
+def test_scan_tokens_after_one_that_resets_the_state(T, resets, B, H):
+    """As above, among the tokens of one call."""
+    i = ssm_inputs(45, B, T, H, 1, 64, 128, BF16)
+    i["dt"] = i["dt"].clone()
+    i["dt"][:, resets] = 6e4
+    d = cuda(i)
+    state = d["h0"].clone()
+    y = gdn.ssm_decode(d["x"], d["dt"], d["A_log"], d["Bm"], d["Cm"], state, D=d["D"], z=d["z"],
+                       dt_bias=d["dt_bias"], out_dtype=F32)
+    ok()
+    ref, rht = M.ssm_scan(i["x"], i["dt"], i["A_log"], i["Bm"], i["Cm"], i["D"], i["z"],
+                          i["dt_bias"], h0=i["h0"])
+    assert_close(y, ref, TOL_F32, "y")
+    assert_close(state, rht, TOL_F32, "state")
