@@ -771,18 +771,20 @@ gdn_status_t check_ssm(const Args &a) {
   return GDN_OK;
 }
 
-// Copies what both forms' parameters share.
+// Copies what both forms' parameters share.  A stride that no second token or batch row
+// uses may be anything (a tensor map takes none of 2^40 bytes): dense rows instead, 0.
 template <typename P, typename Args>
 void set_tokens(P &p, const Args &a) {
   p.x = a.x; p.z = a.z; p.Bm = a.Bm; p.Cm = a.Cm; p.dt = a.dt;
   p.A_log = a.A_log; p.D = a.D; p.dt_bias = a.dt_bias; p.y = a.y;
-  const bool many = a.B > 1;
-  p.xs = a.x_stride; p.xb = many ? a.x_batch_stride : 0;
-  p.zs = a.z_stride; p.zb = many ? a.z_batch_stride : 0;
-  p.bs = a.Bm_stride; p.bb = many ? a.Bm_batch_stride : 0;
-  p.cs = a.Cm_stride; p.cb = many ? a.Cm_batch_stride : 0;
-  p.dts = a.dt_stride; p.dtb = many ? a.dt_batch_stride : 0;
-  p.ys = a.y_stride; p.yb = many ? a.y_batch_stride : 0;
+  const bool many = a.B > 1, tokens = a.T > 1;
+  const int64_t hv = (int64_t)a.H * a.V, gk = (int64_t)a.Hg * a.K;
+  p.xs = tokens ? a.x_stride : hv; p.xb = many ? a.x_batch_stride : 0;
+  p.zs = tokens ? a.z_stride : hv; p.zb = many ? a.z_batch_stride : 0;
+  p.bs = tokens ? a.Bm_stride : gk; p.bb = many ? a.Bm_batch_stride : 0;
+  p.cs = tokens ? a.Cm_stride : gk; p.cb = many ? a.Cm_batch_stride : 0;
+  p.dts = tokens ? a.dt_stride : a.H; p.dtb = many ? a.dt_batch_stride : 0;
+  p.ys = tokens ? a.y_stride : hv; p.yb = many ? a.y_batch_stride : 0;
   p.B = a.B; p.T = a.T; p.H = a.H; p.Hg = a.Hg; p.K = a.K; p.V = a.V;
   p.dt_f32 = a.dt_dtype == GDN_F32;
   p.softplus = a.dt_softplus;

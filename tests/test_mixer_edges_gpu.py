@@ -7,7 +7,7 @@ import gated_delta_rule_kk_gb300 as gdn
 from gated_delta_rule_kk_gb300 import Status
 from oracle import mixer as M
 
-from _mixer import assert_inside, cuda, scan_rooms, ssm_inputs
+from _mixer import assert_inside, conv_inputs, cuda, scan_rooms, ssm_inputs
 from _util import TOL_F32, assert_close
 
 pytestmark = pytest.mark.gpu
@@ -157,3 +157,51 @@ def test_scan_tokens_after_one_that_resets_the_state(T, resets, B, H):
                           i["dt_bias"], h0=i["h0"])
     assert_close(y, ref, TOL_F32, "y")
     assert_close(state, rht, TOL_F32, "state")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_scan_of_single_tokens_with_any_stride_between_them(dtype):
+    """The stride over one token, or one batch row, is never used: 2^41 elements here."""
+    d = cuda(ssm_inputs(46, 2, 1, 4, 1, 64, 128, dtype))
+    y, ht = scan(d)
+
+    def wide(t):
+        s = list(t.stride())
+        s[1] = 2 ** 41 + 8
+        return t.as_strided(t.shape, s)
+
+    y2, ht2 = scan({**d, **{k: wide(d[k]) for k in ("x", "Bm", "Cm", "z", "dt")}}, out=wide(
+        torch.empty_like(y)))
+    ok()
+    assert torch.equal(y2, y) and torch.equal(ht2, ht)
+    one = {k: v[:1] if k in ("x", "Bm", "Cm", "z", "dt", "h0") else v for k, v in d.items()}
+    far = {k: v.as_strided(v.shape, (2 ** 42, *v.stride()[1:]))
+           if k in ("x", "Bm", "Cm", "z", "dt") else v for k, v in one.items()}
+    y3, ht3 = scan(far)
+    ok()
+    assert torch.equal(y3, y[:1]) and torch.equal(ht3, ht[:1])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_inputs_shared_by_a_batch(dtype):
+    """Rows of a batch that are one row expanded (a batch stride of zero)."""
+    d = cuda(ssm_inputs(47, 1, 300, 2, 1, 64, 128, dtype))
+    both = {k: v.expand(3, *v.shape[1:]) if k in ("x", "Bm", "Cm", "z", "dt") else v
+            for k, v in d.items()}
+    y, ht = scan(d)
+    y2, ht2 = scan({**both, "h0": d["h0"].repeat(3, 1, 1, 1)})
+    ok()
+    assert all(torch.equal(y2[b], y[0]) and torch.equal(ht2[b], ht[0]) for b in range(3))
+    for T, D in ((40, 72), (4000, 2056)):  # from memory, and through the ring
+        c = cuda(conv_inputs(48, 1, T, D, 4, dtype))
+        y, ht = gdn.short_conv_fwd(c["x"], c["weight"], c["bias"], c["h0"])
+        y2, ht2 = gdn.short_conv_fwd(c["x"].expand(3, T, D), c["weight"], c["bias"],
+                                     c["h0"].repeat(3, 1, 1))
+        ok()
+        assert all(torch.equal(y2[b], y[0]) and torch.equal(ht2[b], ht[0]) for b in range(3))
+        g = gdn.short_conv_bwd(c["dy"], c["x"], c["weight"], c["bias"], c["h0"])
+        g2 = gdn.short_conv_bwd(c["dy"].expand(3, T, D), c["x"].expand(3, T, D), c["weight"],
+                                c["bias"], c["h0"].repeat(3, 1, 1))
+        ok()
+        assert all(torch.equal(g2[0][b], g[0][0]) and torch.equal(g2[3][b], g[3][0])
+                   for b in range(3))
