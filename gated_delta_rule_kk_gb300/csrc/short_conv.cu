@@ -20,13 +20,11 @@
 #include <initializer_list>
 #include <type_traits>
 
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include "abi_check.h"
 #include "gdn_common.cuh"
 #include "ptx.cuh"
 #include "rows.cuh"
+#include "tensor_map.h"
 
 namespace gdn {
 namespace {
@@ -808,23 +806,10 @@ cudaError_t with_types(int32_t dtype, int W, F &&f) {
   return dtype == GDN_BF16 ? taps(__nv_bfloat16()) : taps(0.f);
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (!fn) {
-    void *ptr = nullptr;
-    cudaDriverEntryPointQueryResult r;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
-                                         &r) == cudaSuccess &&
-        r == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  }
-  return fn;
-}
-
 // [batch][token][channel], boxes of CR_BOX channels and a stage's tokens.
 bool conv_map(CUtensorMap *m, const void *base, int elt, const ConvSeqs &q, int D, int64_t stride,
               int64_t batch_stride) {
-  const auto fn = map_encoder();
+  const auto fn = tensor_map_encoder();
   if (!fn) return false;
   const cuuint64_t gdim[3] = {(cuuint64_t)D, (cuuint64_t)q.T, (cuuint64_t)q.B};
   const cuuint64_t gstride[2] = {(cuuint64_t)stride * elt,

@@ -51,12 +51,10 @@
 // Every wait is bounded: a role whose wait runs out issues nothing more and ends
 // after its step, GDN_ERR_TIMEOUT is recorded, the copies and products that are on
 // their way are waited for and the block returns.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include "ptx.cuh"
 #include "rows.cuh"
 #include "ssm_items.cuh"
+#include "tensor_map.h"
 
 namespace gdn {
 namespace {
@@ -920,24 +918,11 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
   if (warp == 0) ptx::tmem_dealloc<512>(tmem);
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (!fn) {
-    void *ptr = nullptr;
-    cudaDriverEntryPointQueryResult r;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
-                                         &r) == cudaSuccess &&
-        r == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  }
-  return fn;
-}
-
 // [batch][token][heads][dim] bf16 with strides between tokens and batch rows;
 // boxes of 64 columns of one head over 128 tokens in 128-byte swizzled rows.
 bool token_map(CUtensorMap *m, const void *base, int dim, int heads, int T, int B, int64_t stride,
                int64_t batch_stride) {
-  const auto fn = encoder();
+  const auto fn = tensor_map_encoder();
   if (!fn) return false;
   const cuuint64_t gdim[4] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)T, (cuuint64_t)B};
   const cuuint64_t gstride[3] = {(cuuint64_t)dim * 2, (cuuint64_t)stride * 2,

@@ -1,4 +1,6 @@
 """Edges of the short convolution and the state space scan on the GPU."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -205,3 +207,30 @@ def test_inputs_shared_by_a_batch(dtype):
         ok()
         assert all(torch.equal(g2[0][b], g[0][0]) and torch.equal(g2[3][b], g[3][0])
                    for b in range(3))
+
+
+def test_calls_from_several_threads():
+    """Each on a stream of its own, all at once, the first calls among them."""
+    c, d = cuda(conv_inputs(49, 1, 4000, 2056, 4, BF16)), cuda(ssm_inputs(49, 1, 400, 2, 1, 64, 128,
+                                                                          BF16))
+    start, results = threading.Barrier(6), [None] * 6
+    torch.cuda.synchronize()
+
+    def work(k):
+        stream = torch.cuda.Stream()
+        start.wait()
+        out = [*gdn.short_conv_fwd(c["x"], c["weight"], c["bias"], c["h0"], stream=stream),
+               *scan(d, segment_tokens=128, stream=stream)]
+        stream.synchronize()
+        results[k] = out
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(6)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    ok()
+    want = [*gdn.short_conv_fwd(c["x"], c["weight"], c["bias"], c["h0"]),
+            *scan(d, segment_tokens=128)]
+    for out in results:
+        assert out is not None and all(torch.equal(a, b) for a, b in zip(out, want))
