@@ -8,24 +8,31 @@ between an input projection, the convolution and the scan.  Outputs belong to
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
 
 from . import _lib
 from ._lib import ShortConvArgs, ShortConvBwdArgs, ShortConvDecodeArgs, SsmChunkArgs, SsmDecodeArgs
+
 _F32, _BF16 = torch.float32, torch.bfloat16
 _CODE = {_F32: 0, _BF16: 1}
 _ACTIVATIONS = {None: 0, "silu": 1}
 
 # A call for one token is a few microseconds on the GPU, so the checks below
 # read each tensor property once, and the stream's handle comes without a
-# Stream object around it where PyTorch offers that (0.1 us instead of 3).
+# Stream object around it where PyTorch offers that (0.1 us instead of 3), as
+# does the current device.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _stream_handle(stream, device):
     if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream must be one of {device}, where the tensors are, got one of "
+                             f"{stream.device}")
         return stream.cuda_stream
     if _raw_stream is not None:
         return _raw_stream(device.index)
@@ -118,8 +125,14 @@ def _activation(activation):
 
 
 def _call(name, args, stream, device):
-    lib = _lib._lib or _lib.load()
-    st = getattr(lib, name)(ctypes.byref(args), _stream_handle(stream, device))
+    """Call the library with the tensors' device current: it launches, counts SMs and
+    records errors there."""
+    fn, handle = getattr(_lib._lib or _lib.load(), name), _stream_handle(stream, device)
+    if _current_device() == device.index:
+        st = fn(ctypes.byref(args), handle)
+    else:
+        with torch.cuda.device(device):
+            st = fn(ctypes.byref(args), handle)
     if st:
         _lib.check(st, name)
 
@@ -201,14 +214,16 @@ def _workspace(args, size_fn, workspace, device, stream):
     caching allocator, which keeps it valid for the work enqueued on its stream,
     unless the caller passes one)."""
     n = ctypes.c_size_t(0)
-    st = getattr(_lib._lib or _lib.load(), size_fn)(ctypes.byref(args), ctypes.byref(n))
+    with contextlib.nullcontext() if _current_device() == device.index else torch.cuda.device(device):
+        st = getattr(_lib._lib or _lib.load(), size_fn)(ctypes.byref(args), ctypes.byref(n))
     if st:
         _lib.check(st, size_fn)
     if n.value == 0:
         return None
     if workspace is None:
         workspace = _empty(n.value, torch.uint8, device, stream)
-    elif workspace.device != device or not workspace.is_contiguous() or workspace.numel() * workspace.element_size() < n.value:
+    elif (workspace.device != device or not workspace.is_contiguous()
+          or workspace.numel() * workspace.element_size() < n.value):
         raise ValueError(f"workspace needs {n.value} bytes on {device}")
     args.workspace = workspace.data_ptr()
     args.workspace_bytes = workspace.numel() * workspace.element_size()

@@ -8,7 +8,8 @@ import numpy as np
 import pytest
 import torch
 
-from gated_delta_rule_kk_gb300 import _lib, build_lib
+from gated_delta_rule_kk_gb300 import _lib, api_ssm, build_lib
+from gated_delta_rule_kk_gb300._lib import ShortConvBwdArgs, SsmDecodeArgs
 from oracle import mixer as M
 
 from _mixer import scan_rooms, ssm_inputs
@@ -109,3 +110,56 @@ def test_the_scan_bound_sees_a_lost_piece(T, lens):
     room = scan_rooms(i)
     worst = {k: np.max(np.abs(chunked_scan(i, *k) - ref) / room) for k in ((2, 2), (1, 2), (2, 1))}
     assert worst[2, 2] < 1 < min(worst[1, 2], worst[2, 1]), worst
+
+
+class Devices:
+    """Two GPUs of which the first is current, and a library that notes where it was called."""
+
+    def __init__(self, monkeypatch):
+        self.current, self.calls = 0, []
+        devices = self
+
+        class Device:
+            def __init__(self, device):
+                self.to = torch.device(device).index
+
+            def __enter__(self):
+                self.back, devices.current = devices.current, self.to
+
+            def __exit__(self, *exc):
+                devices.current = self.back
+
+        class Library:
+            def __getattr__(self, name):
+                return lambda *args: devices.calls.append((name, devices.current, args)) or 0
+
+        monkeypatch.setattr(api_ssm, "_current_device", lambda: self.current, raising=False)
+        monkeypatch.setattr(torch.cuda, "device", Device)
+        monkeypatch.setattr(api_ssm, "_raw_stream", lambda index: 0x1000 + index)
+        monkeypatch.setattr(_lib, "_lib", Library())
+
+
+@pytest.mark.parametrize("index", [0, 1])
+def test_calls_run_on_the_device_of_their_tensors(monkeypatch, index):
+    """The library launches, counts SMs and records errors on the current device: it has to be
+    the tensors', whichever was current before."""
+    devices = Devices(monkeypatch)
+    device, args = torch.device("cuda", index), ShortConvBwdArgs()
+    api_ssm._call("short_conv_bwd", args, None, device)
+    assert api_ssm._workspace(args, "short_conv_bwd_workspace_size", None, device, None) is None
+    assert [c[:2] for c in devices.calls] == [("short_conv_bwd", index),
+                                              ("short_conv_bwd_workspace_size", index)]
+    assert devices.calls[0][2][1] == 0x1000 + index  # that device's stream
+    assert devices.current == 0
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    devices = Devices(monkeypatch)
+
+    class Stream:
+        device, cuda_stream = torch.device("cuda:0"), 7
+
+    api_ssm._call("ssm_decode", SsmDecodeArgs(), Stream(), torch.device("cuda:0"))
+    with pytest.raises(ValueError, match="stream"):
+        api_ssm._call("ssm_decode", SsmDecodeArgs(), Stream(), torch.device("cuda:1"))
+    assert len(devices.calls) == 1
