@@ -54,6 +54,9 @@ inline int sm_count() {
   return n;
 }
 
+// Tokens of a batch row: the kernels' indexes run up to 256 past the last one.
+constexpr int MAX_TOKENS = 0x7fffff00;
+
 #define CHECK_THAT(cond, st, ...)                       \
   do {                                                  \
     if (!(cond)) return ::gdn::failf(st, __VA_ARGS__);  \

@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(CV_MAX_THREADS, CV_BLOCKS) conv_fwd_kernel(Con
   }
   const int b = blockIdx.x / p.tiles;
   int t = (blockIdx.x % p.tiles) * p.run;
-  const int t1 = min(p.q.T, t + p.run);
+  const int t1 = t + min(p.run, p.q.T - t);
   if (!bounds_ok(b < p.q.B && t < t1, p.err)) return;
   const T *xr = x + b * p.xb;
   T *yr = static_cast<T *>(p.y) + b * p.yb + c;
@@ -251,8 +251,9 @@ __global__ void __launch_bounds__(32 * CB_RUNS, CB_BLOCKS) conv_bwd_kernel(ConvB
   }
   const int b = blockIdx.x / p.tiles;
   if (!bounds_ok(b < p.q.B, p.err)) return;
-  const int lo = ((blockIdx.x % p.tiles) * CB_RUNS + threadIdx.y) * p.run;
-  const int hi = min(p.q.T, lo + p.run);
+  // (a block's last runs may lie past the end: their products pass 31 bits)
+  const int lo = (int)min((int64_t)p.q.T, (int64_t)((blockIdx.x % p.tiles) * CB_RUNS + threadIdx.y) * p.run);
+  const int hi = lo + min(p.run, p.q.T - lo);
   if (live && lo < hi) {
     load_weights<VEC, W>(w, bias, p.weight, p.bias, p.w_f32, c);
     const T *xr = static_cast<const T *>(p.x) + b * p.xb + c;
@@ -463,7 +464,7 @@ conv_ring_kernel(const __grid_constant__ CUtensorMap tm_x,
     return;
   }
   const int b = blockIdx.x / p.runs, lo = blockIdx.x % p.runs * p.run;
-  const int hi = min(p.q.T, lo + p.run), stop = BWD ? min(p.q.T, hi + W - 1) : hi;
+  const int hi = lo + min(p.run, p.q.T - lo), stop = BWD ? min(p.q.T, hi + W - 1) : hi;
   if (!bounds_ok(b < p.q.B && lo < hi && c0 < p.D, p.err)) return;
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
@@ -845,7 +846,7 @@ RingShape ring_shape(int32_t dtype, int B, int T, int D, bool bwd,
   s.use = whole_pieces(D, 4, dtype, {out}, out_strides) &&
           whole_pieces(16, 16 / elt, dtype, in, in_strides) && run >= CR_LEAST;
   s.run = (int)run;
-  s.runs = s.use ? (T + s.run - 1) / s.run : 0;
+  s.runs = s.use ? (int)((T + run - 1) / run) : 0;
   return s;
 }
 
@@ -876,6 +877,7 @@ gdn_status_t check_conv(int32_t dtype, int32_t w_dtype, int B, int T, int D, int
   CHECK_THAT(B >= 1 && T >= 0 && D >= 1 && N >= 1, GDN_ERR_INVALID_ARG,
              "sizes must be positive (B=%d T=%d D=%d N=%d)", B, T, D, N);
   CHECK_THAT(W >= 2 && W <= 4, GDN_ERR_UNSUPPORTED, "W must be 2..4 (got %d)", W);
+  CHECK_THAT(T <= MAX_TOKENS, GDN_ERR_UNSUPPORTED, "T (%d) must be at most %d", T, MAX_TOKENS);
   CHECK_FLAG(silu, "silu");
   if (cu == nullptr) {
     CHECK_THAT(N == B, GDN_ERR_INVALID_ARG, "without cu_seqlens N (%d) must equal B (%d)", N, B);
@@ -923,7 +925,8 @@ BwdShape bwd_shape(const short_conv_bwd_args &a) {
   s.vec = whole ? wide : 1;
   s.run = run_tokens((int64_t)a.B * a.T, (a.D + s.vec - 1) / s.vec, 32 * CB_RUNS * CB_BLOCKS);
   if (s.run < 8) s.run = 8;
-  s.tiles = (a.T + s.run * CB_RUNS - 1) / (s.run * CB_RUNS);
+  const int64_t span = (int64_t)s.run * CB_RUNS;
+  s.tiles = (int)((a.T + span - 1) / span);
   s.blocks = (int64_t)a.B * s.tiles;
   return s;
 }
@@ -963,7 +966,7 @@ gdn_status_t short_conv_fwd(const short_conv_args *a, gdn_stream_t stream) {
   const bool whole = whole_pieces(a->D, wide, a->dtype, {a->x, a->y}, {p.xs, p.xb, p.ys, p.yb});
   const int64_t pieces = a->D / (whole ? wide : 1);
   p.run = run_tokens((int64_t)a->B * a->T, pieces, CV_MAX_THREADS * CV_BLOCKS);
-  p.tiles = (a->T + p.run - 1) / p.run;
+  p.tiles = (int)(((int64_t)a->T + p.run - 1) / p.run);
   const int block = even_block(pieces);
   const int64_t gx = (int64_t)a->B * p.tiles + (a->ht ? a->N : 0);
   if (gx == 0) return GDN_OK;

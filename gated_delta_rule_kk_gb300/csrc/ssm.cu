@@ -751,6 +751,7 @@ gdn_status_t check_ssm(const Args &a) {
   CHECK_THAT(a.H % a.Hg == 0, GDN_ERR_UNSUPPORTED, "H (%d) must be a multiple of Hg (%d)", a.H, a.Hg);
   CHECK_THAT(a.H <= MAX_GRID_YZ, GDN_ERR_UNSUPPORTED, "H (%d) must be at most %d", a.H, MAX_GRID_YZ);
   CHECK_THAT(a.K <= 256, GDN_ERR_UNSUPPORTED, "K=%d exceeds 256", a.K);
+  CHECK_THAT(a.T <= MAX_TOKENS, GDN_ERR_UNSUPPORTED, "T (%d) must be at most %d", a.T, MAX_TOKENS);
   CHECK_FLAG(a.dt_softplus, "dt_softplus");
   CHECK_FLAG(a.y_fp32, "y_fp32");
   if (a.T > 0) {
@@ -832,8 +833,8 @@ int choose_segment(const SsmParams &p, bool tc) {
   const double chains = (double)p.H * ((p.V + cols - 1) / cols);
   const double held = (tc ? 1 : 4) * sm_count();
   const double passes = tc ? 1.4 : 1.85, start = tc ? 400 : 64, state = tc ? 50 : 8;
-  const int longest = p.cu ? (int)std::min<int64_t>(p.T, (int64_t)p.T * 3 / (2 * p.N)) : p.T;
-  auto walked = [&](int seg, int pieces) {
+  const int64_t longest = p.cu ? std::min<int64_t>(p.T, (int64_t)p.T * 3 / (2 * p.N)) : p.T;
+  auto walked = [&](int64_t seg, int64_t pieces) {
     return p.cu ? std::max<double>(seg, p.T * chains / held + seg / 2)
                 : std::ceil(chains * p.N * pieces / held) * seg;
   };
@@ -843,21 +844,21 @@ int choose_segment(const SsmParams &p, bool tc) {
   int best = SSM_WHOLE;
   double least = walked(longest, 1) + start / 2;
   for (int n = 2; n <= 64; ++n) {
-    const int seg = ((longest + n - 1) / n + unit - 1) / unit * unit;
-    const int pieces = (longest + seg - 1) / seg;
+    const int64_t seg = ((longest + n - 1) / n + unit - 1) / unit * unit;
+    const int64_t pieces = (longest + seg - 1) / seg;
     if (pieces < 2) break;
     const double tokens = walked(seg, pieces), starts = tc ? tokens / seg : 1;
     const double cost = passes * tokens + starts * (start + state * pieces);
     if (cost < least) {
       least = cost;
-      best = seg;
+      best = (int)seg;
     }
   }
   return best;
 }
 
-SsmParams chunk_params(const ssm_chunk_args &a) {
-  SsmParams p{};
+// The kernels' parameters of a checked call, but for the workspace and the error word.
+gdn_status_t chunk_params(const ssm_chunk_args &a, SsmParams &p) {
   set_tokens(p, a);
   p.N = a.N;
   p.h0 = a.h0; p.ht = a.ht; p.cu = a.cu_seqlens;
@@ -865,8 +866,11 @@ SsmParams chunk_params(const ssm_chunk_args &a) {
                                : choose_segment(p, ssm_tc_supported(p, a.dtype == GDN_BF16));
   const int64_t longest = a.T;  // no sequence has more tokens
   const int64_t per = longest > p.seg ? (longest + p.seg - 1) / p.seg : 1;
-  p.items = (int)(a.cu_seqlens ? (a.N + (longest > p.seg ? longest / p.seg : 0)) : a.N * per);
-  return p;
+  const int64_t items = a.cu_seqlens ? (a.N + (longest > p.seg ? longest / p.seg : 0)) : a.N * per;
+  CHECK_THAT(items <= 0x7fffffff, GDN_ERR_UNSUPPORTED,
+             "%lld segments of %d tokens are too many for one call", (long long)items, p.seg);
+  p.items = (int)items;
+  return GDN_OK;
 }
 
 // Workspace: segment states, then their decays.  None if no sequence is cut.
@@ -888,7 +892,10 @@ gdn_status_t ssm_chunk_workspace_size(const ssm_chunk_args *a, size_t *bytes) {
   *bytes = 0;
   gdn_status_t st = check_chunk_args(*a);
   if (st != GDN_OK) return st;
-  *bytes = chunk_workspace(chunk_params(*a));
+  SsmParams p{};
+  st = chunk_params(*a, p);
+  if (st != GDN_OK) return st;
+  *bytes = chunk_workspace(p);
   return GDN_OK;
 }
 
@@ -897,7 +904,9 @@ gdn_status_t ssm_chunk_fwd(const ssm_chunk_args *a, gdn_stream_t stream) {
   CHECK_THAT(a != nullptr, GDN_ERR_INVALID_ARG, "args is NULL");
   gdn_status_t st = check_chunk_args(*a);
   if (st != GDN_OK) return st;
-  SsmParams p = chunk_params(*a);
+  SsmParams p{};
+  st = chunk_params(*a, p);
+  if (st != GDN_OK) return st;
   const size_t need = chunk_workspace(p);
   if (need > 0) {
     CHECK_THAT(a->workspace != nullptr && a->workspace_bytes >= need, GDN_ERR_WORKSPACE,

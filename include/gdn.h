@@ -397,8 +397,8 @@ gdn_status_t gdn_decode(const gdn_decode_args *args, gdn_stream_t stream);
  *                                     h0
  *   cu_seqlens [N + 1]       int32    as gdn_chunk_fwd; with bad offsets
  *                                     (GDN_ERR_BAD_SEQLENS) nothing is written
- * Limits: 2 <= W <= 4.  Sums in float32, one rounding at the end.  A stride
- * must be at least D.
+ * Limits: 2 <= W <= 4, T <= 2^31 - 256.  Sums in float32, one rounding at the
+ * end.  A stride must be at least D.
  */
 typedef struct short_conv_args {
   int32_t dtype;               /* gdn_dtype_t of x, y, h0, ht */
@@ -499,7 +499,7 @@ gdn_status_t short_conv_decode(const short_conv_decode_args *args, gdn_stream_t 
  * *_batch_stride apart; within a row the last two dimensions are dense, so all
  * of them may be column ranges of wider buffers, starting at any element.
  * Outputs must not overlap inputs.
- * Limits: 1 <= K <= 256, H % Hg == 0, N and H at most 65535.
+ * Limits: 1 <= K <= 256, H % Hg == 0, N and H at most 65535, T <= 2^31 - 256.
  * Segments: a sequence longer than `segment_tokens` (a multiple of 128; 0 = the
  * library's choice, whole sequences when their number fills the GPU) is cut
  * into segments of that many tokens that are processed at once: first each

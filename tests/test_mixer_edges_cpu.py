@@ -9,11 +9,11 @@ import pytest
 import torch
 
 from gated_delta_rule_kk_gb300 import _lib, api_ssm, build_lib
-from gated_delta_rule_kk_gb300._lib import ShortConvBwdArgs, SsmDecodeArgs
+from gated_delta_rule_kk_gb300._lib import ShortConvBwdArgs, SsmChunkArgs, SsmDecodeArgs, Status
 from oracle import mixer as M
 
 from _mixer import scan_rooms, ssm_inputs
-from test_mixer_cpu import FAKE
+from test_mixer_cpu import FAKE, conv_args, scan_args
 
 TESTS = os.path.dirname(os.path.abspath(__file__))
 
@@ -163,3 +163,49 @@ def test_a_stream_of_another_device_is_refused(monkeypatch):
     with pytest.raises(ValueError, match="stream"):
         api_ssm._call("ssm_decode", SsmDecodeArgs(), Stream(), torch.device("cuda:1"))
     assert len(devices.calls) == 1
+
+
+MOST = 0x7fffff00  # tokens of a batch row
+
+
+def bwd_args(**kw):
+    a = dict(dtype=1, weight_dtype=1, dy=FAKE, x=FAKE, weight=FAKE, dx=FAKE, dweight=FAKE,
+             dy_stride=1, x_stride=1, dx_stride=1, B=1, T=8, D=1, W=4, N=1)
+    return ShortConvBwdArgs(**{**a, **kw})
+
+
+def workspace(lib, name, args):
+    n = ctypes.c_size_t(0)
+    status = getattr(lib, name + "_workspace_size")(ctypes.byref(args), ctypes.byref(n))
+    return status, n.value
+
+
+@pytest.mark.parametrize("T", [2 ** 31 - 2 ** 20, MOST])
+def test_shapes_of_the_longest_calls(lib, T):
+    """The sums behind runs and segments do not pass 31 bits."""
+    status, n = workspace(lib, "short_conv_bwd", bwd_args(T=T))
+    assert status == Status.OK
+    # a block's partial sums cover eight runs; runs are as long as 152 SMs of 256 threads want
+    run = -(-T // (152 * 256))
+    run += -run % 4
+    assert n == -(-T // (8 * run)) * 5 * 4
+    a = dict(T=T, H=1, Hg=1, V=8, K=8, B=1, N=1)
+    status, n = workspace(lib, "ssm_chunk", scan_args(SsmChunkArgs, **a, segment_tokens=128))
+    assert (status, n) == (Status.OK, -(-T // 128) * (8 * 8 + 1) * 4)
+    status, n = workspace(lib, "ssm_chunk", scan_args(SsmChunkArgs, **a))
+    assert status == Status.OK and n >= 2 * (8 * 8 + 1) * 4  # few heads: cut into segments
+
+
+def test_longer_calls_are_refused(lib):
+    assert workspace(lib, "short_conv_bwd", bwd_args(T=MOST + 1))[0] == Status.UNSUPPORTED
+    a = bwd_args(T=MOST + 1)
+    assert lib.short_conv_bwd(ctypes.byref(a), None) == Status.UNSUPPORTED
+    a = conv_args(B=1, N=1, T=MOST + 1)
+    assert lib.short_conv_fwd(ctypes.byref(a), None) == Status.UNSUPPORTED
+    a = scan_args(SsmChunkArgs, B=1, N=1, T=MOST + 1)
+    assert workspace(lib, "ssm_chunk", a)[0] == Status.UNSUPPORTED
+    assert lib.ssm_chunk_fwd(ctypes.byref(a), None) == Status.UNSUPPORTED
+    # more segments than one launch counts
+    a = scan_args(SsmChunkArgs, B=65535, N=65535, T=MOST, segment_tokens=128)
+    assert workspace(lib, "ssm_chunk", a)[0] == Status.UNSUPPORTED
+    assert lib.ssm_chunk_fwd(ctypes.byref(a), None) == Status.UNSUPPORTED

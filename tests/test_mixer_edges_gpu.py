@@ -9,7 +9,7 @@ import gated_delta_rule_kk_gb300 as gdn
 from gated_delta_rule_kk_gb300 import Status
 from oracle import mixer as M
 
-from _mixer import assert_inside, conv_inputs, cuda, scan_rooms, ssm_inputs
+from _mixer import assert_each_close, assert_inside, conv_inputs, cuda, scan_rooms, ssm_inputs
 from _util import TOL_F32, assert_close
 
 pytestmark = pytest.mark.gpu
@@ -234,3 +234,24 @@ def test_calls_from_several_threads():
             *scan(d, segment_tokens=128)]
     for out in results:
         assert out is not None and all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def test_convolution_of_the_longest_row():
+    """One channel of 2^31 - 256 tokens: the last run ends where 31 bits do."""
+    T, n = 0x7fffff00, 600
+    i = conv_inputs(50, 1, n, 1, 4, BF16, state=False)
+    c = cuda(i)
+    x = torch.zeros((1, T, 1), dtype=BF16, device="cuda")
+    x[:, -n:] = c["x"]
+    y, ht = gdn.short_conv_fwd(x, c["weight"], c["bias"])
+    ok()
+    ry, rht = M.short_conv(i["x"], i["weight"], i["bias"])
+    assert_each_close(y[:, -n:], ry, "y", 1e-5)
+    assert_each_close(ht, rht, "ht", 1e-5)
+    del y
+    dx, dw, _, _ = gdn.short_conv_bwd(x, x, c["weight"], c["bias"])
+    ok()
+    rx, rw, _, _ = M.short_conv_grad(i["x"], i["x"], i["weight"], i["bias"])
+    assert_each_close(dx[:, -n:], rx, "dx", 1e-5)
+    assert not dx[:, :-n - 3].any()
+    assert_each_close(dw, rw, "dw", 1e-5)
