@@ -6,7 +6,8 @@
 
 namespace gdn {
 
-// Segments are whole multiples of this many tokens.
+// Segments that a caller sets, and those on the tensor cores, are whole multiples of this many
+// tokens; on CUDA cores the library's choice may be of half of it.
 constexpr int SSM_UNIT = 128;
 // The segment length that leaves every sequence whole.
 constexpr int SSM_WHOLE = 0x7fffff80;

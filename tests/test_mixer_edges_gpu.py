@@ -255,3 +255,57 @@ def test_convolution_of_the_longest_row():
     assert_each_close(dx[:, -n:], rx, "dx", 1e-5)
     assert not dx[:, :-n - 3].any()
     assert_each_close(dw, rw, "dw", 1e-5)
+
+
+def replayed(call, *changed):
+    """The outputs of `call` captured in a graph and replayed on the same inputs, with the
+    buffers it changes in place put back before and returned behind."""
+    before = [t.clone() for t in changed]
+    call()  # attributes and look-ups of a first call
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = [t for t in call() if t is not None]
+    for t in out:
+        t.fill_(7)
+    for t, b in zip(changed, before):
+        t.copy_(b)
+    graph.replay()
+    torch.cuda.synchronize()
+    ok()
+    return [t.clone() for t in (*out, *changed)]
+
+
+@pytest.mark.parametrize("B,T,H", [(2, 1, 4), (3, 4, 4), (100, 1, 16)])  # the last by the ring
+def test_graphs_of_tokens(B, T, H):
+    d = cuda(ssm_inputs(51, B, T, H, 1, 64, 128, BF16))
+    c = cuda(conv_inputs(51, B, T, 264, 4, BF16))
+
+    def token(state):
+        return gdn.ssm_decode(d["x"], d["dt"], d["A_log"], d["Bm"], d["Cm"], state, D=d["D"],
+                              z=d["z"], dt_bias=d["dt_bias"]),
+
+    def conv(state):
+        return gdn.short_conv_decode(c["x"], c["weight"], state, c["bias"]),
+
+    for call, start in ((token, d["h0"]), (conv, c["h0"])):
+        state = start.clone()
+        want = [*call(state), state]
+        assert not torch.equal(state, start)
+        held = start.clone()
+        assert all(map(torch.equal, replayed(lambda: call(held), held), want))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,D", [(300, 72), (4000, 2056)])  # from memory, and through the ring
+def test_graphs_of_prompts(dtype, T, D):
+    lens = [T // 3, 0, T - T // 3]
+    c = cuda(conv_inputs(52, 1, T, D, 4, dtype, lens=lens))
+    d = cuda(ssm_inputs(52, 1, T, 2, 1, 64, 128, dtype, lens=lens))
+    calls = (lambda: gdn.short_conv_fwd(c["x"], c["weight"], c["bias"], c["h0"], c["cu"]),
+             lambda: gdn.short_conv_bwd(c["dy"], c["x"], c["weight"], c["bias"], c["h0"], c["dht"],
+                                        c["cu"]),
+             lambda: scan(d), lambda: scan(d, segment_tokens=128))
+    for call in calls:
+        want = [t for t in call() if t is not None]
+        assert all(map(torch.equal, replayed(call), want))
