@@ -43,12 +43,15 @@ struct SsmDecodeParams {
   int dt_f32, softplus, y_f32;
   int tok_f32;   // type of x, z, Bm, Cm
   int whole_bc;  // rows of Bm and Cm are read in 16-byte pieces
+  float none;    // -0
   int vblocks, rows;  // blocks of rows of a head; rows of a ring tile
 };
 
 // e^x to the rounding of the plain exponential, products and sums rounded one by
 // one below: a bfloat16 state is rounded again at every call, so two ways of
-// writing the same update would drift apart a unit at a time.
+// writing the same update would drift apart a unit at a time.  (A product is taken
+// as a x b + (-0), with a -0 that the compiler does not know: it fuses a packed
+// multiplication with the addition behind it.)
 //
 // The T tokens are taken as one small chunk.  With G_t the decays' running sum
 // and u_t = s_t x_t,
@@ -330,14 +333,14 @@ struct SdRows {
 #pragma unroll
         for (int i = 0; i < VEC; i += 2) {
           float add[2];
-          const float w0[2] = {w[0], w[0]}, kk[2] = {keep, keep};
-          mul_row<2>(add, w0, bv[0] + i);
+          const float w0[2] = {w[0], w[0]}, kk[2] = {keep, keep}, none[2] = {p.none, p.none};
+          fma_rows<2>(add, w0, bv[0] + i, none);
 #pragma unroll
           for (int t = 1; t < TM; ++t) {
             const float wt[2] = {w[t], w[t]};
             fma_row<2>(add, wt, bv[t] + i);
           }
-          mul_row<2>(out + i, kk, s[j][q] + i);
+          fma_rows<2>(out + i, kk, s[j][q] + i, none);
           add_row<2>(out + i, out + i, add);
         }
         Row<S, VEC> r;
@@ -484,7 +487,7 @@ __device__ __forceinline__ void ssm_decode_tile(const SsmDecodeParams &p, const 
   const int own = r0 + ((lane % LPR) / (LPR / SD_ROWS)) * RPS;
   const bool writes = lane % (LPR / SD_ROWS) == 0 && own < rows;
   const float keep = f[c.keep()];
-  const float kk[2] = {keep, keep};
+  const float kk[2] = {keep, keep}, none[2] = {p.none, p.none};
   float sum[TM][SD_ROWS];
 #pragma unroll
   for (int t = 0; t < TM; ++t)
@@ -530,13 +533,13 @@ __device__ __forceinline__ void ssm_decode_tile(const SsmDecodeParams &p, const 
       for (int e = 0; e < VEC; e += 2) {
         float add[2];
         const float w0[2] = {w[0], w[0]};
-        mul_row<2>(add, w0, b[0] + e);
+        fma_rows<2>(add, w0, b[0] + e, none);
 #pragma unroll
         for (int t = 1; t < TM; ++t) {
           const float wt[2] = {w[t], w[t]};
           fma_row<2>(add, wt, b[t] + e);
         }
-        mul_row<2>(out + e, kk, s + e);
+        fma_rows<2>(out + e, kk, s + e, none);
         add_row<2>(out + e, out + e, add);
       }
       row.round(out);
@@ -942,7 +945,7 @@ gdn_status_t ssm_decode(const ssm_decode_args *a, gdn_stream_t stream) {
              "B * H (%lld) is too large for one call", (long long)bh);
   SsmDecodeParams p{};
   set_tokens(p, *a);
-  p.state = a->state; p.slots = a->slot_indices; p.pool = a->pool;
+  p.state = a->state; p.slots = a->slot_indices; p.pool = a->pool; p.none = -0.f;
   const int wide = 16 / (int)dtype_bytes(a->dtype);
   p.whole_bc = aligned_to(a->Bm, 16) && aligned_to(a->Cm, 16) && p.bs % wide == 0 && p.bb % wide == 0 && p.cs % wide == 0 && p.cb % wide == 0;
   p.err = device_error_word();

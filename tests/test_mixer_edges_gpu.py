@@ -309,3 +309,20 @@ def test_graphs_of_prompts(dtype, T, D):
     for call in calls:
         want = [t for t in call() if t is not None]
         assert all(map(torch.equal, replayed(call), want))
+
+
+@pytest.mark.parametrize("B,H,K", [(3, 24, 128), (64, 28, 128), (116, 28, 48)])
+def test_scan_token_states_are_rounded_step_by_step(B, H, K):
+    """A bfloat16 state is its update with every float32 product and sum rounded by itself and
+    one rounding at the end, bit for bit: kept over many calls, it does not drift from that."""
+    d = cuda(ssm_inputs(53, B, 1, H, 1, 64, K, F32))
+    state = (torch.randn((B, H, 64, K), device="cuda") / 2).to(BF16)
+    s = d["dt"][:, 0] + d["dt_bias"]
+    s = torch.where(s > 20, s, torch.log1p(torch.exp(s)))
+    keep = torch.exp(-torch.exp(d["A_log"]) * s)[..., None, None]
+    new = (d["x"][:, 0] * s[..., None])[..., None] * d["Bm"][:, 0, :, None, :]
+    old = keep * state.float()
+    want = (old + new).to(BF16)
+    gdn.ssm_decode(d["x"], d["dt"], d["A_log"], d["Bm"], d["Cm"], state, dt_bias=d["dt_bias"])
+    ok()
+    assert torch.equal(state, want)
