@@ -13,9 +13,10 @@
 // and rows that TMA cannot address, read them into registers.
 //
 // Measured (bf16, W = 4; share of the card's copy rate): two prompts of 4096 tokens
-// and 6144 channels 41 us, 73%; eight packed prompts of 32068 tokens, 4352 channels
-// 105 us, 79%; the gradient of the first 73 us, 61%; one token of 256 requests, 8192
-// channels 7.8 us, 64%, of one request 2.1 us, a launch.
+// and 6144 channels 40 us, 74%; eight packed prompts of 32068 tokens, 4352 channels
+// 105 us, 78%; the gradient of the first 74 us, 60%; one token of 256 requests, 8192
+// channels 7.8 us, 64%, of one request 2.4 us, a launch.  What the gradient is short of
+// is warps: twelve of an SM compute, beside 192 KB that can be on its way.
 #include <algorithm>
 #include <initializer_list>
 #include <type_traits>
@@ -408,7 +409,9 @@ struct ConvRing {
   static constexpr int ROW = CR_BOX * (int)sizeof(T);  // bytes of a box's row
   static constexpr int BOX = CR_STAGE * ROW;
   static constexpr int STAGE = BOXES * BOX * (BWD ? 2 : 1);
-  static constexpr int STAGES = 4;  // and blocks that an SM holds
+  // Stages, and blocks that an SM holds: three of the gradient's take 192 of 227 KB and
+  // 128 registers a thread for its sums and windows; either alone keeps a fourth out.
+  static constexpr int STAGES = 4;
   static constexpr int BLOCKS = BWD ? 3 : 5;
 };
 

@@ -13,9 +13,11 @@
 //   warps turn the items' tokens into float32 coefficients beside the tiles, so
 //   that memory never waits for a block's start, its arithmetic or its end and
 //   the warps that hold the state wait for nothing but shared memory.
-// Measured: one token of 256 requests, 64 heads, bf16 states of 64 x 128 92.9 us,
+// Measured: one token of 256 requests, 64 heads, bf16 states of 64 x 128 93.1 us,
 // 5.8 TB/s (86% of the copy rate); four tokens of 3 requests, 48 heads, float32
-// states 9.0 us, the latency of one trip to memory and of the sums over K.
+// states 9.4 us: the trip to memory for the states, then the tokens one after another,
+// whose rows of B and C (asked for ahead only for a single token) come between the
+// sums over K.
 #include <math.h>
 
 #include <algorithm>
@@ -704,7 +706,7 @@ cudaError_t launch_decode(SsmDecodeParams &p, cudaStream_t stream) {
   const int64_t bh = (int64_t)p.B * p.H;
   // The ring pays once every block has an item (requests of 64 heads, bf16 states of
   // 64 x 128, ring / direct, us: 8 requests 6.2 / 6.3, 16 8.0 / 9.3, 64 20.3 / 28.9,
-  // 256 92.9 / 152.5).
+  // 256 93.1 / 152.5).
   const int blocks = sd_blocks(TM) * sm_count();
   const int rows = std::min(ROWS, (int)(SD_TILE / (p.K * sizeof(S))));
   const int vblocks = (p.V + rows - 1) / rows;
@@ -947,7 +949,8 @@ gdn_status_t ssm_decode(const ssm_decode_args *a, gdn_stream_t stream) {
   set_tokens(p, *a);
   p.state = a->state; p.slots = a->slot_indices; p.pool = a->pool; p.none = -0.f;
   const int wide = 16 / (int)dtype_bytes(a->dtype);
-  p.whole_bc = aligned_to(a->Bm, 16) && aligned_to(a->Cm, 16) && p.bs % wide == 0 && p.bb % wide == 0 && p.cs % wide == 0 && p.cb % wide == 0;
+  p.whole_bc = aligned_to(a->Bm, 16) && aligned_to(a->Cm, 16) && p.bs % wide == 0 &&
+               p.bb % wide == 0 && p.cs % wide == 0 && p.cb % wide == 0;
   p.err = device_error_word();
   if (p.err == nullptr) return launch_status(cudaGetLastError(), "device error word");
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -9,7 +9,10 @@
 // bf16 pieces along the keys), M X (N = 64, M as two pieces) and B^T W (N = 128 +
 // 64: W as three pieces, so that the float32 state gains no rounding from the
 // operands).  x, B and C are bf16 themselves and enter exactly.  One piece each of
-// h and M left y up to 3e-2 of its RMS off, two some 5e-5.
+// h and M left y up to 3e-2 of its RMS off; two leave 16 bits: 2^-16 of the terms'
+// magnitudes, 2.4e-6 of y in norm, of a float32 y too (of those rounded to bf16 one in
+// 800 is then the neighbour of the exact one's).  A third piece would take 64 more
+// columns of TMEM a chunk and another 16 KB, and both are used up.
 //
 // One CTA per (64-column V tile, head, segment of a sequence) walks the
 // segment's chunks; h stays in registers in float32.  S, M and W do not depend
@@ -30,14 +33,15 @@
 //                 others run
 //   30     scalars  step sizes, log-decays and their sums
 //   31     store  TMA: y
-// What bounds it (2 x 4096 tokens, 64 heads of 64 x 128, B and C shared by all:
-// 100 us, where the bytes alone would take 31 at the copy rate and CUDA cores took
-// 1620): 128 CTAs with some 6000 cycles a chunk, in which every role is busy for
-// 3000 to 5000, waiting the rest for one another.  The warps' 14000 instructions a
-// chunk take 65% of an SM's issue slots, the products 42% of the tensor pipe, HBM
-// 22% of its rate: fewer instructions a chunk would be the next step.  Two y in TMEM (111 us with one, which M X of a chunk
-// shared with the output of the one before) and z past shared memory (its tile
-// waited for y's store) keep the output out of that chain.
+// What bounds it (2 x 4096 tokens, 64 heads of 64 x 128, B and C shared by all: 98
+// to 101 us, where the bytes alone would take 31 at the copy rate and CUDA cores
+// took 1620): 128 CTAs with some 6000 cycles a chunk, in which every role is busy
+// for 3000 to 5000, waiting the rest for one another.  The warps' 14900
+// instructions a chunk take 65% of an SM's issue slots, the products 40% of the
+// tensor pipe, HBM 23% of its rate: fewer instructions a chunk would be the next
+// step.  Two y in TMEM (111 us with one, which M X of a chunk shared with the output
+// of the one before) and z past shared memory (its tile waited for y's store) keep
+// the output out of that chain.
 // The decays: every 32-token block b keeps f_j = s_j e^(block end - G_j) and the
 // sums inside the block, so that e^(G_i - G_j) s_j is a product of f_j and one
 // factor per row and block, all exponents sums of the terms between j and i.  Only on
@@ -65,7 +69,7 @@ constexpr int ST_W_OUT = 8, ST_W_STATE = 16, ST_W_W = 24, ST_W_LOAD = 28, ST_W_M
               ST_W_SCALARS = 30, ST_THREADS = 32 * 32;
 // Registers of a thread of each role.  The block starts with 64 a thread, and
 // 64 + 64 + 64 + 64 + 80 + 80 + 48 + 48, the warpgroups' shares, is what 8
-// warpgroups have at 64: no role spills.
+// warpgroups have at 64 (16 bytes of spills are left in all).
 constexpr int ST_R_STATE = 80, ST_R_W = 48, ST_R_REST = 48;
 static_assert(4 * 64 + 2 * ST_R_STATE + ST_R_W + ST_R_REST <= 8 * 64, "registers");
 constexpr uint32_t ST_TILE = 16384;  // 128 rows of 128 bytes, 128-byte swizzle

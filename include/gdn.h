@@ -398,7 +398,10 @@ gdn_status_t gdn_decode(const gdn_decode_args *args, gdn_stream_t stream);
  *   cu_seqlens [N + 1]       int32    as gdn_chunk_fwd; with bad offsets
  *                                     (GDN_ERR_BAD_SEQLENS) nothing is written
  * Limits: 2 <= W <= 4, T <= 2^31 - 256.  Sums in float32, one rounding at the
- * end.  A stride must be at least D.
+ * end.  SiLU and its derivative come from the hardware's fast exponential and
+ * reciprocal, for float32 too: off by a few 2^-23, and for negative p by another
+ * |p| 2^-23 of values that are themselves near |p| e^p.  A stride must be at
+ * least D.
  */
 typedef struct short_conv_args {
   int32_t dtype;               /* gdn_dtype_t of x, y, h0, ht */
@@ -499,6 +502,15 @@ gdn_status_t short_conv_decode(const short_conv_decode_args *args, gdn_stream_t 
  * *_batch_stride apart; within a row the last two dimensions are dense, so all
  * of them may be column ranges of wider buffers, starting at any element.
  * Outputs must not overlap inputs.
+ * Accuracy: states are float32 throughout.  y is float32 arithmetic, rounded once,
+ * but where the tensor cores take the call (dtype GDN_BF16, K <= 128, K and V
+ * multiples of 8, 16-byte aligned rows): there what h_t and the weights of the
+ * tokens x_j, j <= t, are multiplied with enters to 16 bits, so that y is off by at
+ * most 2^-16 of the sum of its terms' magnitudes (2e-6 in norm), also with y_fp32.
+ * An Inf or NaN in x reaches its row of h and of y from its token on, and nothing
+ * else; that y may be NaN where the recurrence has an infinity.  Step sizes below
+ * zero let h grow: the sums of -e^A_log s over 128 tokens should then stay within
+ * +-80.
  * Limits: 1 <= K <= 256, H % Hg == 0, N and H at most 65535, T <= 2^31 - 256.
  * Segments: a sequence longer than `segment_tokens` (a multiple of 128; 0 = the
  * library's choice, whole sequences when their number fills the GPU) is cut
