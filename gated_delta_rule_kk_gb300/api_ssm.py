@@ -214,7 +214,8 @@ def _workspace(args, size_fn, workspace, device, stream):
     caching allocator, which keeps it valid for the work enqueued on its stream,
     unless the caller passes one)."""
     n = ctypes.c_size_t(0)
-    with contextlib.nullcontext() if _current_device() == device.index else torch.cuda.device(device):
+    here = _current_device() == device.index
+    with contextlib.nullcontext() if here else torch.cuda.device(device):
         st = getattr(_lib._lib or _lib.load(), size_fn)(ctypes.byref(args), ctypes.byref(n))
     if st:
         _lib.check(st, size_fn)

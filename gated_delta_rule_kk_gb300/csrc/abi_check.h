@@ -54,7 +54,7 @@ inline int sm_count() {
   return n;
 }
 
-// Tokens of a batch row: the kernels' indexes run up to 256 past the last one.
+// Tokens of a batch row, or rows of a head: the kernels' indexes run up to 256 past the last one.
 constexpr int MAX_TOKENS = 0x7fffff00;
 
 #define CHECK_THAT(cond, st, ...)                       \

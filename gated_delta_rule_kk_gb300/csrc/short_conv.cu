@@ -253,7 +253,8 @@ __global__ void __launch_bounds__(32 * CB_RUNS, CB_BLOCKS) conv_bwd_kernel(ConvB
   const int b = blockIdx.x / p.tiles;
   if (!bounds_ok(b < p.q.B, p.err)) return;
   // (a block's last runs may lie past the end: their products pass 31 bits)
-  const int lo = (int)min((int64_t)p.q.T, (int64_t)((blockIdx.x % p.tiles) * CB_RUNS + threadIdx.y) * p.run);
+  const int64_t warp_run = (int64_t)(blockIdx.x % p.tiles) * CB_RUNS + threadIdx.y;
+  const int lo = (int)min((int64_t)p.q.T, warp_run * p.run);
   const int hi = lo + min(p.run, p.q.T - lo);
   if (live && lo < hi) {
     load_weights<VEC, W>(w, bias, p.weight, p.bias, p.w_f32, c);

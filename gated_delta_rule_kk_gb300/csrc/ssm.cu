@@ -937,6 +937,7 @@ gdn_status_t ssm_decode(const ssm_decode_args *a, gdn_stream_t stream) {
   if (st != GDN_OK) return st;
   CHECK_DTYPE(a->state_dtype, "state_dtype");
   CHECK_THAT(a->K % 8 == 0, GDN_ERR_UNSUPPORTED, "K (%d) must be a multiple of 8", a->K);
+  CHECK_THAT(a->V <= MAX_TOKENS, GDN_ERR_UNSUPPORTED, "V (%d) must be at most %d", a->V, MAX_TOKENS);
   CHECK_THAT(a->pool >= 1, GDN_ERR_INVALID_ARG, "pool must be positive (got %d)", a->pool);
   CHECK_THAT(a->slot_indices != nullptr || a->pool >= a->B, GDN_ERR_INVALID_ARG,
              "identity slots need pool (%d) >= B (%d)", a->pool, a->B);

@@ -1,4 +1,4 @@
-// The driver's tensor map encoder, for the host code of kernels that load by TMA.
+// The CUDA driver's tensor map encoder, for the host code of kernels that load by TMA.
 #pragma once
 
 #include <cuda.h>

@@ -209,3 +209,10 @@ def test_longer_calls_are_refused(lib):
     a = scan_args(SsmChunkArgs, B=65535, N=65535, T=MOST, segment_tokens=128)
     assert workspace(lib, "ssm_chunk", a)[0] == Status.UNSUPPORTED
     assert lib.ssm_chunk_fwd(ctypes.byref(a), None) == Status.UNSUPPORTED
+
+
+@pytest.mark.parametrize("cls,name", [(SsmChunkArgs, "ssm_chunk_fwd"), (SsmDecodeArgs, "ssm_decode")])
+def test_heads_of_more_rows_than_a_launch_counts_are_refused(lib, cls, name):
+    a = scan_args(cls, V=2 ** 31 - 1, H=1, Hg=1, T=1,
+                  **{t + "_stride": 2 ** 31 for t in ("x", "z", "y")})
+    assert getattr(lib, name)(ctypes.byref(a), None) == Status.UNSUPPORTED
