@@ -192,6 +192,45 @@ class SsmDecodeArgs(ctypes.Structure):
     ]
 
 
+def _strides(*tensors):
+    return [(f"{t}{kind}", c_int64) for t in tensors for kind in ("_stride", "_batch_stride")]
+
+
+_NORM_SIZES = [(n, c_int32) for n in ("B", "T", "D", "groups", "shared_weight", "center",
+                                      "gate_first", "activation")] + [("eps", c_float)]
+
+
+class GroupNormArgs(ctypes.Structure):
+    _fields_ = [
+        ("dtype", c_int32), ("weight_dtype", c_int32),
+        ("x", c_void_p), ("z", c_void_p), ("weight", c_void_p), ("bias", c_void_p), ("y", c_void_p),
+        *_strides("x", "z", "y"), *_NORM_SIZES,
+    ]
+
+
+class GroupNormBwdArgs(ctypes.Structure):
+    _fields_ = [
+        ("dtype", c_int32), ("weight_dtype", c_int32),
+        ("dy", c_void_p), ("x", c_void_p), ("z", c_void_p), ("weight", c_void_p), ("bias", c_void_p),
+        ("dx", c_void_p), ("dz", c_void_p), ("dweight", c_void_p), ("dbias", c_void_p),
+        *_strides("dy", "x", "z", "dx", "dz"), *_NORM_SIZES,
+        ("workspace", c_void_p), ("workspace_bytes", c_size_t),
+    ]
+
+
+class KdaDecodeArgs(ctypes.Structure):
+    _fields_ = [
+        ("dtype", c_int32), ("state_dtype", c_int32),
+        ("q", c_void_p), ("k", c_void_p), ("v", c_void_p), ("a", c_void_p), ("b", c_void_p),
+        ("A_log", c_void_p), ("dt_bias", c_void_p), ("state", c_void_p),
+        ("slot_indices", c_void_p), ("o", c_void_p),
+        *_strides("q", "k", "v", "a", "b", "o"),
+        ("B", c_int32), ("T", c_int32), ("H", c_int32), ("HV", c_int32), ("K", c_int32),
+        ("V", c_int32), ("pool", c_int32), ("use_qk_l2norm", c_int32), ("o_fp32", c_int32),
+        ("scale", c_float), ("eps", c_float),
+    ]
+
+
 # name -> (argtypes, restype); exactly the functions include/gdn.h declares
 SIGNATURES = {
     "gdn_chunk_workspace_size": ([ctypes.POINTER(GdnChunkArgs), ctypes.POINTER(c_size_t)], c_int32),
@@ -215,6 +254,11 @@ SIGNATURES = {
     "ssm_chunk_workspace_size": ([ctypes.POINTER(SsmChunkArgs), ctypes.POINTER(c_size_t)], c_int32),
     "ssm_chunk_fwd": ([ctypes.POINTER(SsmChunkArgs), c_void_p], c_int32),
     "ssm_decode": ([ctypes.POINTER(SsmDecodeArgs), c_void_p], c_int32),
+    "group_norm_fwd": ([ctypes.POINTER(GroupNormArgs), c_void_p], c_int32),
+    "group_norm_bwd_workspace_size": ([ctypes.POINTER(GroupNormBwdArgs), ctypes.POINTER(c_size_t)],
+                                      c_int32),
+    "group_norm_bwd": ([ctypes.POINTER(GroupNormBwdArgs), c_void_p], c_int32),
+    "kda_decode": ([ctypes.POINTER(KdaDecodeArgs), c_void_p], c_int32),
     "gdn_self_test_wait": ([c_int32, c_int32, c_void_p], c_int32),
     "gdn_self_test_bounds": ([c_int32, c_int32, ctypes.POINTER(c_int32), c_void_p], c_int32),
     "gdn_check_device_error": ([c_void_p, ctypes.POINTER(c_int32)], c_int32),

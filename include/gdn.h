@@ -573,6 +573,121 @@ typedef struct ssm_decode_args {
 gdn_status_t ssm_decode(const ssm_decode_args *args, gdn_stream_t stream);
 
 /*
+ * Norm over groups of channels of every token, with an activation or a gate: what
+ * stands between a recurrence and its output projection (a group is a head there),
+ * and group norm, channels last, where every token is a sample of its own (its
+ * statistics reach no other token, so that the layer stays causal).  Per token and
+ * group of W = D / groups channels:
+ *     u = x, or x act(z) with gate_first = 1
+ *     n = (u - mean(u)) / sqrt(mean((u - mean(u))^2) + eps)     center = 1
+ *     n = u / sqrt(mean(u^2) + eps)                             center = 0
+ *     m = n weight + bias
+ *     y = m act(z) with z, act(m) without z, m with gate_first
+ *   x, z, y  [B, T, D]      dtype    strided as in short_conv_fwd (z NULL = none);
+ *                                    y must not overlap x or z
+ *   weight, bias            weight_dtype (GDN_F32, or dtype): [D], or [D / groups] for
+ *                                    all groups with shared_weight = 1; NULL = ones / zeros
+ *   activation              gdn_activation_t
+ * Limits: D % groups == 0, D / groups at most 8192, B T at most 2^31 - 256.  Arithmetic in
+ * float32, the mean taken off before squares are summed; one rounding at the end.
+ * SiLU and the sigmoid come from the hardware's fast exponential and reciprocal, as in
+ * short_conv_fwd.  An Inf or NaN in x stays within its token's group.
+ */
+typedef enum gdn_activation {
+  GDN_ACT_NONE = 0,     /* v             */
+  GDN_ACT_SILU = 1,     /* v / (1 + e^-v) */
+  GDN_ACT_SIGMOID = 2   /* 1 / (1 + e^-v) */
+} gdn_activation_t;
+
+typedef struct group_norm_args {
+  int32_t dtype;               /* gdn_dtype_t of x, z, y */
+  int32_t weight_dtype;        /* gdn_dtype_t of weight, bias */
+  const void *x, *z;
+  const void *weight, *bias;
+  void *y;
+  int64_t x_stride, x_batch_stride, z_stride, z_batch_stride, y_stride, y_batch_stride;
+  int32_t B, T, D, groups;
+  int32_t shared_weight;
+  int32_t center, gate_first;
+  int32_t activation;          /* gdn_activation_t */
+  float eps;                   /* >= 0 */
+} group_norm_args;
+
+gdn_status_t group_norm_fwd(const group_norm_args *args, gdn_stream_t stream);
+
+/*
+ * Gradient of group_norm_fwd.  The statistics are formed again from x; nothing of the
+ * forward call is kept.
+ *   dy, x, z, dx, dz [B, T, D]   dtype    strided; dx and dz must not overlap an input;
+ *                                         dz is given exactly when z is
+ *   dweight, dbias               float32  shaped as weight and bias, NULL = not returned
+ * The sums over tokens run in a fixed order (float32 partial sums in `workspace`, 16-byte
+ * aligned, group_norm_bwd_workspace_size() bytes), so results do not change from run to
+ * run.  The rest as group_norm_fwd.
+ */
+typedef struct group_norm_bwd_args {
+  int32_t dtype;               /* gdn_dtype_t of dy, x, z, dx, dz */
+  int32_t weight_dtype;        /* gdn_dtype_t of weight, bias */
+  const void *dy, *x, *z;
+  const void *weight, *bias;
+  void *dx, *dz;
+  float *dweight, *dbias;
+  int64_t dy_stride, dy_batch_stride, x_stride, x_batch_stride, z_stride, z_batch_stride;
+  int64_t dx_stride, dx_batch_stride, dz_stride, dz_batch_stride;
+  int32_t B, T, D, groups;
+  int32_t shared_weight;
+  int32_t center, gate_first;
+  int32_t activation;
+  float eps;
+  void *workspace;
+  size_t workspace_bytes;
+} group_norm_bwd_args;
+
+/* Bytes of workspace group_norm_bwd needs (0 when neither dweight nor dbias is returned);
+ * reads sizes, strides, dtype, the tensors' alignment and which of them are NULL. */
+gdn_status_t group_norm_bwd_workspace_size(const group_norm_bwd_args *args, size_t *bytes);
+gdn_status_t group_norm_bwd(const group_norm_bwd_args *args, gdn_stream_t stream);
+
+/*
+ * KDA for T = 1..4 new tokens per batch entry against pooled states, updated in place:
+ * the recurrence of kda_chunk_fwd with the gates formed as gdn_decode forms them, one per
+ * key channel.  Per token, with S [V, K] of the entry's slot:
+ *     decay[c] = exp(-e^A_log softplus(a[c] + dt_bias[c])),   beta = sigmoid(b)
+ *     S <- S diag(decay),  d = beta (v - S k),  S <- S + d k^T,  o = scale S q
+ * with softplus(x) = log(1 + e^x), x itself above 20.
+ *   q, k     [B, T, H, K]   dtype    value head hv reads key head hv / (HV / H); divided
+ *                                    by sqrt(sum x^2 + eps) when use_qk_l2norm
+ *   v, o     [B, T, HV, V]  dtype    o float32 when o_fp32 = 1
+ *   a        [B, T, HV, K]  dtype
+ *   b        [B, T, HV]     dtype
+ *   A_log    [HV], dt_bias [HV, K]  float32, dt_bias NULL = zeros
+ *   state    [pool, HV, V, K]  state_dtype   K fastest; read once, carried over the T tokens
+ *                                    in float32 and written once
+ *   slot_indices [B]        int32    as gdn_decode
+ * Token tensors are strided as in ssm_chunk_fwd: column ranges of wider buffers, so that q,
+ * k and v may be columns of the short convolution's output.  Outputs must not overlap inputs.
+ * Limits: 8 <= K <= 256, K % 8 == 0, HV % H == 0, HV at most 65535.  scale <= 0 selects
+ * 1/sqrt(K); eps < 0 selects 1e-6.
+ */
+typedef struct kda_decode_args {
+  int32_t dtype;               /* gdn_dtype_t of q, k, v, a, b, o */
+  int32_t state_dtype;         /* gdn_dtype_t of state */
+  const void *q, *k, *v, *a, *b;
+  const float *A_log, *dt_bias;
+  void *state;
+  const int32_t *slot_indices;
+  void *o;
+  int64_t q_stride, q_batch_stride, k_stride, k_batch_stride, v_stride, v_batch_stride;
+  int64_t a_stride, a_batch_stride, b_stride, b_batch_stride, o_stride, o_batch_stride;
+  int32_t B, T, H, HV, K, V, pool;
+  int32_t use_qk_l2norm;
+  int32_t o_fp32;
+  float scale, eps;
+} kda_decode_args;
+
+gdn_status_t kda_decode(const kda_decode_args *args, gdn_stream_t stream);
+
+/*
  * GDN chunked forward without a workspace, for callers that cannot allocate
  * device memory (a host runtime that owns a fixed device-memory budget and
  * forbids cudaMalloc from plugins, or a latency-critical loop that must not
