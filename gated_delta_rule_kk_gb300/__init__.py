@@ -15,6 +15,6 @@ from .api import (  # noqa: F401
 from .api_ssm import (  # noqa: F401
     short_conv_bwd, short_conv_decode, short_conv_fwd, ssm_chunk_fwd, ssm_decode,
 )
-from .api_delta import kda_decode  # noqa: F401
+from .api_delta import gdn_chunk_bwd, kda_decode  # noqa: F401
 from .api_norm import group_norm_bwd, group_norm_fwd  # noqa: F401
 from ._lib import GateKind, GdnError, Status  # noqa: F401

@@ -218,6 +218,20 @@ class GroupNormBwdArgs(ctypes.Structure):
     ]
 
 
+class GdnChunkBwdArgs(ctypes.Structure):
+    _fields_ = [
+        ("dtype", c_int32),
+        ("q", c_void_p), ("k", c_void_p), ("v", c_void_p), ("g", c_void_p), ("beta", c_void_p),
+        ("h0", c_void_p), ("do_", c_void_p), ("dht", c_void_p),
+        ("dq", c_void_p), ("dk", c_void_p), ("dv", c_void_p), ("dg", c_void_p), ("dbeta", c_void_p),
+        ("dh0", c_void_p), ("cu_seqlens", c_void_p),
+        ("B", c_int32), ("T", c_int32), ("H", c_int32), ("Hg", c_int32), ("K", c_int32),
+        ("V", c_int32), ("N", c_int32), ("chunk_size", c_int32), ("g_is_cumsum", c_int32),
+        ("state_v_first", c_int32), ("scale", c_float),
+        ("workspace", c_void_p), ("workspace_bytes", c_size_t),
+    ]
+
+
 class KdaDecodeArgs(ctypes.Structure):
     _fields_ = [
         ("dtype", c_int32), ("state_dtype", c_int32),
@@ -258,6 +272,9 @@ SIGNATURES = {
     "group_norm_bwd_workspace_size": ([ctypes.POINTER(GroupNormBwdArgs), ctypes.POINTER(c_size_t)],
                                       c_int32),
     "group_norm_bwd": ([ctypes.POINTER(GroupNormBwdArgs), c_void_p], c_int32),
+    "gdn_chunk_bwd_workspace_size": ([ctypes.POINTER(GdnChunkBwdArgs), ctypes.POINTER(c_size_t)],
+                                     c_int32),
+    "gdn_chunk_bwd": ([ctypes.POINTER(GdnChunkBwdArgs), c_void_p], c_int32),
     "kda_decode": ([ctypes.POINTER(KdaDecodeArgs), c_void_p], c_int32),
     "gdn_self_test_wait": ([c_int32, c_int32, c_void_p], c_int32),
     "gdn_self_test_bounds": ([c_int32, c_int32, ctypes.POINTER(c_int32), c_void_p], c_int32),

@@ -1,0 +1,98 @@
+// The gated delta rule's gradient over chunks, between its entry point (delta_bwd.cu) and
+// the kernels (delta_bwd_tc.cu on the tensor cores, delta_bwd_simt.cu on CUDA cores).
+//
+// Per chunk of 64 tokens, with G the running sum of the log-gates, h the state [K, V] at the
+// chunk's start and D the gradient of the state at its end:
+//   A_ij = beta_i k_i.k_j e^(G_i - G_j)  (i > j),   P_ij = scale q_i.k_j e^(G_i - G_j)  (i >= j)
+//   T = (I + A)^-1,  r = beta (v - e^G k h),  n = T r,  h+ = e^(G_L) h + (k e^(G_L - G))^T n
+// and back:
+//   dn = P^T do + e^(G_L - G) k D,   dr = T^T dn,
+//   D- = e^(G_L) D + (scale e^G q)^T do - (beta e^G k)^T dr,
+//   dA = -dr n^T (i > j),   dP = do n^T (i >= j),
+//   dq = scale e^G do h^T + (dP L) k,                      L_ij = e^(G_i - G_j), scale in dP L
+//   dk = -beta e^G dr h^T + e^(G_L - G) n D^T + (dP L)^T q + (dA L beta + its transpose) k,
+//   dv = beta dr,   dbeta = dr.v - e^G k.(dr h^T) + rowsum(dA k k^T L),
+//   dG = rowsum(M) - colsum(M) + q.dq_h + k.dk_h - k.dk_s,   M = dA A + dP P,
+//   dG_L += e^(G_L) <h, D> + sum k.dk_s,
+// where dq_h, dk_h and dk_s are the terms with h and D; dg is dG summed from the chunk's end.
+// (dA = -dr n^T holds as n solves (I + A) n = r: neither the gradient of T nor w = T beta e^G k
+// is formed.)  Four launches: T and P of every chunk; the states forward; their gradients
+// backward; everything else, every chunk by itself.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "gdn.h"
+
+namespace gdn {
+
+struct DeltaBwdParams {
+  const void *q, *k, *v, *dout;
+  const float *g, *beta, *h0, *dht;
+  void *dq, *dk, *dv;
+  float *dg, *dbeta, *dh0;
+  const int32_t *cu;
+  int *err;
+  int B, T, H, Hg, K, V, N;
+  int g_is_cumsum, v_first;
+  float scale;
+  int per_seq;                // chunks of a sequence (cu NULL)
+  int64_t chunks;             // chunks at most
+  // workspace
+  int32_t *first;             // [N + 1] first chunk of every sequence (cu given)
+  int32_t *owner;             // [chunks] sequence of every chunk
+  unsigned char *blocks;      // [chunks][H] of `block` bytes each
+  int64_t block;
+};
+
+// A chunk: its sequence, its place there, its first token and how many it has.
+struct DeltaChunk {
+  int n, i, len;
+  int64_t token;
+};
+
+#ifdef __CUDACC__
+// Chunk c; len 0 if there is none.
+__device__ __forceinline__ DeltaChunk delta_chunk(const DeltaBwdParams &p, int64_t c) {
+  DeltaChunk k{0, 0, 0, 0};
+  if (p.cu == nullptr) {
+    k.n = (int)(c / p.per_seq);
+    k.i = (int)(c - (int64_t)k.n * p.per_seq);
+    k.len = min(64, p.T - k.i * 64);
+    k.token = (int64_t)k.n * p.T + k.i * 64;
+    return k;
+  }
+  if (c >= p.first[p.N]) return k;
+  k.n = p.owner[c];
+  k.i = (int)(c - p.first[k.n]);
+  const int lo = p.cu[k.n];
+  k.len = min(64, p.cu[k.n + 1] - lo - k.i * 64);
+  k.token = lo + k.i * 64;
+  return k;
+}
+
+// The chunks of sequence n: the first one, and how many; 0 with bad offsets.
+__device__ __forceinline__ int delta_chunks(const DeltaBwdParams &p, int n, int64_t *first) {
+  if (p.cu == nullptr) {
+    *first = (int64_t)n * p.per_seq;
+    return p.per_seq;
+  }
+  *first = p.first[n];
+  return p.first[n + 1] - p.first[n];
+}
+
+// Whether the offsets were good (the table kernel marks bad ones).
+__device__ __forceinline__ bool delta_good(const DeltaBwdParams &p) {
+  return p.cu == nullptr || p.first[p.N] >= 0;
+}
+#endif
+
+// Whether the tensor cores take the call, the bytes of a chunk and head, and the launches.
+bool delta_bwd_tc_supported(const DeltaBwdParams &p, bool bf16);
+int64_t delta_bwd_tc_block(const DeltaBwdParams &p);
+cudaError_t launch_delta_bwd_tc(const DeltaBwdParams &p, cudaStream_t stream);
+int64_t delta_bwd_simt_block(const DeltaBwdParams &p);
+cudaError_t launch_delta_bwd_simt(const DeltaBwdParams &p, bool bf16, cudaStream_t stream);
+
+}  // namespace gdn

@@ -289,6 +289,57 @@ gdn_status_t gdn_chunk_state_bwd(const gdn_state_bwd_args *args, gdn_stream_t st
 gdn_status_t gdn_chunk_host_workspace_size(const gdn_chunk_args *args, size_t *bytes);
 
 /*
+ * Gradient of gdn_chunk_fwd: of a loss with dL/do and dL/dht given, with respect to q, k, v,
+ * g, beta and h0.  Everything the forward computed is formed again from its inputs; nothing
+ * of that call is kept.
+ *   q, k, dq, dk  [B, T, Hg, K]   dtype    dq and dk summed over the value heads that share
+ *                                          the key head
+ *   v, do, dv     [B, T, H, V]    dtype
+ *   g, beta, dg, dbeta [B, T, H]  float32  dg is the gradient of g as given: of the per-token
+ *                                          gate, or of the chunk-local sum (g_is_cumsum = 1)
+ *   h0, dht, dh0  [N, H, K, V]    float32  ([N, H, V, K] with state_v_first = 1); NULL =
+ *                                          zeros / zeros / not returned
+ *   cu_seqlens    [N + 1]         int32    as gdn_chunk_fwd; with bad offsets nothing is
+ *                                          written
+ * With T == 0 the per-token arrays may be NULL (dh0 = dht, or zeros).  Outputs must not
+ * overlap inputs.  A sum over heads, tokens or channels always runs in the same order, so
+ * results do not change from run to run.
+ * Accuracy: float32 inputs are taken in float32 throughout.  With bfloat16 inputs, K and V
+ * multiples of 8 and V <= 128 the products run on the tensor cores, whose operands carry
+ * float32 values (states, their gradients, corrected values, T and P) as two bfloat16 pieces:
+ * each is off by up to 2^-17 of itself, sums are float32, and dq, dk and dv are rounded once
+ * (float32 results are within 1e-5 of their norm).
+ * Limits: as gdn_chunk_fwd, and V <= 2^20.  scale <= 0 selects 1/sqrt(K).
+ * Workspace: gdn_chunk_bwd_workspace_size() bytes, device memory, 256-byte aligned: for every
+ * chunk of 64 tokens and value head T, P, the corrected values and their gradients, the state
+ * and its gradient (224 KB with K = V = 128).
+ */
+typedef struct gdn_chunk_bwd_args {
+  int32_t dtype;               /* gdn_dtype_t of q, k, v, do, dq, dk, dv */
+  const void *q, *k, *v;
+  const float *g, *beta;
+  const float *h0;
+  const void *do_;
+  const float *dht;
+  void *dq, *dk, *dv;
+  float *dg, *dbeta;
+  float *dh0;
+  const int32_t *cu_seqlens;
+  int32_t B, T, H, Hg, K, V, N;
+  int32_t chunk_size;
+  int32_t g_is_cumsum;
+  int32_t state_v_first;
+  float scale;
+  void *workspace;
+  size_t workspace_bytes;
+} gdn_chunk_bwd_args;
+
+/* Bytes of workspace gdn_chunk_bwd needs; reads only sizes, dtype and whether cu_seqlens is
+ * NULL. */
+gdn_status_t gdn_chunk_bwd_workspace_size(const gdn_chunk_bwd_args *args, size_t *bytes);
+gdn_status_t gdn_chunk_bwd(const gdn_chunk_bwd_args *args, gdn_stream_t stream);
+
+/*
  * Chunked forward with one log-gate per token, value head and key channel
  * (KDA).  Shapes follow chunk_kda_fwd_kernel_inter_solve_fused (vLLM kimi_k3
  * kda/chunk_intra page):
