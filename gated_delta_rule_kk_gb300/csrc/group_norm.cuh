@@ -100,8 +100,9 @@ __device__ __forceinline__ void norm_act(int act, const float *z, float *out, fl
   norm_sigmoid<VEC>(s, z);
 #pragma unroll
   for (int e = 0; e < VEC; ++e) {
-    out[e] = act == GDN_ACT_SILU ? z[e] * s[e] : s[e];
-    if (slope) slope[e] = s[e] * fmaf(act == GDN_ACT_SILU ? z[e] : 1.f, 1.f - s[e],
+    const float v = z[e];  // (out may be z)
+    out[e] = act == GDN_ACT_SILU ? v * s[e] : s[e];
+    if (slope) slope[e] = s[e] * fmaf(act == GDN_ACT_SILU ? v : 1.f, 1.f - s[e],
                                       act == GDN_ACT_SILU ? 1.f : 0.f);
   }
 }
