@@ -303,6 +303,13 @@ __device__ __forceinline__ void stmatrix_x4(void *row_addr, uint32_t r0, uint32_
                : "memory");
 }
 
+// An 8x8 b16 matrix, a word (two neighbours of a row) a lane, transposed.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
 // D (16x8, fp32) += A (16x16, bf16, row-major fragment) * B (16x8, bf16,
 // column-major fragment).
 __device__ __forceinline__ void mma_16816_bf16(float *d, const uint32_t *a, uint32_t b0,
