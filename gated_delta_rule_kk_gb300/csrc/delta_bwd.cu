@@ -114,15 +114,16 @@ DeltaBwdParams make_params(const gdn_chunk_bwd_args &a) {
   return p;
 }
 
-// The table, rounded up to 256 bytes, then the blocks.
+// The table, rounded up to 256 bytes, then the blocks, then scratch.
 size_t table_bytes(const DeltaBwdParams &p) {
   if (p.cu == nullptr) return 0;
   return ((size_t)(p.N + 1 + p.chunks) * sizeof(int32_t) + 255) / 256 * 256;
 }
 
-size_t workspace_bytes(const DeltaBwdParams &p) {
+size_t workspace_bytes(const DeltaBwdParams &p, bool bf16) {
   if (p.T == 0) return 0;
-  return table_bytes(p) + (size_t)p.chunks * p.H * p.block;
+  return table_bytes(p) + (size_t)p.chunks * p.H * p.block +
+         (delta_bwd_tc_supported(p, bf16) ? delta_bwd_tc_scratch(p) : 0);
 }
 
 }  // namespace
@@ -137,7 +138,7 @@ gdn_status_t gdn_chunk_bwd_workspace_size(const gdn_chunk_bwd_args *a, size_t *b
   *bytes = 0;
   gdn_status_t st = check_args(*a, true);
   if (st != GDN_OK) return st;
-  *bytes = workspace_bytes(make_params(*a));
+  *bytes = workspace_bytes(make_params(*a), a->dtype == GDN_BF16);
   return GDN_OK;
 }
 
@@ -155,13 +156,15 @@ gdn_status_t gdn_chunk_bwd(const gdn_chunk_bwd_args *a, gdn_stream_t stream) {
                                : cudaMemsetAsync(p.dh0, 0, n, s),
                          "state gradient copy");
   }
-  const size_t need = workspace_bytes(p);
+  const bool bf16 = a->dtype == GDN_BF16;
+  const size_t need = workspace_bytes(p, bf16);
   CHECK_THAT(a->workspace != nullptr && a->workspace_bytes >= need, GDN_ERR_WORKSPACE,
              "workspace of %zu bytes needed (got %zu)", need, a->workspace_bytes);
   CHECK_THAT(aligned_to(a->workspace, 256), GDN_ERR_MISALIGNED, "workspace is not 256-byte aligned");
   p.first = static_cast<int32_t *>(a->workspace);
   p.owner = p.first + p.N + 1;
   p.blocks = static_cast<unsigned char *>(a->workspace) + table_bytes(p);
+  p.scratch = reinterpret_cast<float *>(p.blocks + (size_t)p.chunks * p.H * p.block);
   p.err = device_error_word();
   if (p.err == nullptr) return launch_status(cudaGetLastError(), "device error word");
   if (p.cu != nullptr) {
@@ -169,7 +172,6 @@ gdn_status_t gdn_chunk_bwd(const gdn_chunk_bwd_args *a, gdn_stream_t stream) {
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return launch_status(e, "chunk table launch");
   }
-  const bool bf16 = a->dtype == GDN_BF16;
   return launch_status(delta_bwd_tc_supported(p, bf16) ? launch_delta_bwd_tc(p, s)
                                                        : launch_delta_bwd_simt(p, bf16, s),
                        "chunk gradient launch");

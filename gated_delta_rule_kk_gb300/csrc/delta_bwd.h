@@ -44,6 +44,7 @@ struct DeltaBwdParams {
   int32_t *owner;             // [chunks] sequence of every chunk
   unsigned char *blocks;      // [chunks][H] of `block` bytes each
   int64_t block;
+  float *scratch;             // of delta_bwd_tc_scratch() bytes, behind the blocks
 };
 
 // A chunk: its sequence, its place there, its first token and how many it has.
@@ -91,6 +92,7 @@ __device__ __forceinline__ bool delta_good(const DeltaBwdParams &p) {
 // Whether the tensor cores take the call, the bytes of a chunk and head, and the launches.
 bool delta_bwd_tc_supported(const DeltaBwdParams &p, bool bf16);
 int64_t delta_bwd_tc_block(const DeltaBwdParams &p);
+int64_t delta_bwd_tc_scratch(const DeltaBwdParams &p);
 cudaError_t launch_delta_bwd_tc(const DeltaBwdParams &p, cudaStream_t stream);
 int64_t delta_bwd_simt_block(const DeltaBwdParams &p);
 cudaError_t launch_delta_bwd_simt(const DeltaBwdParams &p, bool bf16, cudaStream_t stream);

@@ -1,10 +1,11 @@
 // Matrix fragments, images and the workspace of the gated delta rule's gradient on the tensor
-// cores, shared by delta_bwd_walk.cu (the states and their gradients, chunk after chunk) and
-// delta_bwd_tc.cu (what every chunk does by itself).  delta_bwd.h has the formulas.
+// cores, shared by delta_bwd_tc.cu (T and P of every chunk), delta_bwd_walk.cu (the states and
+// their gradients, chunk after chunk) and delta_bwd_inputs.cu (the inputs' gradients).
+// delta_bwd.h has the formulas.
 //
-// Every product is of 64 x 64 x 32 .. 64 x 128 x 128 and stands between element-wise gates,
-// masks and sums, so accumulators stay in registers (warp-level matrix instructions) instead
-// of passing through tensor memory between each two of them.  q, k, v and do are bfloat16 and
+// Where products stand between element-wise gates, masks and sums, accumulators stay in
+// registers (warp-level matrix instructions) instead of passing through tensor memory between
+// each two of them; what is plain contraction runs on tcgen05.  q, k, v and do are bfloat16 and
 // exact; what is float32 (T, P, the states h and their gradients D, the corrected values n and
 // dr) enters as a pair of bfloat16 pieces, hi + lo, with the products hi hi + hi lo + lo hi:
 // off by 2^-17 of each value at most, so that the float32 results (dg, dbeta, dh0) are not
@@ -18,6 +19,7 @@
 #include "delta_bwd.h"
 #include "gdn_common.cuh"
 #include "ptx.cuh"
+#include "rows.cuh"
 
 namespace gdn {
 
@@ -101,13 +103,7 @@ struct Block {
   }
 };
 
-// Straight copies between shared memory and the workspace, by all threads.
-template <int THREADS>
-__device__ __forceinline__ void fetch(void *to, const void *from, int bytes) {
-  for (int i = threadIdx.x * 16; i < bytes; i += THREADS * 16)
-    ptx::cp_async16(static_cast<unsigned char *>(to) + i,
-                    static_cast<const unsigned char *>(from) + i, true);
-}
+// A straight copy from shared memory to the workspace, by all threads.
 template <int THREADS>
 __device__ __forceinline__ void keep(void *to, const void *from, int bytes) {
   for (int i = threadIdx.x * 16; i < bytes; i += THREADS * 16)
@@ -122,28 +118,11 @@ __device__ __forceinline__ void fetch_rows(bf16 *to, const void *tensor, const D
                                            int heads, int head, int D, int c0) {
   const bf16 *from = static_cast<const bf16 *>(tensor) + (ch.token * heads + head) * D;
   const int64_t stride = (int64_t)heads * D;
-  for (int i = threadIdx.x; i < Q * COLS / 8; i += THREADS) {
+  for (int i = threadIdx.x % THREADS; i < Q * COLS / 8; i += THREADS) {
     const int row = i / (COLS / 8), col = i % (COLS / 8) * 8;
     const bool ok = row < ch.len && c0 + col < D;
     ptx::cp_async16(to + at<COLS>(row, col), ok ? from + row * stride + c0 + col : from, ok);
   }
-}
-
-// Fragments from 8 x 8 tiles, COLS / 8 of them a row of tiles.  A from [k][m], B (two tiles of
-// eight columns) from [k][n].
-template <int COLS>
-__device__ __forceinline__ void lda_tiles(uint32_t (&a)[4], const bf16 *s, int m0, int k0) {
-  const int l = threadIdx.x & 31;
-  ptx::ldmatrix_x4_trans(
-      s + ((k0 / 8 + (l >> 4)) * (COLS / 8) + m0 / 8 + ((l >> 3) & 1)) * 64 + (l & 7) * 8, a[0],
-      a[1], a[2], a[3]);
-}
-template <int COLS>
-__device__ __forceinline__ void ldb_tiles(uint32_t (&b)[4], const bf16 *s, int n0, int k0) {
-  const int l = threadIdx.x & 31;
-  ptx::ldmatrix_x4_trans(
-      s + ((k0 / 8 + ((l >> 3) & 1)) * (COLS / 8) + n0 / 8 + (l >> 4)) * 64 + (l & 7) * 8, b[0],
-      b[1], b[2], b[3]);
 }
 
 // x and y as two words, the upper and the lower pieces.
@@ -155,6 +134,10 @@ __device__ __forceinline__ void split(float x, float y, uint32_t &hi, uint32_t &
   lo = *reinterpret_cast<const uint32_t *>(&l);
 }
 
+// Most blocks of the kernel of the inputs' gradients (each has scratch of its own).
+constexpr int DELTA_MAX_BLOCKS = 256;
+
+cudaError_t launch_delta_inputs(const DeltaBwdParams &p, cudaStream_t stream);
 cudaError_t launch_delta_walks(const DeltaBwdParams &p, cudaStream_t stream);
 
 }  // namespace gdn

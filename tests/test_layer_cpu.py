@@ -153,7 +153,7 @@ def test_delta_gradient_workspace(lib):
     n = ctypes.c_size_t(9)
 
     def need(**kw):
-        a = delta_args(**kw)
+        a = delta_args(**{"Hg": 4, **kw})
         assert lib.gdn_chunk_bwd_workspace_size(ctypes.byref(a), ctypes.byref(n)) == Status.OK
         return n.value
 
@@ -164,7 +164,10 @@ def test_delta_gradient_workspace(lib):
     assert need(T=1) == 2 * 4 * block
     # packed: at most one more chunk than the whole chunks of the tokens, a sequence
     assert need(B=1, N=5, T=128, cu_seqlens=FAKE) == 256 + (5 + 2) * 4 * block
-    assert need(dtype=0) >= 2 * 2 * 4 * block
+    # in float32 once, not as pieces and images: gates, T, P, n, dr, h, D
+    assert need(dtype=0) == 2 * 2 * 4 * 4 * (2 * 64 + 2 * 64 * 64 + 2 * 64 * 128 + 2 * 128 * 128)
+    # heads that share a key head: sums of dq and dk for every block of the last kernel
+    assert need(Hg=2) == 2 * 2 * 4 * block + 2 * 2 * 2 * 2 * 64 * 128 * 4
     big = need(B=1, N=1, T=1 << 24)
     assert big == (1 << 18) * 4 * block  # beyond 32 bits
     a = delta_args(H=3)
