@@ -9,8 +9,9 @@
 // of tensor memory, while the warps finish the chunk before: they take over the accumulators
 // (as fragments, which is how tcgen05.ld's 16x256b form gives them), apply gates and masks,
 // and do what is left, dq += (dP L) k and dk += (dP L)^T q + .., on warp-level instructions.
-// One block an SM, persistent, 20 warps: bulk loads; the tcgen05 issuer; <h, D>; do's rows;
-// sixteen that finish, and fetch q and k two items ahead.  Every wait is bounded; a role whose wait ran out
+// One block an SM, persistent, 20 warps: loads; the tcgen05 issuer; <h, D>; one that fetches
+// q and k and adds up dbeta and dg; sixteen that finish.  (q and k come as a bulk copy a row:
+// as 16-byte copies by all threads they held those up for 4500 cycles a chunk.)  Every wait is bounded; a role whose wait ran out
 // issues nothing more.
 // (All on warp-level instructions, 16 warps a chunk, phase after phase: 245 us at 2 x 4096
 // tokens, 16 heads of 128, of which the products took 6 of 18 us a chunk and waiting for loads
@@ -27,7 +28,7 @@ constexpr int IN_WARPS = 20, IN_FINISH = 16;  // of a block; of them, the ones t
 
 template <int KP>
 struct InputsShared {
-  static constexpr int KQ = 2 * Q * KP * 2;  // q, k of an item
+  static constexpr int PITCH = KP + 8, KQ = 2 * Q * PITCH * 2;  // q, k of an item
   static constexpr int DO_ = Q * VT * 2, ROWS = Block<KP>::ROWS, STATE = Block<KP>::STATE;
   // a value tile: do as 8 x 8 tiles [v][token] of tokens' rows, dr, n, h, D as they lie in the
   // workspace
@@ -46,6 +47,27 @@ constexpr int XQ = 0, XK = 128, XS = 256, DP = 384, DA = 448;
 struct InputsItem {
   int64_t token;
   int len;
+};
+
+// The items of a block in turn: chunks x key heads, blockIdx.x, + gridDim.x, ..
+struct InputsWalk {
+  int64_t c, chunks;
+  int hk, heads, dc, dh;
+  __device__ __forceinline__ InputsWalk(int64_t chunks_, int heads_) : chunks(chunks_), heads(heads_) {
+    c = blockIdx.x / heads;
+    hk = blockIdx.x % heads;
+    dc = gridDim.x / heads;
+    dh = gridDim.x % heads;
+  }
+  __device__ __forceinline__ bool there() const { return c < chunks; }
+  __device__ __forceinline__ void next() {
+    c += dc;
+    hk += dh;
+    if (hk >= heads) {
+      hk -= heads;
+      ++c;
+    }
+  }
 };
 
 // N fragments (16 rows x 8 columns each) of this warp's quarter of tensor memory, rows 0 .. 15.
@@ -144,15 +166,15 @@ __device__ __forceinline__ float dot_value(const DeltaBwdParams &p, const Block<
 template <int KP, bool GROUPED>
 __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdParams p) {
   using S = InputsShared<KP>;
-  constexpr int NT = KP / 32;  // tiles of 8 columns of a warp's quarter of [64][KP]
+  constexpr int NT = KP / 32, PITCH = S::PITCH;  // tiles of 8 columns of a warp's quarter of [64][KP]
   extern __shared__ __align__(128) unsigned char shared[];
-  __shared__ uint64_t st_full[2], st_empty[2], x_full, x_empty;
-  __shared__ InputsItem place[4];
-  __shared__ float hD[2];
+  __shared__ uint64_t st_full[2], st_empty[2], x_full, x_empty, kq_full[2], pa_full, begun, summed[2], counted[2];
+  __shared__ InputsItem place[2];
+  __shared__ float hD[4];
   __shared__ uint32_t tmem_at;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rep = p.H / p.Hg, tiles = (p.V + VT - 1) / VT;
-  const int64_t chunks = p.cu ? p.first[p.N] : p.chunks, items = chunks * p.Hg;
+  const int64_t chunks = p.cu ? p.first[p.N] : p.chunks;  // (-1 with bad offsets)
   if (!bounds_ok(chunks <= p.chunks && gridDim.x <= DELTA_MAX_BLOCKS, p.err)) return;
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
@@ -161,9 +183,20 @@ __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdPar
     }
     ptx::mbar_init(&x_full, 2);
     ptx::mbar_init(&x_empty, IN_FINISH);
+    ptx::mbar_init(&pa_full, 1);
+    ptx::mbar_init(&begun, 1);
+    for (int s = 0; s < 2; ++s) {
+      ptx::mbar_init(&kq_full[s], 1);
+      ptx::mbar_init(&summed[s], IN_FINISH);
+      ptx::mbar_init(&counted[s], 1);
+    }
     ptx::fence_mbar_init();
   }
   if (warp == 0) ptx::tmem_alloc<512>(&tmem_at);
+  // (channels past K stay zero: the rows' copies end before them)
+  for (int i = threadIdx.x; i < 2 * S::KQ / 16; i += 32 * IN_WARPS)
+    reinterpret_cast<uint4 *>(shared)[i] = make_uint4(0, 0, 0, 0);
+  ptx::fence_proxy_async_smem();
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -173,13 +206,13 @@ __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdPar
     ok = ptx::mbar_wait_bounded(bar, (uint32_t)(use & 1), ok ? 1u << 22 : 1u) && ok;
   };
   auto stage = [&](int s) { return shared + S::STAGES + (s & 1) * S::STAGE; };
-  if (warp == 0) {  // the workspace's share of every stage
+  if (warp == 0) {  // stages: what the workspace has, and do's rows as a left operand of tcgen05
     int s = 0;
-    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-      const int64_t c = it / p.Hg;
-      const int hk = (int)(it - c * p.Hg);
-      for (int head = hk * rep; head < (hk + 1) * rep; ++head) {
-        const Block<KP> w(p, c, head);
+    for (InputsWalk it(chunks, p.Hg); it.there(); it.next()) {
+      const DeltaChunk ch = delta_chunk(p, it.c);
+      for (int head = it.hk * rep; head < (it.hk + 1) * rep; ++head) {
+        const Block<KP> w(p, it.c, head);
+        const bf16 *from = static_cast<const bf16 *>(p.dout) + (ch.token * p.H + head) * p.V;
         for (int v = 0; v < tiles; ++v, ++s) {
           if (s >= 2) wait(&st_empty[s & 1], s / 2 - 1);
           if (!__all_sync(~0u, ok)) break;
@@ -192,6 +225,18 @@ __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdPar
           if (lane == 2) ptx::bulk_g2s(to + S::H_AT, w.h(v), S::STATE, &st_full[s & 1]);
           if (lane == 3) ptx::bulk_g2s(to + S::D_AT, w.D(v), S::STATE, &st_full[s & 1]);
           __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {  // four pieces of 8 rows at a time
+            const int row = e * 8 + lane / 4, col = lane % 4, at = v * VT + col * 8;
+            const bool in = row < ch.len && at < p.V;
+            ptx::cp_async16(to + (col * 8 + row / 8) * 128 + row % 8 * 16,
+                            in ? from + (int64_t)row * p.H * p.V + at : from, in);
+          }
+          ptx::cp_async_commit();
+          ptx::cp_async_wait<0>();
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&st_full[s & 1]);
         }
       }
     }
@@ -201,7 +246,7 @@ __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdPar
     const uint32_t wide = ptx::idesc_bf16(64, KP, 0, 1), wide_t = ptx::idesc_bf16(64, KP, 1, 1);
     const uint32_t square = ptx::idesc_bf16(64, Q, 0, 1), square_t = ptx::idesc_bf16(64, Q, 1, 1);
     int m = 0, s = 0;  // heads and stages so far
-    for (int64_t it = blockIdx.x; it < items; it += gridDim.x)
+    for (InputsWalk it(chunks, p.Hg); it.there(); it.next())
       for (int r = 0; r < rep; ++r, ++m) {
         if (m >= 1) wait(&x_empty, m - 1);
         ptx::tc_fence_after();
@@ -250,7 +295,7 @@ __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdPar
     if (m >= 1 && ok) wait(&x_full, m - 1);  // nothing is left on its way
   } else if (warp == 2) {  // <h, D>
     int m = 0, s = 0;
-    for (int64_t it = blockIdx.x; it < items; it += gridDim.x)
+    for (InputsWalk it(chunks, p.Hg); it.there(); it.next())
       for (int r = 0; r < rep; ++r, ++m) {
         float sum = 0.f;
         for (int v = 0; v < tiles; ++v, ++s) {
@@ -281,86 +326,113 @@ __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdPar
         // (with the accumulators taken over, x_full's phase before is over)
         if (m >= 1) wait(&x_empty, m - 1);
         if (lane == 0) {
-          hD[m & 1] = sum;
+          hD[m & 3] = sum;
           ptx::mbar_arrive(&x_full);
         }
       }
-  } else if (warp == 3) {  // do's rows of every stage, as a left operand of tcgen05
-    int s = 0;
-    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-      const int64_t c = it / p.Hg;
-      const int hk = (int)(it - c * p.Hg);
-      const DeltaChunk ch = delta_chunk(p, c);
-      for (int head = hk * rep; head < (hk + 1) * rep; ++head) {
-        const bf16 *from = static_cast<const bf16 *>(p.dout) + (ch.token * p.H + head) * p.V;
-        for (int v = 0; v < tiles; ++v, ++s) {
-          if (s >= 2) wait(&st_empty[s & 1], s / 2 - 1);
-          if (!__all_sync(~0u, ok)) break;
-          unsigned char *to = stage(s);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {  // four pieces of 8 rows at a time
-            const int row = e * 8 + lane / 4, col = lane % 4, at = v * VT + col * 8;
-            const bool in = row < ch.len && at < p.V;
-            ptx::cp_async16(to + (col * 8 + row / 8) * 128 + row % 8 * 16,
-                            in ? from + (int64_t)row * p.H * p.V + at : from, in);
-          }
-          ptx::cp_async_commit();
-          ptx::cp_async_wait<0>();
-          ptx::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&st_full[s & 1]);
+  } else if (warp == 3) {
+    // The clerk: an item's q and k, one ahead of the item that is finished; of a finished head
+    // dbeta, and dG summed from the end (lane l has tokens l and l + 32).
+    int m = 0, n = 0;
+    InputsWalk ahead(chunks, p.Hg);
+    auto fetch = [&] {
+      if (!ahead.there() || !__all_sync(~0u, ok)) return;
+      const DeltaChunk ch = delta_chunk(p, ahead.c);
+      bf16 *to = reinterpret_cast<bf16 *>(shared + (n & 1) * S::KQ);
+      for (int row = ch.len; row < Q; ++row)  // (their weights are zero: they may not be NaN)
+        for (int i = lane; i < PITCH / 8; i += 32) {
+          reinterpret_cast<uint4 *>(to + row * PITCH)[i] = make_uint4(0, 0, 0, 0);
+          reinterpret_cast<uint4 *>(to + (Q + row) * PITCH)[i] = make_uint4(0, 0, 0, 0);
         }
+      ptx::fence_proxy_async_smem();
+      if (lane == 0) place[n & 1] = {ch.token, ch.len};
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_expect_tx(&kq_full[n & 1], 2 * ch.len * p.K * 2);
+      __syncwarp();
+      const int64_t stride = (int64_t)p.Hg * p.K, from = ch.token * stride + ahead.hk * p.K;
+      for (int row = lane; row < ch.len; row += 32) {
+        ptx::bulk_g2s(to + row * PITCH, static_cast<const bf16 *>(p.q) + from + row * stride, p.K * 2,
+                      &kq_full[n & 1]);
+        ptx::bulk_g2s(to + (Q + row) * PITCH, static_cast<const bf16 *>(p.k) + from + row * stride,
+                      p.K * 2, &kq_full[n & 1]);
+      }
+      ++n;
+      ahead.next();
+    };
+    fetch();
+    for (InputsWalk it(chunks, p.Hg); it.there(); it.next()) {
+      const DeltaChunk ch = delta_chunk(p, it.c);
+      for (int head = it.hk * rep; head < (it.hk + 1) * rep; ++head, ++m) {
+        if (head == it.hk * rep) {
+          wait(&begun, m / rep);  // the item before has read its q and k
+          fetch();
+        }
+        wait(&summed[m & 1], m / 2);
+        const float *sums = reinterpret_cast<const float *>(shared + S::SUMS) + (m & 1) * S::SUM_SET;
+        const float *qd = sums, *kh = qd + 4 * Q, *kD = kh + 4 * Q, *rM = kD + 4 * Q, *rB = rM + 4 * Q;
+        const float *cM = rB + 4 * Q, *rn = cM + 4 * Q, *beta = rn + 2 * Q, *eG = beta + Q;
+        const float state = hD[m & 3];
+        float d[2], db[2], all = 0.f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int i = lane + 32 * e;
+          auto all_of = [&](const float *x) { return (x[i] + x[Q + i]) + (x[2 * Q + i] + x[3 * Q + i]); };
+          const float kd = all_of(kD), khi = all_of(kh);
+          d[e] = all_of(rM) - all_of(cM) + all_of(qd) + beta[i] * khi - kd;
+          all += kd;
+          // dbeta = dr.n / beta, as n is beta times what it does not depend on it by
+          const bool none = fabsf(beta[i]) < 1e-30f;
+          db[e] = none ? khi + all_of(rB) : rn[i] / beta[i];
+          for (unsigned z = __ballot_sync(~0u, none && i < ch.len); z; z &= z - 1) {
+            const int l = __ffs(z) - 1;
+            const float v = dot_value<KP>(p, Block<KP>(p, it.c, head), ch.token, head, l + 32 * e);
+            if (lane == l) db[e] += v;
+          }
+          if (i < ch.len) p.dbeta[(ch.token + i) * p.H + head] = db[e];
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(~0u, all, o);
+        const float end = fmaf(eG[Q - 1], state, all);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (lane + 32 * e == ch.len - 1) d[e] += end;
+        if (!p.g_is_cumsum) {
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const float a = __shfl_down_sync(~0u, d[0], o), b = __shfl_down_sync(~0u, d[1], o);
+            if (lane + o < 32) {
+              d[0] += a;
+              d[1] += b;
+            }
+          }
+          d[0] += __shfl_sync(~0u, d[1], 0);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (lane + 32 * e < ch.len) p.dg[(ch.token + lane + 32 * e) * p.H + head] = d[e];
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&counted[m & 1]);
       }
     }
+    for (int k = max(0, n - 2); k < n && ok; ++k) wait(&kq_full[k & 1], k / 2);  // all have landed
   } else {
     // Sixteen warps finish a head: rows 16 wm (their quarter of tensor memory), quarter wn of
     // the columns.
     const int tid = threadIdx.x - 128, wm = warp & 3, wn = (warp - 4) >> 2, g = lane >> 2, t = lane & 3;
     const uint32_t quarter = tmem + ((uint32_t)(32 * wm) << 16);
     bf16 *PL = reinterpret_cast<bf16 *>(shared + S::MATS), *AL = PL + 2 * Q * Q;
-    // where the i-th item of this block is, for all the others
-    auto find = [&](int i) {
-      const int64_t it = blockIdx.x + (int64_t)i * gridDim.x;
-      if (tid != 0 || it >= items) return;
-      const DeltaChunk ch = delta_chunk(p, it / p.Hg);
-      place[i & 3] = {ch.token, ch.len};
-    };
-    // its q and k
-    auto fetch = [&](int i) {
-      const int64_t it = blockIdx.x + (int64_t)i * gridDim.x;
-      if (it < items) {
-        const int64_t stride = (int64_t)p.Hg * p.K;
-        const int64_t from = place[i & 3].token * stride + it % p.Hg * p.K;
-        const int len = place[i & 3].len;
-        bf16 *to = reinterpret_cast<bf16 *>(shared + (i & 1) * S::KQ);
-#pragma unroll
-        for (int e = tid; e < Q * KP / 8; e += 32 * IN_FINISH) {
-          const int row = e / (KP / 8), col = e % (KP / 8) * 8;
-          const bool in = row < len && col < p.K;
-          const int64_t at_ = in ? from + row * stride + col : from;
-          ptx::cp_async16(to + at<KP>(row, col), static_cast<const bf16 *>(p.q) + at_, in);
-          ptx::cp_async16(to + Q * KP + at<KP>(row, col), static_cast<const bf16 *>(p.k) + at_, in);
-        }
-      }
-      ptx::cp_async_commit();
-    };
-    find(0);
-    find(1);
-    finishers_meet();
-    fetch(0);
-    fetch(1);
     int m = 0, n = 0;
     float gate = 0.f;
-    if (blockIdx.x < items && tid < 4 * Q)
-      gate = Block<KP>(p, blockIdx.x / p.Hg, blockIdx.x % p.Hg * rep).sc()[tid];
-    for (int64_t it = blockIdx.x; it < items; it += gridDim.x, ++n) {
-      const int64_t c = it / p.Hg;
-      const int hk = (int)(it - c * p.Hg);
-      const int64_t token = place[n & 3].token;
-      const int len = place[n & 3].len;
-      const bf16 *q = reinterpret_cast<const bf16 *>(shared + (n & 1) * S::KQ), *k = q + Q * KP;
-      find(n + 2);
-      ptx::cp_async_wait<1>();  // this item's q and k; visible behind the next meeting
+    InputsWalk it(chunks, p.Hg);
+    if (it.there() && tid < 4 * Q) gate = Block<KP>(p, it.c, it.hk * rep).sc()[tid];
+    for (; it.there(); ++n) {
+      const int64_t c = it.c;
+      const int hk = it.hk;
+      it.next();  // (from here on the next one)
+      wait(&kq_full[n & 1], n / 2);
+      const int64_t token = place[n & 1].token;
+      const int len = place[n & 1].len;
+      const bf16 *q = reinterpret_cast<const bf16 *>(shared + (n & 1) * S::KQ), *k = q + Q * PITCH;
       for (int head = hk * rep; head < (hk + 1) * rep; ++head, ++m) {
         // by quarters: q.dq_h, k.dk_h / beta, k.dk_s, rows of M, rows of B; columns of M by wm;
         // dr.n; gates
@@ -369,19 +441,24 @@ __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdPar
         float *cM = rB + 4 * Q, *rn = cM + 4 * Q, *sc = rn + Q;
         const float *G = sc, *beta = sc + Q, *eG = sc + 2 * Q, *eR = sc + 3 * Q;
         const bool last = head + 1 == (hk + 1) * rep;
+        if (m >= 2) wait(&counted[m & 1], m / 2 - 1);  // the sums' place is free
         if (tid < 4 * Q) {
           sc[tid] = gate;
           // the next head's gates, on their way meanwhile
-          const int64_t next = last ? it + gridDim.x : it;
-          if (next < items) {
-            const int64_t nc = last ? next / p.Hg : c;
-            gate = Block<KP>(p, nc, last ? (int)(next - nc * p.Hg) * rep : head + 1).sc()[tid];
+          if (!last || it.there())
+            gate = Block<KP>(p, last ? it.c : c, last ? it.hk * rep : head + 1).sc()[tid];
+        }
+        ptx::fence_proxy_async_smem();
+        finishers_meet();
+        if (tid == 0) {  // the head before is through: P and A to where dP L and dA L beta will be
+          if (head == hk * rep) ptx::mbar_arrive(&begun);
+          if (ok) {
+            ptx::mbar_arrive_expect_tx(&pa_full, 2 * Block<KP>::SQUARE);
+            ptx::bulk_g2s(PL, Block<KP>(p, c, head).P(), 2 * Block<KP>::SQUARE, &pa_full);
           }
         }
-        finishers_meet();
         wait(&x_full, m);
         ptx::tc_fence_after();
-        const float state = hD[m & 1];
         float dq[NT][4], dk[NT][4], dP[2][4], dA[2][4];
         {
           float xs[NT][4];
@@ -401,7 +478,7 @@ __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdPar
             const float fq = p.scale * eG[row], fk = -eG[row], fs = eR[row], be = beta[row];
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-              const int at_ = at<KP>(row, wn * (KP / 4) + 8 * j + 2 * t);
+              const int at_ = at<PITCH>(row, wn * (KP / 4) + 8 * j + 2 * t);
               const float2 x = get_pair(q, at_), y = get_pair(k, at_);
 #pragma unroll
               for (int u = 0; u < 2; ++u) {
@@ -420,19 +497,9 @@ __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdPar
           put_rows(kh + wn * Q, 16 * wm + g, t, b[0], b[1]);
           put_rows(kD + wn * Q, 16 * wm + g, t, d[0], d[1]);
         }
-        // q k^T and k k^T where this warp has dP and dA: M, dP L and dA L beta
+        // M, dP L and dA L beta, each element of P and A replaced by the thread that read it
+        wait(&pa_full, m);
         {
-          float sq[2][4] = {}, sk[2][4] = {};
-          if (wn <= wm)
-#pragma unroll
-            for (int kk = 0; kk < KP; kk += 16) {
-              uint32_t x[4], y[4], b[4];
-              ldb<KP>(b, k, 16 * wn, kk);
-              lda<KP>(x, q, 16 * wm, kk);
-              lda<KP>(y, k, 16 * wm, kk);
-              mma2(sq, x, b);
-              mma2(sk, y, b);
-            }
           float ms[2] = {}, bs[2] = {}, cols[2][2] = {};
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
@@ -441,23 +508,26 @@ __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdPar
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               const int col = 16 * wn + 8 * j + 2 * t;
+              const int spot = at<64>(row, col);
+              const float2 Ph = get_pair(PL, spot), Pl = get_pair(PL + Q * Q, spot);
+              const float2 Ah = get_pair(AL, spot), Al = get_pair(AL + Q * Q, spot);
               float pl[2], al[2];
 #pragma unroll
               for (int u = 0; u < 2; ++u) {
-                const float raw = dA[j][2 * e + u];
+                const float raw = dA[j][2 * e + u], own = dP[j][2 * e + u];
                 if (row == col + u) rn[row] = raw;
-                const bool in = row >= col + u && row < len;
+                const bool in = row >= col + u && row < len, below = in && row > col + u;
                 const float L = in ? __expf(Gr - G[col + u]) : 0.f;
-                pl[u] = in ? L * p.scale * dP[j][2 * e + u] : 0.f;
-                const float x = in && row > col + u ? -L * raw : 0.f, B = x * sk[j][2 * e + u];
-                al[u] = be * x;
-                const float M = fmaf(pl[u], sq[j][2 * e + u], be * B);
+                pl[u] = in ? L * p.scale * own : 0.f;
+                al[u] = below ? -be * L * raw : 0.f;
+                const float B = below ? -raw * (u ? Ah.y + Al.y : Ah.x + Al.x) : 0.f;
+                const float M = fmaf(in ? own : 0.f, u ? Ph.y + Pl.y : Ph.x + Pl.x, be * B);
                 ms[e] += M;
                 bs[e] += B;
                 cols[j][u] += M;
               }
-              put_pair(PL, PL + Q * Q, at<64>(row, col), pl[0], pl[1]);
-              put_pair(AL, AL + Q * Q, at<64>(row, col), al[0], al[1]);
+              put_pair(PL, PL + Q * Q, spot, pl[0], pl[1]);
+              put_pair(AL, AL + Q * Q, spot, al[0], al[1]);
             }
           }
           put_rows(rM + wn * Q, 16 * wm + g, t, ms[0], ms[1]);
@@ -479,7 +549,7 @@ __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdPar
           uint32_t a[4], al[4], b[NT / 2][4];
           auto add = [&](float (*to)[4], const bf16 *rows) {
 #pragma unroll
-            for (int u = 0; u < NT / 2; ++u) ldb_t<KP>(b[u], rows, wn * (KP / 4) + 16 * u, 16 * i);
+            for (int u = 0; u < NT / 2; ++u) ldb_t<PITCH>(b[u], rows, wn * (KP / 4) + 16 * u, 16 * i);
 #pragma unroll
             for (int u = 0; u < NT / 2; ++u) mma2(to + 2 * u, a, b[u]);
 #pragma unroll
@@ -530,51 +600,10 @@ __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdPar
             }
           }
         }
-        if (warp == 4 + m % IN_FINISH) {  // dbeta, and dG summed from the end: lane l has tokens l, l + 32
-          float d[2], db[2], all = 0.f;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int i = lane + 32 * e;
-            auto all_of = [&](const float *x) { return (x[i] + x[Q + i]) + (x[2 * Q + i] + x[3 * Q + i]); };
-            const float kd = all_of(kD), khi = all_of(kh);
-            d[e] = all_of(rM) - all_of(cM) + all_of(qd) + beta[i] * khi - kd;
-            all += kd;
-            // dbeta = dr.n / beta, as n is beta times what it does not depend on it by
-            const bool none = fabsf(beta[i]) < 1e-30f;
-            db[e] = none ? khi + all_of(rB) : rn[i] / beta[i];
-            for (unsigned z = __ballot_sync(~0u, none && i < len); z; z &= z - 1) {
-              const int l = __ffs(z) - 1;
-              const float v = dot_value<KP>(p, Block<KP>(p, c, head), token, head, l + 32 * e);
-              if (lane == l) db[e] += v;
-            }
-            if (i < len) p.dbeta[(token + i) * p.H + head] = db[e];
-          }
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(~0u, all, o);
-          const float end = fmaf(eG[Q - 1], state, all);
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            if (lane + 32 * e == len - 1) d[e] += end;
-          if (!p.g_is_cumsum) {
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-              const float a = __shfl_down_sync(~0u, d[0], o), b = __shfl_down_sync(~0u, d[1], o);
-              if (lane + o < 32) {
-                d[0] += a;
-                d[1] += b;
-              }
-            }
-            d[0] += __shfl_sync(~0u, d[1], 0);
-          }
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            if (lane + 32 * e < len) p.dg[(token + lane + 32 * e) * p.H + head] = d[e];
-        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&summed[m & 1]);
       }
-      finishers_meet();  // q and k have been read
-      fetch(n + 2);
     }
-    ptx::cp_async_wait<0>();
   }
   if (!ok && lane == 0) record_error(p.err, GDN_ERR_TIMEOUT);
   ptx::tc_fence_before();

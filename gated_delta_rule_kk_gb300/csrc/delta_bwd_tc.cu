@@ -13,7 +13,7 @@ namespace {
 constexpr int PREP = 256;
 template <int KP>
 struct PrepareShared {
-  static constexpr int IMAGES = 2 * Block<KP>::SQUARE;  // q and k, then T and P
+  static constexpr int IMAGES = 2 * Block<KP>::SQUARE;  // q and k, then P and A, then T
   static constexpr int BYTES = IMAGES + (2 * Q * (Q + 1) + 3 * 16 * 17 + 2 * Q) * 4;
 };
 
@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(PREP, 3) tc_prepare_kernel(DeltaBwdParams p) {
       }
   }
   __syncthreads();  // q and k have been read
-  bf16 *Th = reinterpret_cast<bf16 *>(shared), *Tl = Th + Q * Q, *Ph = Tl + Q * Q, *Pl = Ph + Q * Q;
+  bf16 *Ph = reinterpret_cast<bf16 *>(shared), *Pl = Ph + Q * Q, *Ah = Pl + Q * Q, *Al = Ah + Q * Q;
 #pragma unroll
   for (int j = 0; j < 8; ++j)
 #pragma unroll
@@ -90,16 +90,18 @@ __global__ void __launch_bounds__(PREP, 3) tc_prepare_kernel(DeltaBwdParams p) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const bool in = of_q ? row >= col + e : row > col + e;
-        v[e] = in ? (of_q ? p.scale : beta[row]) * s[j][2 * r + e] * __expf(G[row] - G[col + e]) : 0.f;
+        v[e] = in ? (of_q ? p.scale : 1.f) * s[j][2 * r + e] * __expf(G[row] - G[col + e]) : 0.f;
       }
       if (of_q) {
         put_pair(Ph, Pl, at<64>(row, col), v[0], v[1]);
       } else {
-        A[row][col] = v[0];
-        A[row][col + 1] = v[1];
+        put_pair(Ah, Al, at<64>(row, col), v[0], v[1]);
+        A[row][col] = beta[row] * v[0];
+        A[row][col + 1] = beta[row] * v[1];
       }
     }
   __syncthreads();
+  keep<PREP>(w.P(), shared, 2 * Block<KP>::SQUARE);
   if (tid < Q) {
     const int b = tid / 16 * 16, j = tid % 16;
     float x[16];
@@ -132,13 +134,14 @@ __global__ void __launch_bounds__(PREP, 3) tc_prepare_kernel(DeltaBwdParams p) {
     }
     __syncthreads();
   }
+  bf16 *Th = reinterpret_cast<bf16 *>(shared), *Tl = Th + Q * Q;
   for (int i = tid; i < Q * Q / 2; i += PREP) {
     const int row = i / 32, col = i % 32 * 2;
     put_pair(Th, Tl, at<64>(row, col), row >= col ? T[row][col] : 0.f,
              row >= col + 1 ? T[row][col + 1] : 0.f);
   }
   __syncthreads();
-  keep<PREP>(w.T(), shared, 2 * Block<KP>::SQUARE);
+  keep<PREP>(w.T(), shared, Block<KP>::SQUARE);
 }
 
 template <int KP>

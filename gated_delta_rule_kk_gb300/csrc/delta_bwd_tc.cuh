@@ -28,9 +28,11 @@ using bf16 = __nv_bfloat16;
 constexpr int Q = 64;    // tokens of a chunk
 constexpr int VT = 32;   // value columns of a tile
 
-// Place of (row, col) in an image with rows of COLS elements.
+// Place of (row, col) in an image with rows of COLS elements (72 or 136: rows of 64 or 128 that
+// lie a piece further apart instead).
 template <int COLS>
 __device__ __forceinline__ int at(int row, int col) {
+  if constexpr (COLS % 16 == 8) return row * COLS + col;
   const int turn = COLS == 32 ? (row >> 1) & 3 : row & 7;
   return row * COLS + (((col >> 3) ^ turn) << 3) + (col & 7);
 }
@@ -81,7 +83,7 @@ __device__ __forceinline__ float2 get_pair(const bf16 *s, int place) {
 
 // A chunk and head in the workspace (bytes; KP = K rounded up to 64 or 128): G, beta, e^G and
 // e^(G_L - G) of its tokens (past its end G = G_L and beta = 0), then matrices, each hi then
-// lo: T, P as images; by value tiles n, dr [32][64] and h, D [32][KP], value columns first, as
+// lo: T, P and A without beta as images; by value tiles n, dr [32][64] and h, D [32][KP], value columns first, as
 // 8 x 8 tiles of 128 bytes (a warp holds such a tile as a word a lane, in this order).
 template <int KP>
 struct Block {
@@ -94,12 +96,12 @@ struct Block {
   __device__ float *sc() const { return reinterpret_cast<float *>(base); }
   __device__ unsigned char *T() const { return base + SC; }
   __device__ unsigned char *P() const { return base + SC + SQUARE; }
-  __device__ unsigned char *n(int v) const { return base + SC + 2 * SQUARE + v * ROWS; }
+  __device__ unsigned char *n(int v) const { return base + SC + 3 * SQUARE + v * ROWS; }
   __device__ unsigned char *dr(int v) const { return n(tiles) + v * ROWS; }
   __device__ unsigned char *h(int v) const { return dr(tiles) + v * STATE; }
   __device__ unsigned char *D(int v) const { return h(tiles) + v * STATE; }
   static int64_t bytes(int tiles) {
-    return SC + 2 * SQUARE + (int64_t)tiles * 2 * (ROWS + STATE);
+    return SC + 3 * SQUARE + (int64_t)tiles * 2 * (ROWS + STATE);
   }
 };
 

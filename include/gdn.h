@@ -311,8 +311,8 @@ gdn_status_t gdn_chunk_host_workspace_size(const gdn_chunk_args *args, size_t *b
  * (float32 results are within 1e-5 of their norm).
  * Limits: as gdn_chunk_fwd, and V <= 2^20.  scale <= 0 selects 1/sqrt(K).
  * Workspace: gdn_chunk_bwd_workspace_size() bytes, device memory, 256-byte aligned: for every
- * chunk of 64 tokens and value head T, P, the corrected values and their gradients, the state
- * and its gradient (225 KB with K = V = 128).
+ * chunk of 64 tokens and value head A, T, P, the corrected values and their gradients, the
+ * state and its gradient (241 KB with K = V = 128).
  */
 typedef struct gdn_chunk_bwd_args {
   int32_t dtype;               /* gdn_dtype_t of q, k, v, do, dq, dk, dv */

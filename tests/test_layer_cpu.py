@@ -158,7 +158,7 @@ def test_delta_gradient_workspace(lib):
         return n.value
 
     square, rows, state = 4 * 64 * 64, 4 * 64 * 128, 4 * 128 * 128
-    block = 1024 + 2 * (square + rows + state)
+    block = 1024 + 3 * square + 2 * (rows + state)
     assert need() == 2 * 2 * 4 * block
     assert need(T=0) == 0
     assert need(T=1) == 2 * 4 * block
