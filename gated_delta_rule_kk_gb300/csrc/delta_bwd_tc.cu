@@ -6,25 +6,29 @@
 namespace gdn {
 namespace {
 
-// grid: chunks, heads.  Running log-gates, P and T = (I + A)^-1.  [q; k] k^T on the tensor
-// cores; the inverse in float32 on CUDA cores: the four 16 x 16 blocks on the diagonal by
-// forward substitution, a column a thread, then the blocks below it, a diagonal at a time,
-// T_(b+d, b) = -T_(b+d, b+d) sum_m A_(b+d, m) T_(m, b).
+// grid: chunks, heads.  Running log-gates, P, A and T = (I + A)^-1.  [q; k] k^T on the tensor
+// cores.  The inverse: the four 16 x 16 blocks on the diagonal by forward substitution in
+// float32, a column a thread; then the blocks below it, a diagonal at a time and a warp a
+// block, T_(b+d, b) = -T_(b+d, b+d) sum_m A_(b+d, m) T_(m, b), as products of pairs of
+// bfloat16 pieces: transposed, so that the sum's accumulators are the left operand of the
+// product behind it.  (As float32 sums from shared memory, two loads a multiplication, they
+// took a third of the kernel's instructions: 80 us at 2 x 4096 tokens, 16 heads of 128.)
 constexpr int PREP = 256;
 template <int KP>
 struct PrepareShared {
   static constexpr int IMAGES = 2 * Block<KP>::SQUARE;  // q and k, then P and A, then T
-  static constexpr int BYTES = IMAGES + (2 * Q * (Q + 1) + 3 * 16 * 17 + 2 * Q) * 4;
+  static constexpr int PITCH = Q + 8;  // of A and T in float32
+  static constexpr int BYTES = IMAGES + (2 * Q * PITCH + 2 * Q) * 4;
 };
 
 template <int KP>
 __global__ void __launch_bounds__(PREP, 3) tc_prepare_kernel(DeltaBwdParams p) {
   extern __shared__ __align__(128) unsigned char shared[];
   bf16 *q = reinterpret_cast<bf16 *>(shared), *k = q + Q * KP;
-  float(*A)[Q + 1] = reinterpret_cast<float(*)[Q + 1]>(shared + PrepareShared<KP>::IMAGES);
-  float(*T)[Q + 1] = A + Q;
-  float(*X)[16][17] = reinterpret_cast<float(*)[16][17]>(T + Q);
-  float *G = reinterpret_cast<float *>(X + 3), *beta = G + Q;
+  constexpr int PITCH = PrepareShared<KP>::PITCH;
+  float(*A)[PITCH] = reinterpret_cast<float(*)[PITCH]>(shared + PrepareShared<KP>::IMAGES);
+  float(*T)[PITCH] = A + Q;
+  float *G = reinterpret_cast<float *>(T + Q), *beta = G + Q;
   const DeltaChunk ch = delta_chunk(p, blockIdx.x);
   const int head = blockIdx.y, hk = head / (p.H / p.Hg);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -96,8 +100,7 @@ __global__ void __launch_bounds__(PREP, 3) tc_prepare_kernel(DeltaBwdParams p) {
         put_pair(Ph, Pl, at<64>(row, col), v[0], v[1]);
       } else {
         put_pair(Ah, Al, at<64>(row, col), v[0], v[1]);
-        A[row][col] = beta[row] * v[0];
-        A[row][col + 1] = beta[row] * v[1];
+        *reinterpret_cast<float2 *>(&A[row][col]) = make_float2(beta[row] * v[0], beta[row] * v[1]);
       }
     }
   __syncthreads();
@@ -114,23 +117,43 @@ __global__ void __launch_bounds__(PREP, 3) tc_prepare_kernel(DeltaBwdParams p) {
     }
   }
   __syncthreads();
-  const int bi = tid / 16, bj = tid % 16;
 #pragma unroll
   for (int d = 1; d < 4; ++d) {
+    if (warp + d < 4) {
+      const int b = 16 * warp, i0 = 16 * (warp + d);
+      // x^T [j][i] = sum_m T_(m, b)^T A_(b+d, m)^T
+      float x[2][4] = {};
 #pragma unroll
-    for (int b = 0; b + d < 4; ++b) {
-      float x = 0.f;
+      for (int m = 0; m < d; ++m) {
+        uint32_t ah[4], al[4], bh[4], bl[4];
+        const int r0 = b + 16 * m;
 #pragma unroll
-      for (int m = 0; m < 16 * d; ++m) x = fmaf(A[16 * (b + d) + bi][16 * b + m], T[16 * b + m][16 * b + bj], x);
-      X[b][bi][bj] = x;
-    }
-    __syncthreads();
+        for (int e = 0; e < 4; ++e) {
+          const int r = r0 + 2 * t + 8 * (e >> 1), j = b + g + 8 * (e & 1);
+          split(T[r][j], T[r + 1][j], ah[e], al[e]);
+          const float2 y = *reinterpret_cast<const float2 *>(&A[i0 + g + 8 * (e >> 1)][r0 + 2 * t + 8 * (e & 1)]);
+          split(y.x, y.y, bh[e], bl[e]);
+        }
+        mma2(x, ah, bh);
+        mma2(x, ah, bl);
+        mma2(x, al, bh);
+      }
+      // T_(b+d, b)^T [j][i] = -x^T T_(b+d, b+d)^T
+      float y[2][4] = {};
+      uint32_t ah[4], al[4], bh[4], bl[4];
 #pragma unroll
-    for (int b = 0; b + d < 4; ++b) {
-      float x = 0.f;
+      for (int e = 0; e < 4; ++e) {
+        split(x[e >> 1][e % 2 * 2], x[e >> 1][e % 2 * 2 + 1], ah[e], al[e]);
+        const float2 z = *reinterpret_cast<const float2 *>(&T[i0 + g + 8 * (e >> 1)][i0 + 2 * t + 8 * (e & 1)]);
+        split(z.x, z.y, bh[e], bl[e]);
+      }
+      mma2(y, ah, bh);
+      mma2(y, ah, bl);
+      mma2(y, al, bh);
 #pragma unroll
-      for (int m = 0; m < 16; ++m) x = fmaf(T[16 * (b + d) + bi][16 * (b + d) + m], X[b][m][bj], x);
-      T[16 * (b + d) + bi][16 * b + bj] = -x;
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) T[i0 + 8 * n + 2 * t + (e & 1)][b + g + 8 * (e >> 1)] = -y[n][e];
     }
     __syncthreads();
   }
