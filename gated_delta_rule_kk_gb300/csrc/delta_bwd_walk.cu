@@ -18,7 +18,8 @@
 //
 // Backward, what q and do add (E = P^T do and U = (scale e^G q)^T do) does not wait for D: a
 // second set of warps forms it beside the ones that carry D.  One more warp loads chunks, two
-// stages deep.  Every wait is bounded.
+// stages deep, and one stores the states: the bulk copies' issue alone took a carrying warp
+// 500 cycles a chunk.  Every wait is bounded.
 #include <algorithm>
 
 #include "delta_bwd_tc.cuh"
@@ -146,7 +147,7 @@ struct Walk {
   using Sh = WalkShared<KP, BACK>;
   static constexpr int HALF = KP / 2, KS = KP / 32;  // a warp's channels; steps of 16 of them
   unsigned char *shared;
-  uint64_t *full, *empty, *handed, *taken;
+  uint64_t *full, *empty, *ready, *stored, *handed, *taken;
   int vt, v0, head, hk, n, count, len, role, vw, sw, lane, g, t;
   int64_t first, token;
   bool ok;
@@ -218,49 +219,64 @@ struct Walk {
       }
   }
 
-  // x (own tokens) = S k^T.  S's pieces go to shared memory, for the other warp and, by bulk
-  // copies, to the workspace's `image` [32][KP].
-  __device__ __forceinline__ void times_keys(float (*x)[4], const float (*s)[4], const bf16 *k,
-                                             unsigned char *image) const {
+  // x (own tokens) = S k^T of the i-th chunk.  S's pieces go to shared memory, for the other
+  // warp and for the storing one.  (All are formed first: the products then follow one another
+  // without waiting for a rounding.)
+  __device__ __forceinline__ void times_keys(float (*x)[4], const float (*s)[4], const bf16 *k, int i) {
     bf16 *S = tiles(Sh::S_AT);
-    if (lane < 4) ptx::bulk_wait_read<0>();  // the chunk's before
-    __syncwarp();
-    uint32_t hi[4], lo[4], b[2][4];
+    uint32_t hi[KS][4], lo[KS][4], b[KS][2][4];
 #pragma unroll
-    for (int i = 0; i < KS; ++i) {
-      const int c = sw * HALF + 16 * i;
+    for (int j = 0; j < KS; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        split(s[2 * i + e / 2][e % 2 * 2], s[2 * i + e / 2][e % 2 * 2 + 1], hi[e], lo[e]);
+        split(s[2 * j + e / 2][e % 2 * 2], s[2 * j + e / 2][e % 2 * 2 + 1], hi[j][e], lo[j][e]);
+    if (i > 0) wait(stored, i - 1);  // the chunk's before has been read
 #pragma unroll
-      for (int u = 0; u < 2; ++u) right<KP>(b[u], k, 16 * group(sw, u), c);
-      put_matrices(S + tile_row<KP>(16 * vw, c), hi);
-      put_matrices(S + KP * VT + tile_row<KP>(16 * vw, c), lo);
-#pragma unroll
-      for (int u = 0; u < 2; ++u) product2(x + 2 * u, hi, b[u]);
-#pragma unroll
-      for (int u = 0; u < 2; ++u) product2(x + 2 * u, lo, b[u]);
+    for (int j = 0; j < KS; ++j) {
+      put_matrices(S + tile_row<KP>(16 * vw, sw * HALF + 16 * j), hi[j]);
+      put_matrices(S + KP * VT + tile_row<KP>(16 * vw, sw * HALF + 16 * j), lo[j]);
     }
     ptx::fence_proxy_async_smem();
-    meet();
-    if (lane < 4) {  // a row of tiles of each piece, this warp's half of it
-      const int place = (lane & 1) * KP * VT + ((2 * vw + (lane >> 1)) * (KP / 8) + sw * (HALF / 8)) * 64;
-      if (ok) ptx::bulk_s2g(image + place * 2, S + place, HALF / 8 * 128);
-      ptx::bulk_commit();
+    arrive(ready);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int c = (half ? sw ^ 1 : sw) * HALF;
+      if (half) {
+        meet();
+#pragma unroll
+        for (int j = 0; j < KS; ++j) {
+          matrices(hi[j], S + tile_row<KP>(16 * vw, c + 16 * j));
+          matrices(lo[j], S + KP * VT + tile_row<KP>(16 * vw, c + 16 * j));
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < KS; ++j)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) right<KP>(b[j][u], k, 16 * group(sw, u), c + 16 * j);
+#pragma unroll
+      for (int j = 0; j < KS; ++j) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) product2(x + 2 * u, hi[j], b[j][u]);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) product2(x + 2 * u, lo[j], b[j][u]);
+      }
     }
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < KS; ++i) {
-      const int c = (sw ^ 1) * HALF + 16 * i;
-      matrices(hi, S + tile_row<KP>(16 * vw, c));
-      matrices(lo, S + KP * VT + tile_row<KP>(16 * vw, c));
-#pragma unroll
-      for (int u = 0; u < 2; ++u) right<KP>(b[u], k, 16 * group(sw, u), c);
-#pragma unroll
-      for (int u = 0; u < 2; ++u) product2(x + 2 * u, hi, b[u]);
-#pragma unroll
-      for (int u = 0; u < 2; ++u) product2(x + 2 * u, lo, b[u]);
+  }
+
+  // The storing warp: a chunk's state as a whole to the workspace.
+  template <typename Image>
+  __device__ __forceinline__ void store(Image image) {
+    for (int i = 0; i < count; ++i) {
+      wait(ready, i);
+      if (lane == 0) {
+        if (ok) ptx::bulk_s2g(image(i), tiles(Sh::S_AT), Block<KP>::STATE);
+        ptx::bulk_commit();
+        ptx::bulk_wait_read<0>();
+        ptx::mbar_arrive(stored);
+      }
+      __syncwarp();
     }
+    if (lane == 0) ptx::bulk_wait<0>();
   }
 
   // Hands on own tokens' left operands by `to` (tiles [32][64]); fetches the other warp's.
@@ -279,25 +295,37 @@ struct Walk {
     }
   }
 
-  // y (own tokens) += x T^T (backward x T), x being warp `s`'s tokens: into the tokens behind
-  // (before) them, as T's upper triangle is zero.
-  __device__ __forceinline__ void times_T(float (*y)[4], const uint32_t (*hi)[4],
-                                          const uint32_t (*lo)[4], const bf16 *T, int s) const {
+  // What y (own tokens) += x T^T (backward x T) takes of T, x being warp `s`'s tokens, into the
+  // tokens behind (before) them, as T's upper triangle is zero; and the products.
+  struct Triangle {
+    uint32_t b[2][2][2][4];  // [from][to][piece]
+  };
+  __device__ __forceinline__ bool within(int from, int to) const { return BACK ? from >= to : from <= to; }
+  __device__ __forceinline__ void take_T(Triangle &T, const bf16 *at_, int s) const {
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int piece = 0; piece < 2; ++piece)
+      for (int o = 0; o < 2; ++o)
+#pragma unroll
+        for (int piece = 0; piece < 2; ++piece) {
+          const int from = group(s, u), to = group(sw, o);
+          if (!within(from, to)) continue;
+          if (BACK)
+            right_t<64>(T.b[u][o][piece], at_ + piece * Q * Q, 16 * to, 16 * from);
+          else
+            right<64>(T.b[u][o][piece], at_ + piece * Q * Q, 16 * to, 16 * from);
+        }
+  }
+  __device__ __forceinline__ void times_T(float (*y)[4], const uint32_t (*hi)[4],
+                                          const uint32_t (*lo)[4], const Triangle &T, int s) const {
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int piece = 0; piece < 3; ++piece)
 #pragma unroll
         for (int o = 0; o < 2; ++o) {
-          const int from = group(s, u), to = group(sw, o);
-          if (BACK ? from < to : from > to) continue;
-          uint32_t b[4];
-          if (BACK)
-            right_t<64>(b, T + piece * Q * Q, 16 * to, 16 * from);
-          else
-            right<64>(b, T + piece * Q * Q, 16 * to, 16 * from);
-          product2(y + 2 * o, hi[u], b);
-          if (piece == 0) product2(y + 2 * o, lo[u], b);
+          if (!within(group(s, u), group(sw, o))) continue;
+          product2(y + 2 * o, piece == 1 ? lo[u] : hi[u], T.b[u][o][piece == 2]);
         }
   }
 
@@ -351,8 +379,8 @@ __device__ __forceinline__ void to_operand(const float (*y)[4], uint32_t (*hi)[4
   }
 }
 
-// The roles: warps 0 .. CARRY - 1 carry states; backward CARRY more hand them E and U; the
-// last one loads.  Returns false where there is nothing to do.
+// The roles: warps 0 .. CARRY - 1 carry states; backward CARRY more hand them E and U; the last
+// two load and store.  Returns false where there is nothing to do.
 template <int KP, bool BACK>
 __device__ __forceinline__ bool begin_walk(const DeltaBwdParams &p, Walk<KP, BACK> &w,
                                            unsigned char *shared, uint64_t *bars) {
@@ -360,8 +388,10 @@ __device__ __forceinline__ bool begin_walk(const DeltaBwdParams &p, Walk<KP, BAC
   w.shared = shared;
   w.full = bars;
   w.empty = bars + 2;
-  w.handed = bars + 4;
-  w.taken = bars + 4 + 2 * CARRY;
+  w.ready = bars + 4;
+  w.stored = bars + 5;
+  w.handed = bars + 6;
+  w.taken = bars + 6 + 2 * CARRY;
   w.vt = blockIdx.x;
   w.v0 = w.vt * VT;
   w.head = blockIdx.y;
@@ -384,6 +414,8 @@ __device__ __forceinline__ bool begin_walk(const DeltaBwdParams &p, Walk<KP, BAC
       ptx::mbar_init(&w.full[s], 33);
       ptx::mbar_init(&w.empty[s], BACK ? 2 * CARRY : CARRY);
     }
+    ptx::mbar_init(w.ready, CARRY);
+    ptx::mbar_init(w.stored, 1);
     if (BACK)
       for (int s = 0; s < 2 * CARRY; ++s) {
         ptx::mbar_init(&w.handed[s], 1);
@@ -397,15 +429,18 @@ __device__ __forceinline__ bool begin_walk(const DeltaBwdParams &p, Walk<KP, BAC
 
 // grid: value tiles, heads, sequences.  The states, forward.
 template <int KP>
-__global__ void __launch_bounds__(32 * (CARRY + 1), 2) tc_states_kernel(DeltaBwdParams p) {
+__global__ void __launch_bounds__(32 * (CARRY + 2), 2) tc_states_kernel(DeltaBwdParams p) {
   using W = Walk<KP, false>;
   using St = WalkStage<KP, false>;
   extern __shared__ __align__(128) unsigned char shared[];
-  __shared__ uint64_t bars[4];
+  __shared__ uint64_t bars[6];
   W w;
   if (!begin_walk(p, w, shared, bars)) return;
-  if (w.role == 1) {
-    w.load(p);
+  if (w.role == 1 && w.vw == 0) {
+    if (w.sw == 0)
+      w.load(p);
+    else
+      w.store([&](int i) { return Block<KP>(p, w.first + i, w.head).h(w.vt); });
   } else {
     bf16 *R = w.tiles(W::Sh::R_AT), *N = w.tiles(W::Sh::N_AT);
     float s[W::HALF / 8][4];
@@ -419,7 +454,10 @@ __global__ void __launch_bounds__(32 * (CARRY + 1), 2) tc_states_kernel(DeltaBwd
       const float *beta = sc + Q, *eG = sc + 2 * Q, *eR = sc + 3 * Q;
       float x[4][4] = {}, y[4][4] = {};
       uint32_t hi[2][4], lo[2][4], b[4];
-      w.times_keys(x, s, k, block.h(w.vt));
+      typename W::Triangle own, other;
+      w.times_keys(x, s, k, c);
+      w.take_T(own, T, w.sw);
+      w.take_T(other, T, w.sw ^ 1);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {  // the values as the accumulators have them
         left_t<32>(b, v, 16 * w.vw, 16 * w.group(w.sw, u));
@@ -436,10 +474,10 @@ __global__ void __launch_bounds__(32 * (CARRY + 1), 2) tc_states_kernel(DeltaBwd
         }
       }
       w.give(R, hi, lo);
-      w.times_T(y, hi, lo, T, w.sw);
+      w.times_T(y, hi, lo, own, w.sw);
       w.meet();
       w.take(R, hi, lo);
-      w.times_T(y, hi, lo, T, w.sw ^ 1);
+      w.times_T(y, hi, lo, other, w.sw ^ 1);
       if (c + 1 < w.count) {
         to_operand(y, hi, lo, [&](int j) { return w.pair(eR, j); });
         w.give(N, hi, lo);
@@ -458,7 +496,6 @@ __global__ void __launch_bounds__(32 * (CARRY + 1), 2) tc_states_kernel(DeltaBwd
       }
       w.arrive(&w.empty[c & 1]);
     }
-    if (w.lane < 4) ptx::bulk_wait<0>();
   }
   if (!w.ok && w.lane == 0) record_error(p.err, GDN_ERR_TIMEOUT);
 }
@@ -467,15 +504,18 @@ __global__ void __launch_bounds__(32 * (CARRY + 1), 2) tc_states_kernel(DeltaBwd
 //   x = D k^T,  dn = E + e^(G_L - G) x,  dr = dn T,  D <- e^(G_L) D + U - (beta e^G dr) k.
 // dv = beta dr leaves from here too.
 template <int KP>
-__global__ void __launch_bounds__(32 * (2 * CARRY + 1), 1) tc_grads_kernel(DeltaBwdParams p) {
+__global__ void __launch_bounds__(32 * (2 * CARRY + 2), 1) tc_grads_kernel(DeltaBwdParams p) {
   using W = Walk<KP, true>;
   using St = WalkStage<KP, true>;
   extern __shared__ __align__(128) unsigned char shared[];
-  __shared__ uint64_t bars[4 + 4 * CARRY];
+  __shared__ uint64_t bars[6 + 4 * CARRY];
   W w;
   if (!begin_walk(p, w, shared, bars)) return;
   if (w.role == 2) {
-    w.load(p);
+    if (w.sw == 0)
+      w.load(p);
+    else
+      w.store([&](int i) { return Block<KP>(p, w.first + w.chunk(i), w.head).D(w.vt); });
   } else if (w.role == 1) {  // E of own tokens and U of own channels
     for (int i = 0; i < w.count; ++i) {
       w.wait(&w.full[i & 1], i / 2);
@@ -532,7 +572,10 @@ __global__ void __launch_bounds__(32 * (2 * CARRY + 1), 1) tc_grads_kernel(Delta
       const float *beta = sc + Q, *eG = sc + 2 * Q, *eR = sc + 3 * Q;
       float x[4][4] = {}, y[4][4] = {};
       uint32_t hi[2][4], lo[2][4];
-      w.times_keys(x, s, k, block.D(w.vt));
+      typename W::Triangle own, other;
+      w.times_keys(x, s, k, i);
+      w.take_T(own, T, w.sw);
+      w.take_T(other, T, w.sw ^ 1);
       w.wait(&w.handed[w.hand_bar(i)], i / 2);
       const float4 *from = w.hand(i);
 #pragma unroll
@@ -546,7 +589,7 @@ __global__ void __launch_bounds__(32 * (2 * CARRY + 1), 1) tc_grads_kernel(Delta
       }
       to_operand(x, hi, lo, [](int) { return make_float2(1.f, 1.f); });
       w.give(R, hi, lo);
-      w.times_T(y, hi, lo, T, w.sw);
+      w.times_T(y, hi, lo, own, w.sw);
       const float eL = eG[Q - 1];
 #pragma unroll
       for (int j = 0; j < W::HALF / 8; ++j) {
@@ -559,7 +602,7 @@ __global__ void __launch_bounds__(32 * (2 * CARRY + 1), 1) tc_grads_kernel(Delta
       w.arrive(&w.taken[w.hand_bar(i)]);
       w.meet();
       w.take(R, hi, lo);
-      w.times_T(y, hi, lo, T, w.sw ^ 1);
+      w.times_T(y, hi, lo, other, w.sw ^ 1);
       to_operand(y, hi, lo, [&](int j) {
         const float2 f = w.pair(beta, j), e = w.pair(eG, j);
         return make_float2(-f.x * e.x, -f.y * e.y);
@@ -588,7 +631,6 @@ __global__ void __launch_bounds__(32 * (2 * CARRY + 1), 1) tc_grads_kernel(Delta
       }
       w.arrive(&w.empty[i & 1]);
     }
-    if (w.lane < 4) ptx::bulk_wait<0>();
     if (p.dh0 != nullptr)
 #pragma unroll
       for (int j = 0; j < W::HALF / 8; ++j)
@@ -611,8 +653,8 @@ cudaError_t launch(const DeltaBwdParams &p, cudaStream_t stream) {
     e = cudaFuncSetAttribute(tc_grads_kernel<KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, GRADS);
   if (e != cudaSuccess) return e;
   const dim3 grid((p.V + VT - 1) / VT, p.H, p.N);
-  tc_states_kernel<KP><<<grid, 32 * (CARRY + 1), STATES, stream>>>(p);
-  tc_grads_kernel<KP><<<grid, 32 * (2 * CARRY + 1), GRADS, stream>>>(p);
+  tc_states_kernel<KP><<<grid, 32 * (CARRY + 2), STATES, stream>>>(p);
+  tc_grads_kernel<KP><<<grid, 32 * (2 * CARRY + 2), GRADS, stream>>>(p);
   return cudaGetLastError();
 }
 
