@@ -42,9 +42,9 @@ struct KdParams {
 constexpr int KD_WARPS = 8, KD_ROWS = 4;
 // The ring: two blocks an SM (three would leave a thread 48 registers, and its rows would
 // spill), each with as many stages as its half of the shared memory holds, up to KD_STAGES.
-// (A preparing warp skips KD_PREP - 1 items; it may not skip a use of a barrier, so there
-// are at least KD_PREP stages: 256 channels and four tokens have three.)
-constexpr int KD_STAGES = 6, KD_PREP = 3, KD_PER_SM = 2;
+// (A preparing warp skips the others' items; it may not skip a use of a barrier, so no more
+// of them work than there are stages: 256 channels and four tokens have three.)
+constexpr int KD_STAGES = 6, KD_PREP = 4, KD_PER_SM = 2;
 constexpr uint32_t KD_TILE = 16384;
 constexpr int KD_THREADS = 32 * (KD_WARPS + KD_PREP + 2);
 
@@ -53,7 +53,8 @@ struct KdItem {
   int b, h, v, end, slot;
 };
 
-// An item's coefficients (floats): decay, k and q [T][K], v [T][rows], beta and k . q [T].
+// An item's coefficients (floats): decay, k and q [T][K], v [T][rows], beta and k . q [T], and
+// whether its slot is good (so that the warps that take a tile need not look it up).
 struct KdCoef {
   int K, R, T;
   __host__ __device__ KdCoef(int k, int r, int t) : K(k), R((r + 3) / 4 * 4), T(t) {}
@@ -63,65 +64,103 @@ struct KdCoef {
   __host__ __device__ int v(int t) const { return 3 * T * K + t * R; }
   __host__ __device__ int beta(int t) const { return 3 * T * K + T * R + t; }
   __host__ __device__ int kq(int t) const { return 3 * T * K + T * R + T + t; }
-  __host__ __device__ int bytes() const { return ((kq(T) + 1) * 4 + 127) / 128 * 128; }
+  __host__ __device__ int good() const { return kq(T); }
+  __host__ __device__ int bytes() const { return ((good() + 1) * 4 + 127) / 128 * 128; }
 };
 
-__device__ __forceinline__ float kd_token(const KdParams &p, const void *base, int64_t at) {
-  return p.tok_f32 ? static_cast<const float *>(base)[at]
-                   : to_f32(static_cast<const __nv_bfloat16 *>(base)[at]);
-}
+// One warp forms a token's coefficients: what it reads, and what it makes of it.  Lane l takes
+// channels and rows l, l + 32, .., as many as the rows of LPR lanes and PP pieces can have.
+template <typename S, int LPR, int PP>
+struct KdToken {
+  static constexpr int MOST = LPR * PP * 16 / (int)sizeof(S) / 32, ROWS = KD_WARPS * KD_ROWS / LPR;
+  static_assert(MOST >= 1 && ROWS >= 1, "");
+  float q[MOST], k[MOST], a[MOST], bias[MOST], v[ROWS], b, A_log;
 
-// One warp forms token t's coefficients.  Up to 256 channels: lane l takes l, l + 32, ..
-__device__ __forceinline__ void kd_prepare(const KdParams &p, const KdItem &it, int t, float *f) {
-  constexpr int MOST = 8;
-  const int lane = threadIdx.x & 31, hk = it.h / (p.HV / p.H);
-  const KdCoef c(p.K, p.rows, p.T);
-  const int64_t qat = it.b * p.qb + t * p.qs + (int64_t)hk * p.K;
-  const int64_t kat = it.b * p.kb + t * p.ks + (int64_t)hk * p.K;
-  const int64_t aat = it.b * p.ab + t * p.as + (int64_t)it.h * p.K;
-  const int64_t vat = it.b * p.vb + t * p.vs + (int64_t)it.h * p.V + it.v;
-  float q[MOST], k[MOST], a[MOST], bias[MOST];
+  __device__ __forceinline__ void load(const KdParams &p, const KdItem &it, int t) {
+    if (p.tok_f32)
+      load_as<float>(p, it, t);
+    else
+      load_as<__nv_bfloat16>(p, it, t);
+  }
+  // Everything is asked for before anything is used: while states stream, a load takes some
+  // microseconds.  (With the type looked at element by element they followed one another:
+  // 120 us for 256 requests.)
+  template <typename E>
+  __device__ __forceinline__ void load_as(const KdParams &p, const KdItem &it, int t) {
+    const int lane = threadIdx.x & 31, hk = it.h / (p.HV / p.H);
+    const E *qat = static_cast<const E *>(p.q) + it.b * p.qb + t * p.qs + (int64_t)hk * p.K;
+    const E *kat = static_cast<const E *>(p.k) + it.b * p.kb + t * p.ks + (int64_t)hk * p.K;
+    const E *aat = static_cast<const E *>(p.a) + it.b * p.ab + t * p.as + (int64_t)it.h * p.K;
+    const E *vat = static_cast<const E *>(p.v) + it.b * p.vb + t * p.vs + (int64_t)it.h * p.V + it.v;
+    const float *bat = p.dt_bias ? p.dt_bias + (int64_t)it.h * p.K : nullptr;
+    E rq[MOST], rk[MOST], ra[MOST], rv[ROWS];
 #pragma unroll
-  for (int i = 0; i < MOST; ++i) {
-    const int ch = lane + 32 * i;
-    q[i] = k[i] = a[i] = bias[i] = 0.f;
-    if (ch >= p.K) continue;
-    q[i] = kd_token(p, p.q, qat + ch);
-    k[i] = kd_token(p, p.k, kat + ch);
-    a[i] = kd_token(p, p.a, aat + ch);
-    if (p.dt_bias) bias[i] = p.dt_bias[(int64_t)it.h * p.K + ch];
-  }
-  const float b = kd_token(p, p.b, it.b * p.bb + t * p.bs + it.h);
-  const float rate = -expf(p.A_log[it.h]);
-  for (int r = lane; r < it.end - it.v; r += 32) f[c.v(t) + r] = kd_token(p, p.v, vat + r);
-  float qq = 0.f, kk = 0.f, qk = 0.f;
+    for (int i = 0; i < MOST; ++i) {
+      const int ch = lane + 32 * i;
+      const bool in = ch < p.K;  // (q and k of channels past K count in sums; the rest is not used)
+      rq[i] = in ? qat[ch] : E(0.f);
+      rk[i] = in ? kat[ch] : E(0.f);
+      ra[i] = in ? aat[ch] : E(0.f);
+      bias[i] = in && bat ? bat[ch] : 0.f;
+    }
 #pragma unroll
-  for (int i = 0; i < MOST; ++i) {
-    qq = fmaf(q[i], q[i], qq);
-    kk = fmaf(k[i], k[i], kk);
-    qk = fmaf(q[i], k[i], qk);
-  }
+    for (int i = 0; i < ROWS; ++i)
+      rv[i] = it.v + lane + 32 * i < it.end ? vat[lane + 32 * i] : E(0.f);
+    const E rb = static_cast<const E *>(p.b)[it.b * p.bb + t * p.bs + it.h];
+    A_log = p.A_log[it.h];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    qq += __shfl_xor_sync(~0u, qq, o);
-    kk += __shfl_xor_sync(~0u, kk, o);
-    qk += __shfl_xor_sync(~0u, qk, o);
-  }
-  const float qn = p.l2norm ? p.scale / sqrtf(qq + p.eps) : p.scale;
-  const float kn = p.l2norm ? 1.f / sqrtf(kk + p.eps) : 1.f;
+    for (int i = 0; i < MOST; ++i) {
+      q[i] = to_f32(rq[i]);
+      k[i] = to_f32(rk[i]);
+      a[i] = to_f32(ra[i]);
+    }
 #pragma unroll
-  for (int i = 0; i < MOST; ++i) {
-    const int ch = lane + 32 * i;
-    if (ch >= p.K) continue;
-    f[c.decay(t) + ch] = expf(rate * softplus(a[i] + bias[i]));
-    f[c.k(t) + ch] = k[i] * kn;
-    f[c.q(t) + ch] = q[i] * qn;
+    for (int i = 0; i < ROWS; ++i) v[i] = to_f32(rv[i]);
+    b = to_f32(rb);
   }
-  if (lane == 0) {
-    f[c.beta(t)] = 1.f / (1.f + expf(-b));
-    f[c.kq(t)] = qk * qn * kn;
+
+  __device__ __forceinline__ void put(const KdParams &p, const KdItem &it, int t, float *f) const {
+    const int lane = threadIdx.x & 31;
+    const KdCoef c(p.K, p.rows, p.T);
+    float qq = 0.f, kk = 0.f, qk = 0.f;
+#pragma unroll
+    for (int i = 0; i < MOST; ++i) {
+      qq = fmaf(q[i], q[i], qq);
+      kk = fmaf(k[i], k[i], kk);
+      qk = fmaf(q[i], k[i], qk);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      qq += __shfl_xor_sync(~0u, qq, o);
+      kk += __shfl_xor_sync(~0u, kk, o);
+      qk += __shfl_xor_sync(~0u, qk, o);
+    }
+    const float qn = p.l2norm ? p.scale / sqrtf(qq + p.eps) : p.scale;
+    const float kn = p.l2norm ? 1.f / sqrtf(kk + p.eps) : 1.f;
+    const float rate = -expf(A_log);
+    float decay[MOST];  // side by side: each is a long chain
+#pragma unroll
+    for (int i = 0; i < MOST; ++i) {
+      const float x = a[i] + bias[i], y = log1pf(expf(fminf(x, 20.f)));
+      decay[i] = expf(rate * (x > 20.f ? x : y));
+    }
+#pragma unroll
+    for (int i = 0; i < MOST; ++i) {
+      const int ch = lane + 32 * i;
+      if (ch >= p.K) continue;
+      f[c.decay(t) + ch] = decay[i];
+      f[c.k(t) + ch] = k[i] * kn;
+      f[c.q(t) + ch] = q[i] * qn;
+    }
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i)
+      if (it.v + lane + 32 * i < it.end) f[c.v(t) + lane + 32 * i] = v[i];
+    if (lane == 0) {
+      f[c.beta(t)] = 1.f / (1.f + expf(-b));
+      f[c.kq(t)] = qk * qn * kn;
+    }
   }
-}
+};
 
 __device__ __forceinline__ void kd_put(const KdParams &p, const KdItem &it, int t, int r, float o) {
   const int64_t at = it.b * p.ob + t * p.os + (int64_t)it.h * p.V + r;
@@ -253,16 +292,47 @@ __device__ __forceinline__ S *kd_tile_at(const KdParams &p, const KdItem &it) {
   return static_cast<S *>(p.state) + (((int64_t)it.slot * p.HV + it.h) * p.V + it.v) * p.K;
 }
 
-__device__ __forceinline__ KdItem kd_item(const KdParams &p, int64_t i) {
-  KdItem it;
-  it.v = (int)(i % p.vblocks) * p.rows;
-  it.end = min(it.v + p.rows, p.V);
-  const int64_t bh = i / p.vblocks;
-  it.b = (int)(bh / p.HV);
-  it.h = (int)(bh % p.HV);
-  it.slot = p.slots ? p.slots[it.b] : it.b;
-  return it;
-}
+// Items in turn, i, i + step, ..: the divisions are done once (each of an item's warps doing
+// them anew took most of the ring's instructions).
+struct KdWalk {
+  int b, h, v, db, dh, dv;  // request, head, tile; and the step's
+  __device__ __forceinline__ KdWalk(const KdParams &p, unsigned i, unsigned step) {
+    const unsigned heads = p.HV, tiles = p.vblocks;
+    v = i % tiles;
+    h = i / tiles % heads;
+    b = i / tiles / heads;
+    dv = step % tiles;
+    dh = step / tiles % heads;
+    db = step / tiles / heads;
+  }
+  __device__ __forceinline__ void next(const KdParams &p) {
+    v += dv;
+    h += dh;
+    b += db;
+    if (v >= p.vblocks) {
+      v -= p.vblocks;
+      ++h;
+    }
+    if (h >= p.HV) {
+      h -= p.HV;
+      ++b;
+    }
+  }
+  __device__ __forceinline__ KdItem place(const KdParams &p) const {  // all but its slot
+    KdItem it;
+    it.v = v * p.rows;
+    it.end = min(it.v + p.rows, p.V);
+    it.b = b;
+    it.h = h;
+    it.slot = 0;
+    return it;
+  }
+  __device__ __forceinline__ KdItem item(const KdParams &p) const {
+    KdItem it = place(p);
+    it.slot = p.slots ? p.slots[b] : b;
+    return it;
+  }
+};
 
 __device__ __forceinline__ bool kd_good(const KdParams &p, const KdItem &it) {
   return it.slot >= 0 && it.slot < p.pool;
@@ -281,14 +351,18 @@ __global__ void __launch_bounds__(32 * KD_WARPS) kda_decode_kernel(KdParams p) {
   extern __shared__ __align__(128) float coef[];
   constexpr int WARP_ROWS = KD_ROWS * 32 / LPR;
   const int warp = threadIdx.x >> 5;
-  const KdItem it = kd_item(p, blockIdx.x);
+  const KdItem it = KdWalk(p, blockIdx.x, 1).item(p);
   if (!bounds_ok(it.b < p.B && it.h < p.HV && it.v < p.V && p.rows <= KD_WARPS * WARP_ROWS, p.err))
     return;
   if (!kd_good(p, it)) return kd_refuse(p, it, threadIdx.x, blockDim.x);
   S *tile = kd_tile_at<S>(p, it);
   KdTile<S, LPR, PP> rows;
   rows.load(tile, warp * WARP_ROWS, it.end - it.v, p.K);
-  if (warp < p.T) kd_prepare(p, it, warp, coef);
+  if (warp < p.T) {
+    KdToken<S, LPR, PP> token;
+    token.load(p, it, warp);
+    token.put(p, it, warp, coef);
+  }
   __syncthreads();
   rows.template take<TM>(p, it, tile, warp * WARP_ROWS, coef);
 }
@@ -315,7 +389,7 @@ kda_decode_ring_kernel(KdParams p, int items) {
     ptx::fence_mbar_init();
   }
   __syncthreads();
-  if (!bounds_ok(stages >= KD_PREP && stages <= KD_STAGES && p.rows > 0 &&
+  if (!bounds_ok(stages >= 1 && stages <= KD_STAGES && p.rows > 0 &&
                      p.rows <= KD_WARPS * WARP_ROWS &&
                      p.rows * p.K * (int)sizeof(S) <= (int)KD_TILE,
                  p.err))
@@ -331,13 +405,14 @@ kda_decode_ring_kernel(KdParams p, int items) {
     return reinterpret_cast<float *>(ring + stages * KD_TILE + s * coef_bytes);
   };
   int n = 0;  // items of this block so far
+  KdWalk walk(p, blockIdx.x, gridDim.x);
   if (warp < KD_WARPS) {
-    for (int i = blockIdx.x; i < items; i += gridDim.x, ++n) {
+    for (int i = blockIdx.x; i < items; i += gridDim.x, ++n, walk.next(p)) {
       const int s = n % stages;
-      const KdItem it = kd_item(p, i);
+      const KdItem it = walk.place(p);
       wait(&ready[s], n / stages);
       wait(&full[s], n / stages);
-      if (kd_good(p, it)) {
+      if (coef(s)[KdCoef(p.K, p.rows, p.T).good()] != 0.f) {
         if (warp * WARP_ROWS < it.end - it.v) {
           S *tile = reinterpret_cast<S *>(ring + s * KD_TILE);
           KdTile<S, LPR, PP> rows;
@@ -352,19 +427,27 @@ kda_decode_ring_kernel(KdParams p, int items) {
       if (lane == 0) ptx::mbar_arrive(&done[s]);
     }
   } else if (warp < KD_WARPS + KD_PREP) {
-    for (int i = blockIdx.x; i < items; i += gridDim.x, ++n) {
-      if (n % KD_PREP != warp - KD_WARPS) continue;
+    const int preps = min(KD_PREP, stages);
+    for (int i = blockIdx.x; i < items; i += gridDim.x, ++n, walk.next(p)) {
+      if (n % preps != warp - KD_WARPS) continue;
       const int s = n % stages;
-      const KdItem it = kd_item(p, i);
+      const KdItem it = walk.item(p);
+      KdToken<S, LPR, PP> token;
+      token.load(p, it, 0);
       if (n >= stages) wait(&done[s], n / stages - 1);
-      for (int t = 0; t < p.T; ++t) kd_prepare(p, it, t, coef(s));
+      token.put(p, it, 0, coef(s));
+      for (int t = 1; t < p.T; ++t) {
+        token.load(p, it, t);
+        token.put(p, it, t, coef(s));
+      }
+      if (lane == 0) coef(s)[KdCoef(p.K, p.rows, p.T).good()] = kd_good(p, it) ? 1.f : 0.f;
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&ready[s]);
     }
   } else if (warp == KD_WARPS + KD_PREP) {
-    for (int i = blockIdx.x; i < items; i += gridDim.x, ++n) {
+    for (int i = blockIdx.x; i < items; i += gridDim.x, ++n, walk.next(p)) {
       const int s = n % stages;
-      const KdItem it = kd_item(p, i);
+      const KdItem it = walk.item(p);
       if (n >= stages) wait(&empty[s], n / stages - 1);
       if (!__all_sync(~0u, ok)) break;
       if (lane == 0) {
@@ -381,9 +464,9 @@ kda_decode_ring_kernel(KdParams p, int items) {
     for (int k = max(0, n - stages); k < n; ++k)
       ok = ptx::mbar_wait_bounded(&full[k % stages], (uint32_t)(k / stages & 1), 1u << 22) && ok;
   } else {
-    for (int i = blockIdx.x; i < items; i += gridDim.x, ++n) {
+    for (int i = blockIdx.x; i < items; i += gridDim.x, ++n, walk.next(p)) {
       const int s = n % stages;
-      const KdItem it = kd_item(p, i);
+      const KdItem it = walk.item(p);
       wait(&done[s], n / stages);
       if (lane == 0) {
         if (kd_good(p, it) && ok) ptx::bulk_s2g(kd_tile_at<S>(p, it), ring + s * KD_TILE, bytes_of(it));
