@@ -13,57 +13,70 @@
 namespace gdn {
 namespace {
 
-template <typename T, int VEC, int PP, bool Z>
-__global__ void __launch_bounds__(norm_threads(PP * VEC)) norm_fwd_kernel(NormParams p) {
+template <typename T, int VEC, int PP, bool Z, bool WIDE>
+__global__ void __launch_bounds__(
+    norm_block(PP * VEC, WIDE),
+    WIDE ? 1 : norm_fwd_per_sm(PP * VEC, norm_words(sizeof(T), VEC, PP), Z))
+norm_fwd_kernel(NormParams p) {
+  constexpr int AHEAD = WIDE ? 1 : norm_fwd_ahead(norm_words(sizeof(T), VEC, PP), Z);
   __shared__ float buf[2][NORM_WARPS][2];
   const NormTeam m(p);
   if (!bounds_ok(p.team * p.rows * p.span <= (int)blockDim.x, p.err)) return;
   int turn = 0;
-  float w[PP][VEC], b[PP][VEC];
-  NormRow<T, VEC, PP> x, z;
-  x.zero();
-  z.zero();
-  x.load(p, m, p.x, p.xs, p.xb, m.t);
-  if (Z) z.load(p, m, p.z, p.zs, p.zb, m.t);
-  norm_weights<T>(p, m, p.weight, 1.f, w);
-  norm_weights<T>(p, m, p.bias, 0.f, b);
+  NormCursor<T> xc(p, m, p.x, p.xs, p.xb, VEC), zc(p, m, p.z, p.zs, p.zb, VEC);
+  NormCursor<T> yc(p, m, p.y, p.ys, p.yb, VEC);
+  NormRow<T, VEC, PP> x[AHEAD], z[Z ? AHEAD : 1];
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) {
+    x[i].zero();
+    x[i].load(p, m, xc, m.t + i * p.step);
+    if constexpr (Z) {
+      z[i].zero();
+      z[i].load(p, m, zc, m.t + i * p.step);
+    }
+  }
   // every team of a block takes as many turns: the sums are the block's
   const int first = blockIdx.x / p.blocks_per_row * p.rows;
-  for (int t0 = first, t = m.t; t0 < p.tokens; t0 += p.step, t += p.step) {
-    float u[PP][VEC], gate[Z ? PP : 1][VEC];
+  for (int t0 = first, t = m.t; t0 < p.tokens;) {
 #pragma unroll
-    for (int j = 0; j < PP; ++j) {
-      x.r[j].widen(u[j]);
-      if constexpr (Z) {
-        float v[VEC];
-        z.r[j].widen(v);
-        norm_act<VEC>(p.act, v, gate[j], nullptr);
-        if (p.gate_first)
+    for (int i = 0; i < AHEAD; ++i, t0 += p.step, t += p.step) {
+      if (t0 >= p.tokens) break;
+      float u[PP][VEC], gate[Z ? PP : 1][VEC];
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) u[j][e] *= gate[j][e];
+      for (int j = 0; j < PP; ++j) {
+        x[i].r[j].widen(u[j]);
+        if constexpr (Z) {
+          z[i].r[j].widen(gate[j]);
+          norm_act<VEC, false>(p.act, gate[j], gate[j], nullptr);
+          if (p.gate_first) vmul<VEC>(u[j], u[j], gate[j]);
+        }
       }
-    }
-    x.load(p, m, p.x, p.xs, p.xb, t + p.step);
-    if (Z) z.load(p, m, p.z, p.zs, p.zb, t + p.step);
-    normalise<VEC, PP>(p, m, u, buf, turn);
-    NormRow<T, VEC, PP> y;
+      x[i].load(p, m, xc, t + AHEAD * p.step);
+      if constexpr (Z) z[i].load(p, m, zc, t + AHEAD * p.step);
+      const float r = norm_root<VEC, PP>(p, m, u, buf, turn);
+      NormRow<T, VEC, PP> y;
 #pragma unroll
-    for (int j = 0; j < PP; ++j) {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) u[j][e] = fmaf(u[j][e], w[j][e], b[j][e]);
-      if constexpr (Z) {
-        if (!p.gate_first)
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) u[j][e] *= gate[j][e];
-      } else {
-        float v[VEC];
-        norm_act<VEC>(p.act, u[j], v, nullptr);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) u[j][e] = v[e];
+      for (int j = 0; j < PP; ++j) {
+        vmul<VEC>(u[j], u[j], r);
+        if (p.weight != nullptr) {
+          float w[VEC];
+          norm_weights<T, VEC>(p, m, p.weight, j, w);
+          vmul<VEC>(u[j], u[j], w);
+        }
+        if (p.bias != nullptr) {
+          float b[VEC];
+          norm_weights<T, VEC>(p, m, p.bias, j, b);
+          vadd<VEC>(u[j], u[j], b);
+        }
+        if constexpr (Z) {
+          if (!p.gate_first) vmul<VEC>(u[j], u[j], gate[j]);
+        } else {
+          norm_act<VEC, false>(p.act, u[j], u[j], nullptr);
+        }
+        y.r[j].round(u[j]);
       }
-      y.r[j].round(u[j]);
+      y.store(p, m, yc, t);
     }
-    y.store(p, m, p.y, p.ys, p.yb, t);
   }
 }
 
@@ -74,18 +87,19 @@ struct NormPlan {
   int vec, pieces, threads, blocks;
 };
 
-// `t + step` passes the last token by at most a step, and has to stay within 31 bits.
+// `t` passes the last token by a few steps of less than 2^18, and has to stay within 31 bits.
 constexpr int64_t NORM_MAX_TOKENS = MAX_TOKENS - (1 << 20);
 
-NormPlan norm_plan(NormParams &p, int vec, bool bwd) {
+NormPlan norm_plan(NormParams &p, bool bf16, int vec, bool bwd) {
   const int all = p.W / vec, most = norm_pieces(vec);
   // as few pieces a thread as keep a group within a warp, where that can be
   int n = 1;
   while (n < most && (all + n - 1) / n > 32) n += n < 4 ? n : 2;
   p.team = 1;
   while (p.team * n < all) p.team *= 2;
-  NormPlan plan{vec, n, std::max(bwd ? NORM_BWD_THREADS : NORM_FWD_THREADS, p.team), 0};
-  const int per_sm = bwd ? norm_bwd_per_sm(vec * n) : norm_fwd_per_sm(vec * n);
+  NormPlan plan{vec, n, std::max(NORM_THREADS, p.team), 0};
+  const int per_sm = bwd ? norm_bwd_per_sm(vec * n)
+                         : norm_fwd_per_sm(vec * n, norm_words(bf16 ? 2 : 4, vec, n), p.z != nullptr);
   const int teams = plan.threads / p.team;
   p.span = std::min(teams, p.G);
   p.blocks_per_row = (p.G + p.span - 1) / p.span;
@@ -105,6 +119,8 @@ int norm_vec(const NormParams &p, bool bf16, std::initializer_list<const void *>
   const int elt = bf16 ? 2 : 4;
   for (int vec = 16 / elt; vec > 1; vec = bf16 && vec == 8 ? 2 : 1) {
     bool ok = p.W % vec == 0;
+    for (const void *w : {p.weight, p.bias})  // a piece of them, in loads of 16 bytes at most
+      ok = ok && aligned_to(w, std::min(vec * (p.w_f32 ? 4 : elt), 16));
     for (const void *t : tensors) ok = ok && aligned_to(t, vec * elt);
     for (int64_t s : strides) ok = ok && s % vec == 0;
     if (ok) return vec;
@@ -155,9 +171,13 @@ NormParams norm_params(const Args &a) {
   p.tokens = a.B * a.T; p.T = a.T;
   p.G = a.groups; p.W = a.D / a.groups; p.D = a.D;
   p.shared = a.shared_weight; p.w_f32 = a.weight_dtype == GDN_F32;
+  p.flat = a.B == 1;
   p.center = a.center; p.gate_first = a.gate_first; p.act = a.activation; p.eps = a.eps;
   return p;
 }
+
+// Whether a tensor's batch rows follow one another.
+bool evenly(const NormParams &p, int64_t stride, int64_t batch) { return batch == p.T * stride; }
 
 gdn_status_t check_bwd(const group_norm_bwd_args &a) {
   gdn_status_t st = check_norm(a);
@@ -185,9 +205,12 @@ NormPlan bwd_plan(const group_norm_bwd_args &a, NormParams &p) {
   p.gs = tokens ? a.dy_stride : a.D; p.gb = many ? a.dy_batch_stride : 0;
   p.ys = tokens ? a.dx_stride : a.D; p.yb = many ? a.dx_batch_stride : 0;
   p.ds = tokens && a.z ? a.dz_stride : a.D; p.db = many && a.z ? a.dz_batch_stride : 0;
+  const bool z = p.z != nullptr;
+  p.flat = p.flat || (evenly(p, p.gs, p.gb) && evenly(p, p.xs, p.xb) && evenly(p, p.ys, p.yb) &&
+                      (!z || (evenly(p, p.zs, p.zb) && evenly(p, p.ds, p.db))));
   const int vec = norm_vec(p, bf16, {p.dy, p.x, p.z, p.y, p.dz},
                            {p.gs, p.gb, p.xs, p.xb, p.zs, p.zb, p.ys, p.yb, p.ds, p.db});
-  return norm_plan(p, vec, true);
+  return norm_plan(p, bf16, vec, true);
 }
 
 int part_columns(const NormParams &p) { return p.shared ? p.W : p.D; }
@@ -206,8 +229,17 @@ size_t bwd_workspace(const group_norm_bwd_args &a, const NormParams &p, const No
 cudaError_t launch_norm_fwd(const NormParams &p, bool bf16, int vec, int pieces, int threads,
                             int blocks, cudaStream_t stream) {
   return norm_forms(bf16, vec, pieces, p.z != nullptr, [&](auto t, auto v, auto n, auto z) {
-    norm_fwd_kernel<decltype(t), decltype(v)::value, decltype(n)::value, decltype(z)::value>
-        <<<blocks, threads, 0, stream>>>(p);
+    using T = decltype(t);
+    constexpr int VEC = decltype(v)::value, PP = decltype(n)::value;
+    constexpr bool Z = decltype(z)::value;
+    if (threads <= NORM_THREADS) {
+      norm_fwd_kernel<T, VEC, PP, Z, false><<<blocks, threads, 0, stream>>>(p);
+    } else {  // only with the most pieces a thread
+      if constexpr (PP == norm_pieces(VEC))
+        norm_fwd_kernel<T, VEC, PP, Z, true><<<blocks, threads, 0, stream>>>(p);
+      else
+        return cudaErrorInvalidConfiguration;
+    }
     return cudaGetLastError();
   });
 }
@@ -231,8 +263,10 @@ gdn_status_t group_norm_fwd(const group_norm_args *a, gdn_stream_t stream) {
   p.y = a->y;
   p.ys = a->T > 1 ? a->y_stride : a->D;
   p.yb = a->B > 1 ? a->y_batch_stride : 0;
+  p.flat = p.flat || (evenly(p, p.xs, p.xb) && (p.z == nullptr || evenly(p, p.zs, p.zb)) &&
+                      evenly(p, p.ys, p.yb));
   const int vec = norm_vec(p, bf16, {p.x, p.z, p.y}, {p.xs, p.xb, p.zs, p.zb, p.ys, p.yb});
-  const NormPlan plan = norm_plan(p, vec, false);
+  const NormPlan plan = norm_plan(p, bf16, vec, false);
   p.err = device_error_word();
   if (p.err == nullptr) return launch_status(cudaGetLastError(), "device error word");
   return launch_status(launch_norm_fwd(p, bf16, plan.vec, plan.pieces, plan.threads, plan.blocks,

@@ -3,9 +3,16 @@
 //
 // A team of threads (a power of two, of one warp or several) holds one token's group in
 // registers: PP pieces of VEC channels a thread, `team` pieces apart, so that a warp's loads
-// are contiguous.  A team keeps its group and walks tokens, so that its weights are loaded
-// once and, in the gradient, its sums over tokens stay in registers.  The next token's rows
-// are on their way while one is computed: the operator is bound by memory.
+// are contiguous.  A team keeps its group and walks tokens, so that its weights stay in L1 and,
+// in the gradient, its sums over tokens in registers.  The next tokens' rows are on their way
+// while one is computed, and each tensor's place moves on by one addition.
+//
+// The floor is the rows' bytes, but at 16 channels a lane the instructions are what bounds it
+// (issue slots 70% full, DRAM 60%): hence arithmetic on two values an instruction and weights
+// in the rows' own type.  Forward with a gate, bf16: 2 x 4096 tokens of 16 heads of 128 take
+// 24.6 us (4.1 TB/s of 6.8), 32068 tokens of 8 groups of 512 take 122 us (4.3 TB/s); the
+// gradient of the first 51.4 us (3.3 TB/s).  With one token ahead, weights held in registers
+// and scalar arithmetic they took 28.7, 139.6 and 59.5 us.
 #pragma once
 
 #include <type_traits>
@@ -22,6 +29,7 @@ struct NormParams {
   int64_t gs, gb, xs, xb, zs, zb, ys, yb, ds, db;
   int tokens, T, G, W, D;     // all tokens, tokens of a batch row
   int shared, w_f32, center, gate_first, act;
+  int flat;                   // tokens of all batch rows one stride apart
   float eps;
   // teams: `team` threads each; `rows` tokens and `span` groups a block, blocks_per_row
   // blocks side by side over the groups; `step` tokens at once
@@ -40,6 +48,10 @@ struct NormTeam {
     t = blockIdx.x / p.blocks_per_row * p.rows + row;
     live = row < p.rows && g < p.G;
   }
+  // whether this thread's piece `from` channels behind its first is one of the group's
+  __device__ __forceinline__ bool in(const NormParams &p, int from, int vec) const {
+    return lane * vec + from < p.W;
+  }
 };
 
 constexpr int NORM_WARPS = 32;
@@ -47,10 +59,22 @@ constexpr int NORM_WARPS = 32;
 // Most threads of a block whose threads hold `elements` channels (8192 a group: 16 of them
 // want the registers of half the threads).
 constexpr int norm_threads(int elements) { return elements > 8 ? 512 : 1024; }
-// Threads of an ordinary block, and the blocks that an SM holds of them.
-constexpr int NORM_FWD_THREADS = 256, NORM_BWD_THREADS = 256;
-constexpr int norm_fwd_per_sm(int elements) { return elements > 8 ? 2 : elements > 2 ? 4 : 8; }
+// Threads of an ordinary block; tokens whose rows are on their way and blocks an SM, by the
+// words that a thread's part of a row takes (some 48 KB of an SM's are on their way).
+constexpr int NORM_THREADS = 256;
+constexpr int norm_words(int elt, int vec, int pieces) {
+  return pieces * (vec * elt >= 4 ? vec * elt / 4 : 1);
+}
+constexpr int norm_fwd_ahead(int words, bool z) { return words > 8 ? 1 : words > 4 || z ? 2 : 3; }
+constexpr int norm_fwd_per_sm(int elements, int words, bool z) {
+  return words > 8 || (elements > 8 && z) ? 2 : words > 4 || z ? 3 : elements > 2 ? 4 : 6;
+}
+constexpr int norm_bwd_ahead(int words) { return words > 4 ? 1 : 2; }
 constexpr int norm_bwd_per_sm(int elements) { return elements > 8 ? 1 : elements > 2 ? 2 : 4; }
+// A block's threads: NORM_THREADS, or what the widest groups want.
+constexpr int norm_block(int elements, bool wide) {
+  return wide ? norm_threads(elements) : NORM_THREADS;
+}
 // Most pieces a thread takes.
 constexpr int norm_pieces(int vec) { return vec == 8 ? 2 : vec == 4 ? 4 : 8; }
 
@@ -59,9 +83,11 @@ constexpr int norm_pieces(int vec) { return vec == 8 ? 2 : vec == 4 ? 4 : 8; }
 template <int N>
 __device__ __forceinline__ void team_sum(float (&v)[N], int team, float (*buf)[NORM_WARPS][2],
                                          int &turn) {
-  for (int o = min(team, 32) >> 1; o > 0; o >>= 1)
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(~0u, v[i], o);
+  for (int o = 16; o > 0; o >>= 1)
+    if (team > o)
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(~0u, v[i], o);
   if (team <= 32) return;
   const int warp = threadIdx.x >> 5, each = team >> 5, first = warp / each * each;
   if ((threadIdx.x & 31) == 0)
@@ -76,81 +102,163 @@ __device__ __forceinline__ void team_sum(float (&v)[N], int team, float (*buf)[N
   turn ^= 1;
 }
 
-// 1 / (1 + e^-z) of VEC values (two an instruction where there are two)
+// Element-wise operations on VEC values, two an instruction where there are two.
 template <int VEC>
-__device__ __forceinline__ void norm_sigmoid(float *out, const float *z) {
+__device__ __forceinline__ void vmul(float *out, const float *a, const float *b) {
   if constexpr (VEC == 1)
-    out[0] = __fdividef(1.f, 1.f + __expf(-z[0]));
+    out[0] = a[0] * b[0];
   else
-    sigmoid_row<VEC>(out, z);
+    mul_row<VEC>(out, a, b);
+}
+template <int VEC>
+__device__ __forceinline__ void vmul(float *out, const float *a, float f) {
+  const float b[2] = {f, f};
+#pragma unroll
+  for (int e = 0; e < VEC; e += 2) vmul<VEC == 1 ? 1 : 2>(out + e, a + e, b);
+}
+template <int VEC>
+__device__ __forceinline__ void vadd(float *out, const float *a, const float *b) {
+  if constexpr (VEC == 1)
+    out[0] = a[0] + b[0];
+  else
+    add_row<VEC>(out, a, b);
+}
+template <int VEC>
+__device__ __forceinline__ void vsub(float *out, const float *a, float f) {
+  const float b[2] = {f, f};
+#pragma unroll
+  for (int e = 0; e < VEC; e += 2) {
+    if constexpr (VEC == 1)
+      out[0] = a[0] - f;
+    else
+      sub_row<2>(out + e, a + e, b);
+  }
+}
+// out = a b + c, and with one factor for all
+template <int VEC>
+__device__ __forceinline__ void vfma(float *out, const float *a, const float *b, const float *c) {
+  if constexpr (VEC == 1)
+    out[0] = fmaf(a[0], b[0], c[0]);
+  else
+    fma_rows<VEC>(out, a, b, c);
+}
+template <int VEC>
+__device__ __forceinline__ void vfma(float *out, const float *a, float f, const float *c) {
+  const float b[2] = {f, f};
+#pragma unroll
+  for (int e = 0; e < VEC; e += 2) vfma<VEC == 1 ? 1 : 2>(out + e, a + e, b, c + e);
+}
+// Two partial sums of products, and of values.
+template <int VEC>
+__device__ __forceinline__ void vdot(float (&sum)[2], const float *a, const float *b) {
+#pragma unroll
+  for (int e = 0; e < VEC; e += 2) vfma<VEC == 1 ? 1 : 2>(sum, a + e, b + e, sum);
+}
+template <int VEC>
+__device__ __forceinline__ void vsum(float (&sum)[2], const float *a) {
+#pragma unroll
+  for (int e = 0; e < VEC; e += 2) vadd<VEC == 1 ? 1 : 2>(sum, sum, a + e);
 }
 
-// act(z), and its derivative where wanted
-template <int VEC>
+// act(z) (out may be z), and its derivative where wanted: s (1 + z (1 - s)) or s (1 - s) with
+// s = 1 / (1 + e^-z).
+template <int VEC, bool SLOPE>
 __device__ __forceinline__ void norm_act(int act, const float *z, float *out, float *slope) {
-  float s[VEC];
   if (act == GDN_ACT_NONE) {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       out[e] = z[e];
-      if (slope) slope[e] = 1.f;
+      if (SLOPE) slope[e] = 1.f;
     }
     return;
   }
-  norm_sigmoid<VEC>(s, z);
+  float s[VEC], rest[VEC];
+  if constexpr (VEC == 1)
+    s[0] = __fdividef(1.f, 1.f + __expf(-z[0]));
+  else
+    sigmoid_row<VEC>(s, z);
+  if constexpr (SLOPE) {
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) {
-    const float v = z[e];  // (out may be z)
-    out[e] = act == GDN_ACT_SILU ? v * s[e] : s[e];
-    if (slope) slope[e] = s[e] * fmaf(act == GDN_ACT_SILU ? v : 1.f, 1.f - s[e],
-                                      act == GDN_ACT_SILU ? 1.f : 0.f);
+    for (int e = 0; e < VEC; ++e) rest[e] = 1.f - s[e];
+  }
+  if (act == GDN_ACT_SILU) {
+    vmul<VEC>(out, z, s);
+    if constexpr (SLOPE) vfma<VEC>(slope, out, rest, s);
+  } else {
+    if constexpr (SLOPE) vmul<VEC>(slope, s, rest);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) out[e] = s[e];
   }
 }
 
-// Weights or biases of a team's channels (`none` where there are none).
-template <typename T, int VEC, int PP>
+// A piece of weights or biases (zero past the group), which lies as wide as the rows'.
+template <typename T, int VEC>
 __device__ __forceinline__ void norm_weights(const NormParams &p, const NormTeam &m,
-                                             const void *from, float none, float (&w)[PP][VEC]) {
-  const int base = p.shared ? 0 : m.g * p.W;
+                                             const void *from, int piece, float *w) {
+  const int c = (m.lane + piece * p.team) * VEC;
+  if (!m.live || c >= p.W) {
 #pragma unroll
-  for (int j = 0; j < PP; ++j) {
-    const int c = (m.lane + j * p.team) * VEC;
+    for (int e = 0; e < VEC; ++e) w[e] = 0.f;
+    return;
+  }
+  const int64_t at = (p.shared ? 0 : (int64_t)m.g * p.W) + c;
+  if (p.w_f32) {
+    constexpr int N = VEC >= 4 ? 4 : VEC;
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) w[j][e] = none;
-    if (from == nullptr || !m.live || c >= p.W) continue;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e)
-      w[j][e] = p.w_f32 ? static_cast<const float *>(from)[base + c + e]
-                        : to_f32(static_cast<const T *>(from)[base + c + e]);
+    for (int e = 0; e < VEC; e += N) {
+      Row<float, N> r;
+      r.load(static_cast<const float *>(from) + at + e);
+      r.widen(w + e);
+    }
+  } else {
+    Row<T, VEC> r;
+    r.load(static_cast<const T *>(from) + at);
+    r.widen(w);
   }
 }
+
+// A team's way through one tensor: where the next token's pieces of it are.  (A place is
+// worked out once where tokens lie one stride apart, then moved on.)
+template <typename T>
+struct NormCursor {
+  T *at;
+  int64_t stride, batch, move;
+  __device__ __forceinline__ NormCursor(const NormParams &p, const NormTeam &m, const void *base,
+                                        int64_t stride_, int64_t batch_, int vec)
+      : stride(stride_), batch(batch_), move(p.step * stride_) {
+    at = static_cast<T *>(const_cast<void *>(base)) + (int64_t)m.g * p.W + m.lane * vec;
+    if (p.flat) at += m.t * stride;
+  }
+  // token t's place (of tokens taken in turn)
+  __device__ __forceinline__ T *next(const NormParams &p, int t) {
+    if (p.flat) {
+      T *here = at;
+      at += move;
+      return here;
+    }
+    const int b = t / p.T;
+    return at + b * batch + (t - b * p.T) * stride;
+  }
+};
 
 // A token's pieces of one tensor, as they lie in memory.
 template <typename T, int VEC, int PP>
 struct NormRow {
   Row<T, VEC> r[PP];
-  __device__ __forceinline__ void load(const NormParams &p, const NormTeam &m, const void *base,
-                                       int64_t stride, int64_t batch, int t) {
+  __device__ __forceinline__ void load(const NormParams &p, const NormTeam &m, NormCursor<T> &c, int t) {
+    const T *at = c.next(p, t);
     if (!m.live || t >= p.tokens) return;
-    const int b = t / p.T;
-    const T *at = static_cast<const T *>(base) + b * batch + (t - b * p.T) * stride +
-                  (int64_t)m.g * p.W;
 #pragma unroll
-    for (int j = 0; j < PP; ++j) {
-      const int c = (m.lane + j * p.team) * VEC;
-      if (c < p.W) r[j].load(at + c);
-    }
+    for (int j = 0; j < PP; ++j)
+      if (m.in(p, j * VEC * p.team, VEC)) r[j].load(at + j * VEC * p.team);
   }
-  __device__ __forceinline__ void store(const NormParams &p, const NormTeam &m, void *base,
-                                        int64_t stride, int64_t batch, int t) const {
+  __device__ __forceinline__ void store(const NormParams &p, const NormTeam &m, NormCursor<T> &c,
+                                        int t) const {
+    T *at = c.next(p, t);
     if (!m.live || t >= p.tokens) return;
-    const int b = t / p.T;
-    T *at = static_cast<T *>(base) + b * batch + (t - b * p.T) * stride + (int64_t)m.g * p.W;
 #pragma unroll
-    for (int j = 0; j < PP; ++j) {
-      const int c = (m.lane + j * p.team) * VEC;
-      if (c < p.W) r[j].store(at + c);
-    }
+    for (int j = 0; j < PP; ++j)
+      if (m.in(p, j * VEC * p.team, VEC)) r[j].store(at + j * VEC * p.team);
   }
   __device__ __forceinline__ void zero() {
 #pragma unroll
@@ -158,40 +266,31 @@ struct NormRow {
   }
 };
 
-// u to its normal form in place; returns 1 / root.  Pieces past the group hold zero and
+// Takes u's mean off (where wanted) and returns 1 / root.  Pieces past the group hold zero and
 // stay so.
 template <int VEC, int PP>
-__device__ __forceinline__ float normalise(const NormParams &p, const NormTeam &m,
+__device__ __forceinline__ float norm_root(const NormParams &p, const NormTeam &m,
                                            float (&u)[PP][VEC], float (*buf)[NORM_WARPS][2],
                                            int &turn) {
   const float inv = 1.f / (float)p.W;
-  float s[1] = {0.f};
+  float v[1];
   if (p.center) {
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < PP; ++j) vsum<VEC>(s, u[j]);
+    v[0] = s[0] + s[1];
+    team_sum(v, p.team, buf, turn);
+    const float mean = v[0] * inv;
 #pragma unroll
     for (int j = 0; j < PP; ++j)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) s[0] += u[j][e];
-    team_sum(s, p.team, buf, turn);
-    const float mean = s[0] * inv;
-#pragma unroll
-    for (int j = 0; j < PP; ++j)
-      if ((m.lane + j * p.team) * VEC < p.W)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) u[j][e] -= mean;
-    s[0] = 0.f;
+      if (m.in(p, j * VEC * p.team, VEC)) vsub<VEC>(u[j], u[j], mean);
   }
+  float s[2] = {0.f, 0.f};
 #pragma unroll
-  for (int j = 0; j < PP; ++j)
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) s[0] = fmaf(u[j][e], u[j][e], s[0]);
-  team_sum(s, p.team, buf, turn);
-  const float r = 1.f / sqrtf(fmaf(s[0], inv, p.eps));
-#pragma unroll
-  for (int j = 0; j < PP; ++j)
-    if ((m.lane + j * p.team) * VEC < p.W)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) u[j][e] *= r;
-  return r;
+  for (int j = 0; j < PP; ++j) vdot<VEC>(s, u[j], u[j]);
+  v[0] = s[0] + s[1];
+  team_sum(v, p.team, buf, turn);
+  return rsqrtf(fmaf(v[0], inv, p.eps));
 }
 
 cudaError_t launch_norm_fwd(const NormParams &p, bool bf16, int vec, int pieces, int threads,

@@ -12,13 +12,8 @@
 namespace gdn {
 namespace {
 
-// Threads of a block: 256, or what the widest groups want (WIDE).
-constexpr int bwd_threads(int elements, bool wide) {
-  return wide ? norm_threads(elements) : NORM_BWD_THREADS;
-}
-
 template <typename T, int VEC, int PP, bool Z, bool WIDE>
-__global__ void __launch_bounds__(bwd_threads(PP * VEC, WIDE), WIDE ? 1 : norm_bwd_per_sm(PP * VEC))
+__global__ void __launch_bounds__(norm_block(PP * VEC, WIDE), WIDE ? 1 : norm_bwd_per_sm(PP * VEC))
 norm_bwd_kernel(NormParams p) {
   __shared__ float buf[2][NORM_WARPS][2];
   extern __shared__ float sums[];  // [threads][PP * VEC]
@@ -26,105 +21,115 @@ norm_bwd_kernel(NormParams p) {
   if (!bounds_ok(p.team * p.rows * p.span <= (int)blockDim.x, p.err)) return;
   int turn = 0;
   const float inv = 1.f / (float)p.W;
-  float w[PP][VEC], b[PP][VEC], dw[PP][VEC], db[PP][VEC];
-  NormRow<T, VEC, PP> x, z, g;
-  x.zero();
-  z.zero();
-  g.zero();
-  g.load(p, m, p.dy, p.gs, p.gb, m.t);
-  x.load(p, m, p.x, p.xs, p.xb, m.t);
-  if (Z) z.load(p, m, p.z, p.zs, p.zb, m.t);
-  norm_weights<T>(p, m, p.weight, 1.f, w);
-  norm_weights<T>(p, m, p.bias, 0.f, b);
+  constexpr int AHEAD = WIDE ? 1 : norm_bwd_ahead(norm_words(sizeof(T), VEC, PP));
+  float dw[PP][VEC], db[PP][VEC];
+  NormCursor<T> gc(p, m, p.dy, p.gs, p.gb, VEC), xc(p, m, p.x, p.xs, p.xb, VEC);
+  NormCursor<T> zc(p, m, p.z, p.zs, p.zb, VEC), dxc(p, m, p.y, p.ys, p.yb, VEC);
+  NormCursor<T> dzc(p, m, p.dz, p.ds, p.db, VEC);
+  NormRow<T, VEC, PP> x[AHEAD], z[Z ? AHEAD : 1], g[AHEAD];
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) {
+    x[i].zero();
+    g[i].zero();
+    g[i].load(p, m, gc, m.t + i * p.step);
+    x[i].load(p, m, xc, m.t + i * p.step);
+    if constexpr (Z) {
+      z[i].zero();
+      z[i].load(p, m, zc, m.t + i * p.step);
+    }
+  }
 #pragma unroll
   for (int j = 0; j < PP; ++j)
 #pragma unroll
     for (int e = 0; e < VEC; ++e) dw[j][e] = db[j][e] = 0.f;
   const int first = blockIdx.x / p.blocks_per_row * p.rows;
-  for (int t0 = first, t = m.t; t0 < p.tokens; t0 += p.step, t += p.step) {
-    const bool there = m.live && t < p.tokens;
-    float n[PP][VEC], d[PP][VEC], raw[Z ? PP : 1][VEC], zv[Z ? PP : 1][VEC];
+  for (int t0 = first, t = m.t; t0 < p.tokens;) {
 #pragma unroll
-    for (int j = 0; j < PP; ++j) {
-      x.r[j].widen(n[j]);
-      g.r[j].widen(d[j]);
-      if constexpr (Z) {
-        z.r[j].widen(zv[j]);
-        if (p.gate_first) {
-          float gate[VEC];
-          norm_act<VEC>(p.act, zv[j], gate, nullptr);
+    for (int i = 0; i < AHEAD; ++i, t0 += p.step, t += p.step) {
+      if (t0 >= p.tokens) break;
+      const bool there = m.live && t < p.tokens;
+      float n[PP][VEC], d[PP][VEC], gate[Z ? PP : 1][VEC], slope[Z ? PP : 1][VEC];
+      NormRow<T, VEC, PP> raw = x[i];  // (x itself, for a gate before the norm)
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            raw[j][e] = n[j][e];
-            n[j][e] *= gate[e];
-          }
+      for (int j = 0; j < PP; ++j) {
+        x[i].r[j].widen(n[j]);
+        g[i].r[j].widen(d[j]);
+        if constexpr (Z) {
+          z[i].r[j].widen(gate[j]);
+          norm_act<VEC, true>(p.act, gate[j], gate[j], slope[j]);
+          if (p.gate_first) vmul<VEC>(n[j], n[j], gate[j]);
         }
       }
-    }
-    g.load(p, m, p.dy, p.gs, p.gb, t + p.step);
-    x.load(p, m, p.x, p.xs, p.xb, t + p.step);
-    if (Z) z.load(p, m, p.z, p.zs, p.zb, t + p.step);
-    const float r = normalise<VEC, PP>(p, m, n, buf, turn);
-    float s[2] = {0.f, 0.f};  // of dn n and of dn
-    NormRow<T, VEC, PP> out;
+      g[i].load(p, m, gc, t + AHEAD * p.step);
+      x[i].load(p, m, xc, t + AHEAD * p.step);
+      if constexpr (Z) z[i].load(p, m, zc, t + AHEAD * p.step);
+      const float r = norm_root<VEC, PP>(p, m, n, buf, turn);
+      float dots[2] = {0.f, 0.f}, total[2] = {0.f, 0.f};  // of dn n and of dn
+      NormRow<T, VEC, PP> out;
 #pragma unroll
-    for (int j = 0; j < PP; ++j) {
-      if constexpr (Z) {
-        if (!p.gate_first) {
-          float gate[VEC], slope[VEC];
-          norm_act<VEC>(p.act, zv[j], gate, slope);
+      for (int j = 0; j < PP; ++j) {
+        vmul<VEC>(n[j], n[j], r);
+        float w[VEC], v[VEC];
+        if (p.weight != nullptr) norm_weights<T, VEC>(p, m, p.weight, j, w);
+        const bool gated = Z && !p.gate_first, alone = !Z && p.act != GDN_ACT_NONE;
+        if (gated || alone) {  // m
+          if (p.weight != nullptr) {
+            vmul<VEC>(v, n[j], w);
+          } else {
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            slope[e] *= d[j][e] * fmaf(n[j][e], w[j][e], b[j][e]);
-            d[j][e] *= gate[e];
+            for (int e = 0; e < VEC; ++e) v[e] = n[j][e];
           }
-          out.r[j].round(slope);
+          if (p.bias != nullptr) {
+            float b[VEC];
+            norm_weights<T, VEC>(p, m, p.bias, j, b);
+            vadd<VEC>(v, v, b);
+          }
+          if constexpr (Z) {
+            vmul<VEC>(v, v, d[j]);
+            vmul<VEC>(v, v, slope[j]);
+            out.r[j].round(v);
+            vmul<VEC>(d[j], d[j], gate[j]);
+          } else {
+            float by[VEC];
+            norm_act<VEC, true>(p.act, v, v, by);
+            vmul<VEC>(d[j], d[j], by);
+          }
         }
-      } else if (p.act != GDN_ACT_NONE) {
-        float v[VEC], slope[VEC];
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) v[e] = fmaf(n[j][e], w[j][e], b[j][e]);
-        norm_act<VEC>(p.act, v, v, slope);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) d[j][e] *= slope[e];
-      }
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
         if (there) {
-          dw[j][e] = fmaf(d[j][e], n[j][e], dw[j][e]);
-          db[j][e] += d[j][e];
+          vfma<VEC>(dw[j], d[j], n[j], dw[j]);
+          vadd<VEC>(db[j], db[j], d[j]);
         }
-        d[j][e] *= w[j][e];
-        s[0] = fmaf(d[j][e], n[j][e], s[0]);
-        s[1] += d[j][e];
+        if (p.weight != nullptr) vmul<VEC>(d[j], d[j], w);
+        vdot<VEC>(dots, d[j], n[j]);
+        if (p.center) vsum<VEC>(total, d[j]);
       }
-    }
-    if constexpr (Z)
-      if (!p.gate_first) out.store(p, m, p.dz, p.ds, p.db, t);
-    team_sum(s, p.team, buf, turn);
-    const float a = s[0] * inv, mean = p.center ? s[1] * inv : 0.f;
-    NormRow<T, VEC, PP> dx;
+      if constexpr (Z)
+        if (!p.gate_first) out.store(p, m, dzc, t);
+      float s[2] = {dots[0] + dots[1], total[0] + total[1]};
+      team_sum(s, p.team, buf, turn);
+      const float a = -s[0] * inv, mean = s[1] * inv;
+      NormRow<T, VEC, PP> dx;
 #pragma unroll
-    for (int j = 0; j < PP; ++j) {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) d[j][e] = r * (fmaf(-n[j][e], a, d[j][e]) - mean);
-      if constexpr (Z) {
-        if (p.gate_first) {
-          float gate[VEC], slope[VEC];
-          norm_act<VEC>(p.act, zv[j], gate, slope);
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            slope[e] *= d[j][e] * raw[j][e];
-            d[j][e] *= gate[e];
+      for (int j = 0; j < PP; ++j) {
+        vfma<VEC>(d[j], n[j], a, d[j]);
+        if (p.center) vsub<VEC>(d[j], d[j], mean);
+        vmul<VEC>(d[j], d[j], r);
+        if constexpr (Z) {
+          if (p.gate_first) {
+            float u[VEC];
+            raw.r[j].widen(u);
+            vmul<VEC>(u, u, d[j]);
+            vmul<VEC>(u, u, slope[j]);
+            out.r[j].round(u);
+            vmul<VEC>(d[j], d[j], gate[j]);
           }
-          out.r[j].round(slope);
         }
+        dx.r[j].round(d[j]);
       }
-      dx.r[j].round(d[j]);
+      dx.store(p, m, dxc, t);
+      if constexpr (Z)
+        if (p.gate_first) out.store(p, m, dzc, t);
     }
-    dx.store(p, m, p.y, p.ys, p.yb, t);
-    if constexpr (Z)
-      if (p.gate_first) out.store(p, m, p.dz, p.ds, p.db, t);
   }
   if (p.part == nullptr) return;
   // a column's sums over the block's teams that hold it, in their order
@@ -181,7 +186,7 @@ cudaError_t launch_norm_bwd(const NormParams &p, bool bf16, int vec, int pieces,
     using T = decltype(t);
     constexpr int VEC = decltype(v)::value, PP = decltype(n)::value;
     constexpr bool Z = decltype(z)::value;
-    if (threads <= NORM_BWD_THREADS) {
+    if (threads <= NORM_THREADS) {
       norm_bwd_kernel<T, VEC, PP, Z, false><<<blocks, threads, smem, stream>>>(p);
     } else {  // only with the most pieces a thread
       if constexpr (PP == norm_pieces(VEC))
