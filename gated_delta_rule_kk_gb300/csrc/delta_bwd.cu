@@ -11,16 +11,25 @@
 namespace gdn {
 namespace {
 
-// First chunk of every sequence and every chunk's sequence; with bad offsets first[N] = -1,
-// and no kernel behind writes anything.  One block.
+// Sequences of about as many chunks, more of them first: four classes to a power of two.
+constexpr int CLASSES = 128;
+__device__ __forceinline__ int length_class(int chunks) {
+  return chunks == 0 ? CLASSES - 1
+                     : CLASSES - 2 - ((__float_as_int((float)chunks) >> 21) - (127 << 2));
+}
+
+// First chunk of every sequence, every chunk's sequence and the sequences by their lengths;
+// with bad offsets first[N] = -1, and no kernel behind writes anything.  One block.  (The order
+// among sequences of one class is any; it changes no result.)
 __global__ void __launch_bounds__(1024) delta_table_kernel(DeltaBwdParams p) {
-  __shared__ int sums[32], total;
+  __shared__ int sums[32], total, class_at[CLASSES];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (!offsets_ok(p.cu, p.N, p.T, p.err)) {
     if (tid == 0) p.first[p.N] = -1;
     return;
   }
   if (tid == 0) total = 0;
+  if (tid < CLASSES) class_at[tid] = 0;
   __syncthreads();
   for (int base = 0; base < p.N; base += 1024) {
     const int n = base + tid;
@@ -34,13 +43,25 @@ __global__ void __launch_bounds__(1024) delta_table_kernel(DeltaBwdParams p) {
     __syncthreads();
     int before = total;
     for (int w = 0; w < warp; ++w) before += sums[w];
-    if (n < p.N) p.first[n] = before + s - own;
+    if (n < p.N) {
+      p.first[n] = before + s - own;
+      atomicAdd(&class_at[length_class(own)], 1);
+    }
     __syncthreads();
     if (tid == 1023) total = before + s;
     __syncthreads();
   }
-  if (tid == 0) p.first[p.N] = total;
+  if (tid == 0) {
+    p.first[p.N] = total;
+    for (int c = 0, before = 0; c < CLASSES; ++c) {
+      const int here = class_at[c];
+      class_at[c] = before;
+      before += here;
+    }
+  }
   __syncthreads();
+  for (int n = tid; n < p.N; n += 1024)
+    p.order[atomicAdd(&class_at[length_class(p.first[n + 1] - p.first[n])], 1)] = n;
   if (!bounds_ok(total <= p.chunks, p.err)) return;
   for (int c = tid; c < total; c += 1024) {  // the last sequence that begins at c or before
     int lo = 0, hi = p.N - 1;
@@ -117,7 +138,7 @@ DeltaBwdParams make_params(const gdn_chunk_bwd_args &a) {
 // The table, rounded up to 256 bytes, then the blocks, then scratch.
 size_t table_bytes(const DeltaBwdParams &p) {
   if (p.cu == nullptr) return 0;
-  return ((size_t)(p.N + 1 + p.chunks) * sizeof(int32_t) + 255) / 256 * 256;
+  return ((size_t)(2 * (int64_t)p.N + 1 + p.chunks) * sizeof(int32_t) + 255) / 256 * 256;
 }
 
 size_t workspace_bytes(const DeltaBwdParams &p, bool bf16) {
@@ -162,7 +183,8 @@ gdn_status_t gdn_chunk_bwd(const gdn_chunk_bwd_args *a, gdn_stream_t stream) {
              "workspace of %zu bytes needed (got %zu)", need, a->workspace_bytes);
   CHECK_THAT(aligned_to(a->workspace, 256), GDN_ERR_MISALIGNED, "workspace is not 256-byte aligned");
   p.first = static_cast<int32_t *>(a->workspace);
-  p.owner = p.first + p.N + 1;
+  p.order = p.first + p.N + 1;
+  p.owner = p.order + p.N;
   p.blocks = static_cast<unsigned char *>(a->workspace) + table_bytes(p);
   p.scratch = reinterpret_cast<float *>(p.blocks + (size_t)p.chunks * p.H * p.block);
   p.err = device_error_word();

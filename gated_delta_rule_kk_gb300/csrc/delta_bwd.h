@@ -41,6 +41,7 @@ struct DeltaBwdParams {
   int64_t chunks;             // chunks at most
   // workspace
   int32_t *first;             // [N + 1] first chunk of every sequence (cu given)
+  int32_t *order;             // [N] the sequences, longest first (about)
   int32_t *owner;             // [chunks] sequence of every chunk
   unsigned char *blocks;      // [chunks][H] of `block` bytes each
   int64_t block;
@@ -71,6 +72,12 @@ __device__ __forceinline__ DeltaChunk delta_chunk(const DeltaBwdParams &p, int64
   k.len = min(64, p.cu[k.n + 1] - lo - k.i * 64);
   k.token = lo + k.i * 64;
   return k;
+}
+
+// The sequence that the i-th blocks of a walk take: a walk is as long as its sequence, and one
+// that is begun last ends last.  Only behind delta_good().
+__device__ __forceinline__ int delta_turn(const DeltaBwdParams &p, int i) {
+  return p.cu == nullptr ? i : p.order[i];
 }
 
 // The chunks of sequence n: the first one, and how many; 0 with bad offsets.

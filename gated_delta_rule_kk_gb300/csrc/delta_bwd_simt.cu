@@ -132,11 +132,11 @@ __global__ void __launch_bounds__(THREADS) simt_prepare_kernel(DeltaBwdParams p)
 template <typename E>
 __global__ void __launch_bounds__(THREADS) simt_states_kernel(DeltaBwdParams p) {
   __shared__ __align__(16) float tiles[2 * TILE];
-  const int v0 = blockIdx.x * COLS, nv = min(COLS, p.V - v0), head = blockIdx.y, n = blockIdx.z;
+  const int v0 = blockIdx.x * COLS, nv = min(COLS, p.V - v0), head = blockIdx.y;
   const int hk = head / (p.H / p.Hg), K = p.K, V = p.V;
   int64_t first;
   if (!delta_good(p)) return;
-  const int count = delta_chunks(p, n, &first);
+  const int n = delta_turn(p, blockIdx.z), count = delta_chunks(p, n, &first);
   if (count == 0) return;
   {
     const Block w(p, first, head);
@@ -174,11 +174,11 @@ __global__ void __launch_bounds__(THREADS) simt_states_kernel(DeltaBwdParams p) 
 template <typename E>
 __global__ void __launch_bounds__(THREADS) simt_grads_kernel(DeltaBwdParams p) {
   __shared__ __align__(16) float tiles[2 * TILE];
-  const int v0 = blockIdx.x * COLS, nv = min(COLS, p.V - v0), head = blockIdx.y, n = blockIdx.z;
+  const int v0 = blockIdx.x * COLS, nv = min(COLS, p.V - v0), head = blockIdx.y;
   const int hk = head / (p.H / p.Hg), K = p.K, V = p.V;
   int64_t first;
   if (!delta_good(p)) return;
-  const int count = delta_chunks(p, n, &first);
+  const int n = delta_turn(p, blockIdx.z), count = delta_chunks(p, n, &first);
   const int64_t state = ((int64_t)n * p.H + head) * K * V;
   auto outer = [&](int c, int j) {  // of h0, dht and dh0
     return state + (p.v_first ? (int64_t)j * K + c : (int64_t)c * V + j);

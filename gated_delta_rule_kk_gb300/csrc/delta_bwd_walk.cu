@@ -395,7 +395,6 @@ __device__ __forceinline__ bool begin_walk(const DeltaBwdParams &p, Walk<KP, BAC
   w.vt = blockIdx.x;
   w.v0 = w.vt * VT;
   w.head = blockIdx.y;
-  w.n = blockIdx.z;
   w.hk = w.head / (p.H / p.Hg);
   w.role = warp / CARRY;
   w.vw = warp % CARRY / 2;
@@ -405,6 +404,7 @@ __device__ __forceinline__ bool begin_walk(const DeltaBwdParams &p, Walk<KP, BAC
   w.t = w.lane & 3;
   w.ok = true;
   if (!delta_good(p)) return false;
+  w.n = delta_turn(p, blockIdx.z);
   w.count = delta_chunks(p, w.n, &w.first);
   if (!bounds_ok(w.v0 < p.V && w.head < p.H && w.n < p.N && w.first + w.count <= p.chunks, p.err))
     return false;

@@ -107,6 +107,18 @@ def test_delta_gradient_of_resets_and_of_beta_zero(dtype):
     assert got[3][:, ::5].abs().max() <= 2.0 ** -17 * got[3].abs().max()
 
 
+@pytest.mark.parametrize("dtype,K", [(BF16, 16), (F32, 12)])
+def test_delta_gradient_of_more_sequences_than_threads(dtype, K):
+    """1100 sequences of nothing to a few tokens, some of several chunks: the order in which
+    they are taken is by their lengths."""
+    lens = [n % 3 for n in range(1100)]
+    lens[5], lens[700], lens[1099] = 200, 65, 130
+    i = delta_inputs(17, 1, sum(lens), 1, 1, K, K, dtype, lens)
+    got = run_delta(cuda(i))
+    ok()
+    check_delta(got, i, pieces=dtype is BF16, norm=False)
+
+
 def test_delta_gradient_of_growing_states():
     """Gates above zero: the running sums grow to +20 within a chunk."""
     i = delta_inputs(10, 1, 130, 2, 2, 64, 64, BF16)
