@@ -3,7 +3,12 @@
 // the formulas.
 //
 // All products go through one tiled product of a block (64 x 64 outputs, 16 of them a thread,
-// operands read through functions, so that gates, masks and transposes need no copies).
+// operands read through functions, so that gates, masks and transposes need no copies).  What
+// bounds a call of few heads is the latency of the products that wait for one another along a
+// walk: the next 32 steps' operands are on their way in registers while 32 are multiplied, and
+// every load is of a place that exists, with the value chosen behind it, so that no load waits
+// for another.  (Three sequences of 261 to 376 tokens, 12 heads of 48 x 40, float32: SIMT_US us;
+// with 16 steps a tile, two barriers each, and loads inside branches 502 us.)
 #include "delta_bwd.h"
 #include "gdn_common.cuh"
 
@@ -11,7 +16,9 @@ namespace gdn {
 namespace {
 
 constexpr int Q = 64, THREADS = 256, COLS = 64;
-constexpr int TILE = 16 * (Q + 4);  // floats of one operand's tile
+constexpr int DEPTH = 32, TILE = DEPTH * (Q + 4);  // steps and floats of one operand's tile
+constexpr int TILES = 4 * TILE;      // two operands, two buffers
+constexpr int SIDE = Q + 1;          // pitch of square matrices in shared memory
 
 // A chunk and head's floats: running log-gates and beta, T, P, n and dr [64][V], the state
 // and its gradient [K][V].
@@ -34,36 +41,69 @@ int64_t block_floats(const DeltaBwdParams &p) {
   return 2 * Q + 2 * Q * Q + 2 * (int64_t)(Q + p.K) * p.V;
 }
 
-// out(i, j, sum_k a(i, k) b(k, j)) for i < M, j < N.  `tiles` is shared memory of 2 TILE
-// floats.  Every operand is read before the first output of its 64 x 64 tile is written.
-template <typename A, typename B, typename Out>
+// Which of an operand's indexes neighbouring threads take: the one along which it is stored.
+enum Along { ROWS, STEPS };  // (a's rows and b's columns; or the steps of the sum)
+
+template <Along ALONG>
+__device__ __forceinline__ void tile_place(int e, int &row, int &step) {
+  const int tid = threadIdx.x;
+  if (ALONG == STEPS) {  // eight steps of four rows a warp: whole sectors, no bank twice
+    step = tid % 8 + 8 * (e % 4);
+    row = tid / 8 + 32 * (e / 4);
+  } else {
+    row = tid % 64;
+    step = tid / 64 + 4 * e;
+  }
+}
+
+// out(i, j, sum_k a(i, k) b(k, j)) for i < M, j < N; a and b are only asked for what is inside.
+// `tiles` is shared memory of TILES floats.  Every operand is read before the first output of
+// its 64 x 64 tile is written.
+template <Along A_ALONG, Along B_ALONG, typename A, typename B, typename Out>
 __device__ __forceinline__ void product(int M, int N, int K, float *tiles, A a, B b, Out out) {
-  float *as = tiles, *bs = tiles + TILE;
-  const int tid = threadIdx.x, ti = tid / 16 * 4, tj = tid % 16 * 4;
+  constexpr int EACH = DEPTH * Q / THREADS, PITCH = Q + 4;
+  const int ti = threadIdx.x / 16 * 4, tj = threadIdx.x % 16 * 4;
   for (int i0 = 0; i0 < M; i0 += 64)
     for (int j0 = 0; j0 < N; j0 += 64) {
-      float acc[4][4] = {};
-      for (int k0 = 0; k0 < K; k0 += 16) {
+      float acc[4][4] = {}, x[EACH], y[EACH];
+      auto fetch = [&](int k0) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int x = tid + e * THREADS;
-          const int ai = i0 + x / 16, ak = k0 + x % 16, bk = k0 + x / 64, bj = j0 + x % 64;
-          as[x % 16 * 68 + x / 16] = ai < M && ak < K ? a(ai, ak) : 0.f;
-          bs[x / 64 * 68 + x % 64] = bk < K && bj < N ? b(bk, bj) : 0.f;
+        for (int e = 0; e < EACH; ++e) {
+          int r, k;
+          tile_place<A_ALONG>(e, r, k);
+          const float u = a(min(i0 + r, M - 1), min(k0 + k, K - 1));
+          x[e] = i0 + r < M && k0 + k < K ? u : 0.f;
+          tile_place<B_ALONG>(e, r, k);
+          const float v = b(min(k0 + k, K - 1), min(j0 + r, N - 1));
+          y[e] = j0 + r < N && k0 + k < K ? v : 0.f;
+        }
+      };
+      fetch(0);
+      for (int k0 = 0, turn = 0; k0 < K; k0 += DEPTH, turn ^= 1) {
+        float *as = tiles + turn * 2 * TILE, *bs = as + TILE;
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) {
+          int r, k;
+          tile_place<A_ALONG>(e, r, k);
+          as[k * PITCH + r] = x[e];
+          tile_place<B_ALONG>(e, r, k);
+          bs[k * PITCH + r] = y[e];
         }
         __syncthreads();
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float4 u = *reinterpret_cast<const float4 *>(as + k * 68 + ti);
-          const float4 v = *reinterpret_cast<const float4 *>(bs + k * 68 + tj);
-          const float x[4] = {u.x, u.y, u.z, u.w}, y[4] = {v.x, v.y, v.z, v.w};
+        if (k0 + DEPTH < K) fetch(k0 + DEPTH);
+        const int steps = min(DEPTH, K - k0);
+#pragma unroll 8
+        for (int k = 0; k < steps; ++k) {
+          const float4 u = *reinterpret_cast<const float4 *>(as + k * PITCH + ti);
+          const float4 v = *reinterpret_cast<const float4 *>(bs + k * PITCH + tj);
+          const float f[4] = {u.x, u.y, u.z, u.w}, g[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
+            for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(f[i], g[j], acc[i][j]);
         }
-        __syncthreads();
       }
+      __syncthreads();  // the tiles have been read
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -83,16 +123,19 @@ struct Rows {
       : at(static_cast<const E *>(base) + (token * heads + head) * D), stride((int64_t)heads * D),
         len(len_) {}
   __device__ float operator()(int i, int c) const {
-    return i < len ? to_f32(at[i * stride + c]) : 0.f;
+    const float x = to_f32(at[min(i, len - 1) * stride + c]);
+    return i < len ? x : 0.f;
   }
 };
 
 // grid: chunks, heads.  G, beta, P, A and T = (I + A)^-1 by forward substitution, a column a
-// thread (the columns of the identity, so that row i of T needs the rows before it).
+// thread (the columns of the identity, so that row i of T needs the rows before it), which
+// holds it in registers.
 template <typename E>
 __global__ void __launch_bounds__(THREADS) simt_prepare_kernel(DeltaBwdParams p) {
-  __shared__ __align__(16) float tiles[2 * TILE];
-  __shared__ float A[Q][Q + 1], G[Q], beta[Q];
+  extern __shared__ __align__(16) float shared[];
+  __shared__ float G[Q], beta[Q];
+  float *tiles = shared, *A = shared + TILES;  // [Q][Q]
   const DeltaChunk ch = delta_chunk(p, blockIdx.x);
   const int head = blockIdx.y, hk = head / (p.H / p.Hg), tid = threadIdx.x;
   if (ch.len <= 0) return;
@@ -113,25 +156,53 @@ __global__ void __launch_bounds__(THREADS) simt_prepare_kernel(DeltaBwdParams p)
   }
   const Rows<E> q(p.q, ch.token, p.Hg, hk, p.K, ch.len), k(p.k, ch.token, p.Hg, hk, p.K, ch.len);
   auto kt = [&](int c, int j) { return k(j, c); };
-  product(Q, Q, p.K, tiles, q, kt, [&](int i, int j, float s) {
+  product<STEPS, STEPS>(Q, Q, p.K, tiles, q, kt, [&](int i, int j, float s) {
     w.P[i * Q + j] = i >= j ? p.scale * s * expf(G[i] - G[j]) : 0.f;
   });
-  product(Q, Q, p.K, tiles, k, kt, [&](int i, int j, float s) {
-    A[i][j] = i > j ? beta[i] * s * expf(G[i] - G[j]) : 0.f;
+  product<STEPS, STEPS>(Q, Q, p.K, tiles, k, kt, [&](int i, int j, float s) {
+    A[i * Q + j] = i > j ? beta[i] * s * expf(G[i] - G[j]) : 0.f;
   });
   if (tid < Q) {
+    float x[Q];
+#pragma unroll
     for (int i = 0; i < Q; ++i) {
-      float s = i == tid ? 1.f : 0.f;
-      for (int m = tid; m < i; ++m) s = fmaf(-A[i][m], w.T[m * Q + tid], s);
-      w.T[i * Q + tid] = i >= tid ? s : 0.f;
+      float s[4] = {i == tid ? 1.f : 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int m = 0; m < i; m += 4) {
+        const float4 u = *reinterpret_cast<const float4 *>(A + i * Q + m);
+        s[0] = fmaf(-u.x, x[m], s[0]);
+        if (m + 1 < i) s[1] = fmaf(-u.y, x[m + 1], s[1]);
+        if (m + 2 < i) s[2] = fmaf(-u.z, x[m + 2], s[2]);
+        if (m + 3 < i) s[3] = fmaf(-u.w, x[m + 3], s[3]);
+      }
+      x[i] = (s[0] + s[1]) + (s[2] + s[3]);
+      w.T[i * Q + tid] = x[i];
     }
   }
 }
 
+// The factors of a chunk's rows in a walk: beta, e^G and e^(G_L - G), which is zero past the
+// chunk's end (there the gate may not be a sum).
+struct Factors {
+  float beta[Q], eG[Q], eR[Q];
+  __device__ __forceinline__ void load(const Block &w, int len) {
+    __syncthreads();  // the ones before have been read
+    if (threadIdx.x < Q) {
+      const int i = threadIdx.x;
+      const float G = w.G[i], GL = w.G[len - 1];
+      beta[i] = w.beta[i];
+      eG[i] = expf(G);
+      eR[i] = i < len ? expf(GL - G) : 0.f;
+    }
+    __syncthreads();
+  }
+};
+
 // grid: 64 value columns, heads, sequences.  The states, forward.
 template <typename E>
 __global__ void __launch_bounds__(THREADS) simt_states_kernel(DeltaBwdParams p) {
-  __shared__ __align__(16) float tiles[2 * TILE];
+  __shared__ __align__(16) float tiles[TILES];
+  __shared__ Factors f;
   const int v0 = blockIdx.x * COLS, nv = min(COLS, p.V - v0), head = blockIdx.y;
   const int hk = head / (p.H / p.Hg), K = p.K, V = p.V;
   int64_t first;
@@ -152,28 +223,30 @@ __global__ void __launch_bounds__(THREADS) simt_states_kernel(DeltaBwdParams p) 
     const DeltaChunk ch = delta_chunk(p, first + c);
     const Block w(p, first + c, head);
     const Rows<E> k(p.k, ch.token, p.Hg, hk, K, ch.len), v(p.v, ch.token, p.H, head, V, ch.len);
-    product(Q, nv, K, tiles, k, [&](int i, int j) { return w.h[(int64_t)i * V + v0 + j]; },
-            [&](int i, int j, float s) {
-              w.n[(int64_t)i * V + v0 + j] = w.beta[i] * (v(i, v0 + j) - expf(w.G[i]) * s);
-            });
+    f.load(w, ch.len);
+    product<STEPS, ROWS>(Q, nv, K, tiles, k, [&](int i, int j) { return w.h[(int64_t)i * V + v0 + j]; },
+                         [&](int i, int j, float s) {
+                           w.n[(int64_t)i * V + v0 + j] = f.beta[i] * (v(i, v0 + j) - f.eG[i] * s);
+                         });
     auto rows = [&](int i, int j) { return w.n[(int64_t)i * V + v0 + j]; };
-    product(Q, nv, Q, tiles, [&](int i, int m) { return w.T[i * Q + m]; }, rows,
-            [&](int i, int j, float s) { w.n[(int64_t)i * V + v0 + j] = s; });
+    product<STEPS, ROWS>(Q, nv, Q, tiles, [&](int i, int m) { return w.T[i * Q + m]; }, rows,
+                         [&](int i, int j, float s) { w.n[(int64_t)i * V + v0 + j] = s; });
     if (c + 1 == count) break;
     const Block next(p, first + c + 1, head);
-    const float GL = w.G[ch.len - 1], keep = expf(GL);
-    product(K, nv, ch.len, tiles, [&](int kc, int i) { return k(i, kc) * expf(GL - w.G[i]); }, rows,
-            [&](int kc, int j, float s) {
-              const int64_t at = (int64_t)kc * V + v0 + j;
-              next.h[at] = fmaf(keep, w.h[at], s);
-            });
+    const float keep = f.eG[ch.len - 1];
+    product<ROWS, ROWS>(K, nv, ch.len, tiles, [&](int kc, int i) { return k(i, kc) * f.eR[i]; }, rows,
+                        [&](int kc, int j, float s) {
+                          const int64_t at = (int64_t)kc * V + v0 + j;
+                          next.h[at] = fmaf(keep, w.h[at], s);
+                        });
   }
 }
 
 // grid: as simt_states_kernel.  The states' gradients, backward.
 template <typename E>
 __global__ void __launch_bounds__(THREADS) simt_grads_kernel(DeltaBwdParams p) {
-  __shared__ __align__(16) float tiles[2 * TILE];
+  __shared__ __align__(16) float tiles[TILES];
+  __shared__ Factors f;
   const int v0 = blockIdx.x * COLS, nv = min(COLS, p.V - v0), head = blockIdx.y;
   const int hk = head / (p.H / p.Hg), K = p.K, V = p.V;
   int64_t first;
@@ -197,34 +270,36 @@ __global__ void __launch_bounds__(THREADS) simt_grads_kernel(DeltaBwdParams p) {
     const Block w(p, first + c, head);
     const Rows<E> q(p.q, ch.token, p.Hg, hk, K, ch.len), k(p.k, ch.token, p.Hg, hk, K, ch.len);
     const Rows<E> go(p.dout, ch.token, p.H, head, V, ch.len);
-    const float GL = w.G[ch.len - 1], keep = expf(GL);
-    product(Q, nv, Q, tiles, [&](int j, int i) { return w.P[i * Q + j]; },
-            [&](int i, int j) { return go(i, v0 + j); },
-            [&](int i, int j, float s) { w.dr[(int64_t)i * V + v0 + j] = s; });
-    product(Q, nv, K, tiles, k, [&](int i, int j) { return w.D[(int64_t)i * V + v0 + j]; },
-            [&](int i, int j, float s) {
-              // (past the chunk's end k is zero and the gate may not be a sum)
-              if (i < ch.len) w.dr[(int64_t)i * V + v0 + j] += expf(GL - w.G[i]) * s;
-            });
+    f.load(w, ch.len);
+    const float keep = f.eG[ch.len - 1];
+    product<ROWS, ROWS>(Q, nv, Q, tiles, [&](int j, int i) { return w.P[i * Q + j]; },
+                        [&](int i, int j) { return go(i, v0 + j); },
+                        [&](int i, int j, float s) { w.dr[(int64_t)i * V + v0 + j] = s; });
+    product<STEPS, ROWS>(Q, nv, K, tiles, k, [&](int i, int j) { return w.D[(int64_t)i * V + v0 + j]; },
+                         [&](int i, int j, float s) { w.dr[(int64_t)i * V + v0 + j] += f.eR[i] * s; });
     auto rows = [&](int i, int j) { return w.dr[(int64_t)i * V + v0 + j]; };
-    product(Q, nv, Q, tiles, [&](int i, int m) { return w.T[m * Q + i]; }, rows,
-            [&](int i, int j, float s) { w.dr[(int64_t)i * V + v0 + j] = s; });
+    product<ROWS, ROWS>(Q, nv, Q, tiles, [&](int i, int m) { return w.T[m * Q + i]; }, rows,
+                        [&](int i, int j, float s) { w.dr[(int64_t)i * V + v0 + j] = s; });
     if (c == 0 && p.dh0 == nullptr) break;
     float *prev = c > 0 ? Block(p, first + c - 1, head).D : nullptr;
-    product(K, nv, 2 * ch.len, tiles,
-            [&](int kc, int i) {
-              if (i < ch.len) return q(i, kc) * p.scale * expf(w.G[i]);
-              i -= ch.len;
-              return -k(i, kc) * w.beta[i] * expf(w.G[i]);
-            },
-            [&](int i, int j) { return i < ch.len ? go(i, v0 + j) : rows(i - ch.len, j); },
-            [&](int kc, int j, float s) {
-              const float d = fmaf(keep, w.D[(int64_t)kc * V + v0 + j], s);
-              if (prev)
-                prev[(int64_t)kc * V + v0 + j] = d;
-              else
-                p.dh0[outer(kc, v0 + j)] = d;
-            });
+    // steps 0 .. 63: q and do, behind them k and dr
+    product<ROWS, ROWS>(K, nv, 2 * Q, tiles,
+                        [&](int kc, int i) {
+                          const Rows<E> &from = i < Q ? q : k;
+                          const float x = from(i % Q, kc) * f.eG[i % Q];
+                          return i < Q ? p.scale * x : -f.beta[i % Q] * x;
+                        },
+                        [&](int i, int j) {
+                          const float x = go(i % Q, v0 + j), y = rows(i % Q, j);
+                          return i < Q ? x : y;
+                        },
+                        [&](int kc, int j, float s) {
+                          const float d = fmaf(keep, w.D[(int64_t)kc * V + v0 + j], s);
+                          if (prev)
+                            prev[(int64_t)kc * V + v0 + j] = d;
+                          else
+                            p.dh0[outer(kc, v0 + j)] = d;
+                        });
   }
 }
 
@@ -233,16 +308,16 @@ struct Inputs {
   float *tiles, *dq, *dk, *x, *P, *A, *M, *B, *sums;
   __device__ explicit Inputs(float *f) {
     tiles = f;
-    dq = tiles + 2 * TILE;
+    dq = tiles + TILES;
     dk = dq + Q * KMAX;
     x = dk + Q * KMAX;
     P = x + Q * KMAX;
-    A = P + Q * Q;
-    M = A + Q * Q;
-    B = M + Q * Q;
-    sums = B + Q * Q;   // 8 x 64
+    A = P + Q * SIDE;
+    M = A + Q * SIDE;
+    B = M + Q * SIDE;
+    sums = B + Q * SIDE;   // 8 x 64
   }
-  static constexpr int FLOATS = 2 * TILE + 3 * Q * KMAX + 4 * Q * Q + 8 * Q;
+  static constexpr int FLOATS = TILES + 3 * Q * KMAX + 4 * Q * SIDE + 8 * Q;
 };
 
 // sum_c x[i][c] y(i, c) of every row, four threads a row, to out[i].
@@ -262,100 +337,120 @@ __device__ __forceinline__ void row_dots(const float *x, int K, Y y, float *out)
 template <typename E>
 __global__ void __launch_bounds__(THREADS) simt_inputs_kernel(DeltaBwdParams p) {
   extern __shared__ __align__(16) float shared[];
+  __shared__ Factors f;
   const Inputs s(shared);
   const DeltaChunk ch = delta_chunk(p, blockIdx.x);
   const int hk = blockIdx.y, rep = p.H / p.Hg, tid = threadIdx.x, K = p.K, V = p.V;
   if (ch.len <= 0) return;
   if (!bounds_ok(ch.n < p.N && ch.token + ch.len <= (int64_t)p.B * p.T, p.err)) return;
   const Rows<E> q(p.q, ch.token, p.Hg, hk, K, ch.len), k(p.k, ch.token, p.Hg, hk, K, ch.len);
-  float *qd = s.sums, *kh = qd + Q, *kD = kh + Q, *rv = kD + Q, *dG = rv + Q, *part = dG + Q;
+  float *qd = s.sums, *kh = qd + Q, *kD = kh + Q, *G = kD + Q, *dG = G + Q, *part = dG + Q;
   for (int x = tid; x < Q * K; x += THREADS) s.dq[x] = s.dk[x] = 0.f;
   __syncthreads();
   for (int head = hk * rep; head < (hk + 1) * rep; ++head) {
     const Block w(p, blockIdx.x, head);
     const Rows<E> go(p.dout, ch.token, p.H, head, V, ch.len), v(p.v, ch.token, p.H, head, V, ch.len);
-    const float GL = w.G[ch.len - 1], keep = expf(GL);
+    f.load(w, ch.len);
+    const float keep = f.eG[ch.len - 1];
+    if (tid < Q) G[tid] = w.G[tid];
+    __syncthreads();
     auto kt = [&](int c, int j) { return k(j, c); };
-    auto nt = [&](int c, int j) { return w.n[(int64_t)j * V + c]; };
+    auto n = [&](int i, int c) { return w.n[(int64_t)i * V + c]; };
+    auto nt = [&](int c, int j) { return n(j, c); };
     auto dr = [&](int i, int c) { return w.dr[(int64_t)i * V + c]; };
     auto ht = [&](int c, int kc) { return w.h[(int64_t)kc * V + c]; };
-    product(Q, Q, K, s.tiles, q, kt, [&](int i, int j, float x) { s.P[i * Q + j] = x; });
-    product(Q, Q, V, s.tiles, go, nt, [&](int i, int j, float x) {
-      const float L = i >= j && i < ch.len ? p.scale * expf(w.G[i] - w.G[j]) : 0.f;
-      s.M[i * Q + j] = L * x * s.P[i * Q + j];
-      s.P[i * Q + j] = L * x;
+    auto Dt = [&](int c, int kc) { return w.D[(int64_t)kc * V + c]; };
+    product<STEPS, STEPS>(Q, Q, K, s.tiles, q, kt, [&](int i, int j, float x) { s.P[i * SIDE + j] = x; });
+    product<STEPS, STEPS>(Q, Q, V, s.tiles, go, nt, [&](int i, int j, float x) {
+      const float L = i >= j && i < ch.len ? p.scale * expf(G[i] - G[j]) : 0.f;
+      s.M[i * SIDE + j] = L * x * s.P[i * SIDE + j];
+      s.P[i * SIDE + j] = L * x;
     });
-    product(Q, Q, K, s.tiles, k, kt, [&](int i, int j, float x) { s.A[i * Q + j] = x; });
-    product(Q, Q, V, s.tiles, dr, nt, [&](int i, int j, float x) {
-      const float L = i > j && i < ch.len ? expf(w.G[i] - w.G[j]) : 0.f;
-      s.B[i * Q + j] = -L * x * s.A[i * Q + j];
-      s.A[i * Q + j] = -L * x * w.beta[i];
+    product<STEPS, STEPS>(Q, Q, K, s.tiles, k, kt, [&](int i, int j, float x) { s.A[i * SIDE + j] = x; });
+    product<STEPS, STEPS>(Q, Q, V, s.tiles, dr, nt, [&](int i, int j, float x) {
+      const float L = i > j && i < ch.len ? expf(G[i] - G[j]) : 0.f;
+      s.B[i * SIDE + j] = -L * x * s.A[i * SIDE + j];
+      s.A[i * SIDE + j] = -L * x * f.beta[i];
     });
-    product(Q, K, V, s.tiles, go, ht, [&](int i, int c, float x) {
-      x *= p.scale * expf(w.G[i]);
+    product<STEPS, STEPS>(Q, K, V, s.tiles, go, ht, [&](int i, int c, float x) {
+      x *= p.scale * f.eG[i];
       s.x[i * K + c] = x;
       s.dq[i * K + c] += x;
     });
     row_dots(s.x, K, q, qd);
-    product(Q, K, V, s.tiles, dr, ht, [&](int i, int c, float x) {
-      x *= -expf(w.G[i]);
+    product<STEPS, STEPS>(Q, K, V, s.tiles, dr, ht, [&](int i, int c, float x) {
+      x *= -f.eG[i];
       s.x[i * K + c] = x;
-      s.dk[i * K + c] += w.beta[i] * x;
+      s.dk[i * K + c] += f.beta[i] * x;
     });
     row_dots(s.x, K, k, kh);
-    product(Q, K, V, s.tiles, [&](int i, int c) { return w.n[(int64_t)i * V + c]; },
-            [&](int c, int kc) { return w.D[(int64_t)kc * V + c]; }, [&](int i, int c, float x) {
-              x = i < ch.len ? x * expf(GL - w.G[i]) : 0.f;
-              s.x[i * K + c] = x;
-              s.dk[i * K + c] += x;
-            });
+    product<STEPS, STEPS>(Q, K, V, s.tiles, n, Dt, [&](int i, int c, float x) {
+      x *= f.eR[i];
+      s.x[i * K + c] = x;
+      s.dk[i * K + c] += x;
+    });
     row_dots(s.x, K, k, kD);
-    product(Q, K, Q, s.tiles, [&](int i, int j) { return s.P[i * Q + j]; }, k,
-            [&](int i, int c, float x) { s.dq[i * K + c] += x; });
-    product(Q, K, Q, s.tiles, [&](int j, int i) { return s.P[i * Q + j]; }, q,
-            [&](int i, int c, float x) { s.dk[i * K + c] += x; });
-    product(Q, K, Q, s.tiles, [&](int i, int j) { return s.A[i * Q + j] + s.A[j * Q + i]; }, k,
-            [&](int i, int c, float x) { s.dk[i * K + c] += x; });
-    // dr.v of every row, and dv
+    product<STEPS, ROWS>(Q, K, Q, s.tiles, [&](int i, int j) { return s.P[i * SIDE + j]; }, k,
+                         [&](int i, int c, float x) { s.dq[i * K + c] += x; });
+    product<ROWS, ROWS>(Q, K, Q, s.tiles, [&](int j, int i) { return s.P[i * SIDE + j]; }, q,
+                        [&](int i, int c, float x) { s.dk[i * K + c] += x; });
+    product<STEPS, ROWS>(Q, K, Q, s.tiles,
+                         [&](int i, int j) { return s.A[i * SIDE + j] + s.A[j * SIDE + i]; }, k,
+                         [&](int i, int c, float x) { s.dk[i * K + c] += x; });
+    // dr.v of every row, and dv; M's and B's sums, four threads a row
     const int row = tid / 4;
-    float sum = 0.f;
+    float sum = 0.f, m = 0.f, b = 0.f;
     for (int c = tid % 4; c < V; c += 4) {
       const float d = w.dr[(int64_t)row * V + c];
       sum = fmaf(d, v(row, c), sum);
       if (row < ch.len)
         static_cast<E *>(p.dv)[((ch.token + row) * p.H + head) * V + c] =
-            from_f32<E>(w.beta[row] * d);
+            from_f32<E>(f.beta[row] * d);
     }
-    sum += __shfl_xor_sync(~0u, sum, 1);
-    sum += __shfl_xor_sync(~0u, sum, 2);
-    if (tid % 4 == 0) rv[row] = sum;
+    for (int j = tid % 4; j < Q; j += 4) {
+      m += s.M[row * SIDE + j] + f.beta[row] * s.B[row * SIDE + j];
+      m -= s.M[j * SIDE + row] + f.beta[j] * s.B[j * SIDE + row];
+      b += s.B[row * SIDE + j];
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      sum += __shfl_xor_sync(~0u, sum, o);
+      m += __shfl_xor_sync(~0u, m, o);
+      b += __shfl_xor_sync(~0u, b, o);
+    }
+    if (tid % 4 == 0) {
+      dG[row] = m + qd[row] + f.beta[row] * kh[row] - kD[row];
+      if (row < ch.len) p.dbeta[(ch.token + row) * p.H + head] = sum + kh[row] + b;
+    }
     // <h, D>
     sum = 0.f;
     for (int x = tid; x < K * V; x += THREADS) sum = fmaf(w.h[x], w.D[x], sum);
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
     if (tid % 32 == 0) part[tid / 32] = sum;
     __syncthreads();
-    if (tid < Q) {
-      float m = 0.f, b = 0.f;
-      for (int j = 0; j < Q; ++j) {
-        m += s.M[tid * Q + j] + w.beta[tid] * s.B[tid * Q + j];
-        m -= s.M[j * Q + tid] + w.beta[j] * s.B[j * Q + tid];
-        b += s.B[tid * Q + j];
-      }
-      dG[tid] = m + qd[tid] + w.beta[tid] * kh[tid] - kD[tid];
-      if (tid < ch.len) p.dbeta[(ch.token + tid) * p.H + head] = rv[tid] + kh[tid] + b;
-    }
-    __syncthreads();
-    if (tid == 0) {
-      float hD = 0.f, all = 0.f;
+    if (tid < 32) {  // dG's sums from the end, two tokens a lane
+      float hD = 0.f, all = kD[tid] + kD[tid + 32];  // (kD is zero past the end)
       for (int i = 0; i < THREADS / 32; ++i) hD += part[i];
-      for (int i = 0; i < ch.len; ++i) all += kD[i];
-      dG[ch.len - 1] += fmaf(keep, hD, all);
-      float run = 0.f;
-      for (int i = ch.len - 1; i >= 0; --i) {
-        run = p.g_is_cumsum ? dG[i] : run + dG[i];
-        p.dg[(ch.token + i) * p.H + head] = run;
+      for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(~0u, all, o);
+      float d[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int i = tid + 32 * e;
+        d[e] = i < ch.len ? dG[i] + (i == ch.len - 1 ? fmaf(keep, hD, all) : 0.f) : 0.f;
       }
+      if (!p.g_is_cumsum) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const float x = __shfl_down_sync(~0u, d[e], o);
+            if (tid + o < 32) d[e] += x;
+          }
+        d[0] += __shfl_sync(~0u, d[1], 0);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (tid + 32 * e < ch.len) p.dg[(ch.token + tid + 32 * e) * p.H + head] = d[e];
     }
     __syncthreads();
   }
@@ -370,10 +465,14 @@ template <typename E>
 cudaError_t launch(const DeltaBwdParams &p, cudaStream_t stream) {
   const dim3 walks((p.V + COLS - 1) / COLS, p.H, p.N);
   const int smem = Inputs::FLOATS * (int)sizeof(float);
-  const cudaError_t e = cudaFuncSetAttribute(simt_inputs_kernel<E>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  constexpr int PREPARE = (TILES + Q * Q) * (int)sizeof(float);
+  cudaError_t e = cudaFuncSetAttribute(simt_inputs_kernel<E>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(simt_prepare_kernel<E>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             PREPARE);
   if (e != cudaSuccess) return e;
-  simt_prepare_kernel<E><<<dim3((unsigned)p.chunks, p.H), THREADS, 0, stream>>>(p);
+  simt_prepare_kernel<E><<<dim3((unsigned)p.chunks, p.H), THREADS, PREPARE, stream>>>(p);
   simt_states_kernel<E><<<walks, THREADS, 0, stream>>>(p);
   simt_grads_kernel<E><<<walks, THREADS, 0, stream>>>(p);
   simt_inputs_kernel<E><<<dim3((unsigned)p.chunks, p.Hg), THREADS, smem, stream>>>(p);
