@@ -46,6 +46,9 @@ constexpr int KD_WARPS = 8, KD_ROWS = 4;
 // of them work than there are stages: 256 channels and four tokens have three.)
 constexpr int KD_STAGES = 6, KD_PREP = 4, KD_PER_SM = 2;
 constexpr uint32_t KD_TILE = 16384;
+// Shared memory of a ring, at most (the kernels' limit is this, whatever a call takes: calls
+// of several threads set the same).
+constexpr int KD_RING = 112 << 10;
 constexpr int KD_THREADS = 32 * (KD_WARPS + KD_PREP + 2);
 
 // A head's rows v .. end - 1 of one request.
@@ -491,13 +494,13 @@ cudaError_t launch_kda(KdParams &p, cudaStream_t stream) {
   p.vblocks = (p.V + rows - 1) / rows;
   p.rows = (p.V + p.vblocks - 1) / p.vblocks;
   const int coef = KdCoef(p.K, p.rows, p.T).bytes();
-  p.stages = std::min(KD_STAGES, (112 << 10) / ((int)KD_TILE + coef));
+  p.stages = std::min(KD_STAGES, KD_RING / ((int)KD_TILE + coef));
   const int smem = p.stages * ((int)KD_TILE + coef);
   const int blocks = KD_PER_SM * sm_count();
   const int64_t items = bh * p.vblocks;
   if (items >= blocks && items <= 0x7fff0000) {
     const cudaError_t e = cudaFuncSetAttribute(kda_decode_ring_kernel<S, LPR, PP, TM>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, KD_RING);
     if (e != cudaSuccess) return e;
     kda_decode_ring_kernel<S, LPR, PP, TM><<<blocks, KD_THREADS, smem, stream>>>(p, (int)items);
   } else {
