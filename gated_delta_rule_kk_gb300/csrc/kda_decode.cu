@@ -144,8 +144,7 @@ struct KdToken {
     float decay[MOST];  // side by side: each is a long chain
 #pragma unroll
     for (int i = 0; i < MOST; ++i) {
-      const float x = a[i] + bias[i], y = log1pf(expf(fminf(x, 20.f)));
-      decay[i] = expf(rate * (x > 20.f ? x : y));
+      decay[i] = expf(rate * softplus(a[i] + bias[i]));
     }
 #pragma unroll
     for (int i = 0; i < MOST; ++i) {

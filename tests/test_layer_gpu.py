@@ -323,6 +323,25 @@ def test_kda_tokens_of_a_bad_slot(B):
             assert torch.equal(d["state"][s], before[s])
 
 
+@pytest.mark.parametrize("B", [2, 300])
+def test_kda_tokens_of_gates_that_are_no_numbers(B):
+    """A NaN reaches its own head's channel and no other; infinities mean keep and forget."""
+    i = kda_inputs(7, B, 2, 2, 2, 64, 64, F32, F32)
+    bad = {k: v.clone() if isinstance(v, torch.Tensor) else v for k, v in i.items()}
+    i["a"][0, 0, 1, 3], i["a"][1, 1, 0, 5] = -float("inf"), float("inf")
+    bad["a"][0, 0, 1, 3], bad["a"][0, 1, 0, 5] = float("nan"), -float("inf")
+    for x in (i, bad):
+        d = cuda(x)
+        o = gdn.kda_decode(d["q"], d["k"], d["v"], d["a"], d["b"], d["A_log"], d["dt_bias"],
+                           d["state"], slot_indices=d["slots"])
+        if x is i:
+            assert_each_close(o, L.kda_decode(**i)[0], "o", 1e-5)
+    assert o[0, :, 1].isnan().all() and d["state"][d["slots"][0], 1, :, 3].isnan().all()
+    o[0, :, 1] = 0
+    assert o.isfinite().all()
+    ok()
+
+
 def test_kda_tokens_replay():
     i = kda_inputs(6, 40, 1, 4, 8, 128, 128, BF16, BF16)
     d = cuda(i)
