@@ -90,6 +90,10 @@ __device__ __forceinline__ int delta_chunks(const DeltaBwdParams &p, int n, int6
   return p.first[n + 1] - p.first[n];
 }
 
+// A token's log-gate for the running sums: what lies below e^-104 is zero in float32, and
+// sums that pass through lesser values (or through -infinity) would lose the gates behind.
+__device__ __forceinline__ float delta_gate(float g) { return g < -104.f ? -104.f : g; }
+
 // Whether the offsets were good (the table kernel marks bad ones).
 __device__ __forceinline__ bool delta_good(const DeltaBwdParams &p) {
   return p.cu == nullptr || p.first[p.N] >= 0;

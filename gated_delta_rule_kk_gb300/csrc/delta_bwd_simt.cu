@@ -144,11 +144,17 @@ __global__ void __launch_bounds__(THREADS) simt_prepare_kernel(DeltaBwdParams p)
   if (tid < Q) {
     const int64_t at = (ch.token + min(tid, ch.len - 1)) * p.H + head;
     G[tid] = tid < ch.len || p.g_is_cumsum ? p.g[at] : 0.f;
+    if (!p.g_is_cumsum) G[tid] = delta_gate(G[tid]);
     beta[tid] = tid < ch.len ? p.beta[at] : 0.f;
   }
   __syncthreads();
-  if (tid == 0 && !p.g_is_cumsum)
-    for (int i = 1; i < Q; ++i) G[i] += G[i - 1];
+  if (tid == 0 && !p.g_is_cumsum) {  // (in 64 bits: differences of the sums are taken)
+    double sum = 0.;
+    for (int i = 0; i < Q; ++i) {
+      sum += G[i];
+      G[i] = (float)sum;
+    }
+  }
   __syncthreads();
   if (tid < Q) {
     w.G[tid] = G[tid];

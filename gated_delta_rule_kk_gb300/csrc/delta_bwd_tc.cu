@@ -47,17 +47,21 @@ __global__ void __launch_bounds__(PREP, 3) tc_prepare_kernel(DeltaBwdParams p) {
       const int i = lane + 32 * e;
       const int64_t where = (ch.token + min(i, ch.len - 1)) * p.H + head;
       g[e] = i < ch.len || p.g_is_cumsum ? p.g[where] : 0.f;
+      if (!p.g_is_cumsum) g[e] = delta_gate(g[e]);
       beta[i] = i < ch.len ? p.beta[where] : 0.f;
     }
-    if (!p.g_is_cumsum) {
+    if (!p.g_is_cumsum) {  // (in 64 bits: differences of the sums are taken)
+      double sum[2] = {g[0], g[1]};
 #pragma unroll
       for (int e = 0; e < 2; ++e)
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const float v = __shfl_up_sync(~0u, g[e], o);
-          if (lane >= o) g[e] += v;
+          const double v = __shfl_up_sync(~0u, sum[e], o);
+          if (lane >= o) sum[e] += v;
         }
-      g[1] += __shfl_sync(~0u, g[0], 31);
+      sum[1] += __shfl_sync(~0u, sum[0], 31);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) g[e] = (float)sum[e];
     }
     G[lane] = g[0];
     G[lane + 32] = g[1];

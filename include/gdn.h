@@ -301,6 +301,8 @@ gdn_status_t gdn_chunk_host_workspace_size(const gdn_chunk_args *args, size_t *b
  *                                          zeros / zeros / not returned
  *   cu_seqlens    [N + 1]         int32    as gdn_chunk_fwd; with bad offsets nothing is
  *                                          written
+ * A per-token gate may be anything up to -infinity (the state is forgotten: e^g is zero below
+ * -104); a chunk-local sum has to be finite.
  * With T == 0 the per-token arrays may be NULL (dh0 = dht, or zeros).  Outputs must not
  * overlap inputs.  A sum over heads, tokens or channels always runs in the same order, so
  * results do not change from run to run.

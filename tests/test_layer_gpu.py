@@ -107,6 +107,16 @@ def test_delta_gradient_of_resets_and_of_beta_zero(dtype):
     assert got[3][:, ::5].abs().max() <= 2.0 ** -17 * got[3].abs().max()
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("gate", [-float("inf"), -3.4e38, -1e4, -150.0])
+def test_delta_gradient_of_gates_that_forget_all(dtype, gate):
+    i = delta_inputs(19, 1, 150, 2, 2, 64, 64, dtype, [90, 60])
+    i["g"][:, [0, 40, 41, 100]] = gate
+    got = run_delta(cuda(i))
+    ok()
+    check_delta(got, i, pieces=dtype is BF16, norm=False)
+
+
 @pytest.mark.parametrize("dtype,K", [(BF16, 16), (F32, 12)])
 def test_delta_gradient_of_more_sequences_than_threads(dtype, K):
     """1100 sequences of nothing to a few tokens, some of several chunks: the order in which
