@@ -144,7 +144,7 @@ __device__ __forceinline__ void store_row(bf16 *to, const float (*v)[4], int e, 
   }
 }
 
-// dr.v of a token whose beta is zero (dbeta is (dr.n) / beta of any other), by one warp.
+// dr.v of a token whose beta is next to zero (dbeta is (dr.n) / beta of any other), by one warp.
 template <int KP>
 __device__ __forceinline__ float dot_value(const DeltaBwdParams &p, const Block<KP> &w, int64_t token,
                                            int head, int row) {
@@ -380,8 +380,9 @@ __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdPar
           const float kd = all_of(kD), khi = all_of(kh);
           d[e] = all_of(rM) - all_of(cM) + all_of(qd) + beta[i] * khi - kd;
           all += kd;
-          // dbeta = dr.n / beta, as n is beta times what it does not depend on it by
-          const bool none = fabsf(beta[i]) < 1e-30f;
+          // dbeta = dr.n / beta, as n is beta times what it does not depend on it by (of a beta
+          // next to nothing the products of dr's and n's pieces could fall below float32)
+          const bool none = fabsf(beta[i]) < 1e-12f;
           db[e] = none ? khi + all_of(rB) : rn[i] / beta[i];
           for (unsigned z = __ballot_sync(~0u, none && i < ch.len); z; z &= z - 1) {
             const int l = __ffs(z) - 1;

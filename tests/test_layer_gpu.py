@@ -129,6 +129,18 @@ def test_delta_gradient_of_more_sequences_than_threads(dtype, K):
     check_delta(got, i, pieces=dtype is BF16, norm=False)
 
 
+def test_delta_gradient_of_beta_next_to_zero():
+    """Products of a tiny beta and a tiny gradient are not lost."""
+    i = delta_inputs(20, 1, 130, 2, 2, 64, 64, BF16)
+    i["beta"][:, ::3] *= 1e-25
+    i["do"], i["dht"] = i["do"] * 2.0 ** -50, i["dht"] * 2.0 ** -50
+    dbeta = run_delta(cuda(i))[4]
+    ok()
+    ref = L.gdn_grad(i["do"], i["q"], i["k"], i["v"], i["g"], i["beta"], i["scale"], i["h0"],
+                     i["dht"], i["cu"])[4]
+    assert_each_close(dbeta, ref, "dbeta", PIECES)
+
+
 def test_delta_gradient_of_growing_states():
     """Gates above zero: the running sums grow to +20 within a chunk."""
     i = delta_inputs(10, 1, 130, 2, 2, 64, 64, BF16)
