@@ -140,6 +140,7 @@ gdn_status_t check_norm(const Args &a) {
              a.D, a.groups);
   CHECK_THAT(a.D / a.groups <= 8192, GDN_ERR_UNSUPPORTED, "groups of %d channels exceed 8192",
              a.D / a.groups);
+  CHECK_THAT(a.D <= (1 << 28), GDN_ERR_UNSUPPORTED, "D (%d) must be at most %d", a.D, 1 << 28);
   CHECK_THAT((int64_t)a.B * a.T <= NORM_MAX_TOKENS, GDN_ERR_UNSUPPORTED,
              "B * T (%lld) must be at most %lld", (long long)a.B * a.T, (long long)NORM_MAX_TOKENS);
   CHECK_FLAG(a.shared_weight, "shared_weight");

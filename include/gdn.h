@@ -641,7 +641,8 @@ gdn_status_t ssm_decode(const ssm_decode_args *args, gdn_stream_t stream);
  *   weight, bias            weight_dtype (GDN_F32, or dtype): [D], or [D / groups] for
  *                                    all groups with shared_weight = 1; NULL = ones / zeros
  *   activation              gdn_activation_t
- * Limits: D % groups == 0, D / groups at most 8192, B T at most 2^31 - 256.  Arithmetic in
+ * Limits: D % groups == 0, D / groups at most 8192, D at most 2^28, B T at most
+ * 2^31 - 2^20 - 256.  Arithmetic in
  * float32, the mean taken off before squares are summed; one rounding at the end.
  * SiLU and the sigmoid come from the hardware's fast exponential and reciprocal, as in
  * short_conv_fwd.  An Inf or NaN in x stays within its token's group.

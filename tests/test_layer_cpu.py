@@ -208,6 +208,7 @@ NORM_CHANGES = [
     (dict(dtype=2), Status.INVALID_ARG), (dict(dtype=0), Status.INVALID_ARG),
     (dict(groups=0), Status.INVALID_ARG), (dict(groups=5), Status.INVALID_ARG),
     (dict(D=8193, groups=1, x_stride=8193), Status.UNSUPPORTED),
+    (dict(D=1 << 29, groups=1 << 20, x_stride=1 << 29), Status.UNSUPPORTED),
     (dict(B=1 << 15, T=1 << 16), Status.UNSUPPORTED), (dict(x_stride=63), Status.INVALID_ARG),
     (dict(center=2), Status.INVALID_ARG), (dict(shared_weight=3), Status.INVALID_ARG),
     (dict(activation=3), Status.INVALID_ARG), (dict(activation=-1), Status.INVALID_ARG),
