@@ -12,12 +12,16 @@ norm the pieces' errors are independent: 2^-19 of a value each, some 20 of them 
 quadrature, 1e-5.
 """
 import ctypes
+import os
+import subprocess
+import sys
+import threading
 
 import pytest
 import torch
 
 import gated_delta_rule_kk_gb300 as gdn
-from gated_delta_rule_kk_gb300 import GdnError, Status, _lib
+from gated_delta_rule_kk_gb300 import GdnError, Status, _lib, build_lib
 from gated_delta_rule_kk_gb300._lib import GdnChunkBwdArgs
 from oracle import layer as L
 
@@ -606,3 +610,136 @@ def test_a_layer_trains_and_decodes():
     # up to 30, so 30 times the float32 bound of the recurrence's 1e-5 typical error)
     for name, got, want in zip(p, (dx, dcw, dnw, dz, dg, db), ref):
         assert_each_close(got, want.numpy(), name, 3e-4)
+
+
+# ---------------------------------------------------------------- calls at once, the checked build
+
+def everything(seed, K, heads):
+    """One call of each operator as a function of the stream; the states are new every time."""
+    i = cuda(delta_inputs(seed, 1, 300, heads, 1, K, K, BF16, [170, 130]))
+    t = cuda(kda_inputs(seed, 40, 2, heads, 2 * heads, K, 64, BF16, BF16))
+    n = cuda(norm_inputs(seed, 1, 400, heads, K, BF16))
+    start = t["state"].clone()
+
+    def run(stream=None):
+        state = t["state"] if stream is None else torch.empty_like(start)
+        with torch.cuda.stream(stream or torch.cuda.current_stream()):
+            state.copy_(start)
+        o = gdn.kda_decode(t["q"], t["k"], t["v"], t["a"], t["b"], t["A_log"], t["dt_bias"], state,
+                           slot_indices=t["slots"], stream=stream)
+        y = gdn.group_norm_fwd(n["x"], heads, n["weight"], n["bias"], n["z"], activation="silu",
+                               stream=stream)
+        g = gdn.group_norm_bwd(n["dy"], n["x"], heads, n["weight"], n["bias"], n["z"],
+                               activation="silu", stream=stream)
+        return [o, state, y, *g, *run_delta(i, stream=stream)]
+
+    return run
+
+
+def test_calls_from_several_threads():
+    """Each on a stream of its own, of other sizes, all at once."""
+    calls = [everything(30 + k, (128, 64, 40)[k % 3], 2 + k) for k in range(6)]
+    begin, results = threading.Barrier(6), [None] * 6
+    torch.cuda.synchronize()
+
+    def work(k):
+        stream = torch.cuda.Stream()
+        begin.wait()
+        for _ in range(5):
+            out = calls[k](stream)
+        stream.synchronize()
+        results[k] = out
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(6)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    ok()
+    for out, call in zip(results, calls):
+        for a, b in zip(out, call()):
+            assert torch.equal(a, b)
+
+
+def test_graphs_that_share_a_workspace():
+    ins = [cuda(delta_inputs(40 + k, 1, 260, 4, 2, 128, 64, BF16, [100, 160])) for k in range(2)]
+    n = cuda(norm_inputs(41, 1, 500, 8, 64, BF16))
+    want = [run_delta(i) for i in ins]
+    norm = gdn.group_norm_bwd(n["dy"], n["x"], 8, n["weight"], n["bias"])
+    room = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    graphs, held = [], []
+    for i in ins:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            held.append((run_delta(i, workspace=room),
+                         gdn.group_norm_bwd(n["dy"], n["x"], 8, n["weight"], n["bias"], workspace=room)))
+    for k in (0, 1, 1, 0):
+        room.fill_(255)
+        for x in (*held[k][0], *held[k][1][:3]):
+            x.fill_(7)
+        graphs[k].replay()
+        for a, b in zip((*held[k][0], *held[k][1][:3]), (*want[k], *norm[:3])):
+            assert torch.equal(a, b)
+    ok()
+
+
+CHECKED = r"""
+import sys
+sys.path[:0] = [sys.argv[1], sys.argv[2]]
+import torch
+from gated_delta_rule_kk_gb300 import _lib
+import gated_delta_rule_kk_gb300 as gdn
+from _layer import delta_inputs, kda_inputs, norm_inputs
+from _mixer import cuda
+
+checked, release = _lib.load(), _lib.load(sys.argv[3])
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def delta(T, H, Hg, K, V, dtype, lens=None):
+    d = cuda(delta_inputs(1, 1, T, H, Hg, K, V, dtype, lens))
+    return gdn.gdn_chunk_bwd(d["do"], d["q"], d["k"], d["v"], d["g"], d["beta"], scale=d["scale"],
+                             initial_state=d["h0"], dfinal_state=d["dht"], cu_seqlens=d["cu"])
+
+
+def tokens(B, T, K, V, state):
+    d = cuda(kda_inputs(2, B, T, 4, 8, K, V, BF16, state))
+    o = gdn.kda_decode(d["q"], d["k"], d["v"], d["a"], d["b"], d["A_log"], d["dt_bias"], d["state"],
+                       slot_indices=d["slots"])
+    return o, d["state"]
+
+
+def norm(T, groups, width, dtype):
+    d = cuda(norm_inputs(3, 1, T, groups, width, dtype))
+    how = dict(activation="silu")
+    y = gdn.group_norm_fwd(d["x"], groups, d["weight"], d["bias"], d["z"], **how)
+    return y, *gdn.group_norm_bwd(d["dy"], d["x"], groups, d["weight"], d["bias"], d["z"], **how)
+
+
+cases = []
+for dt in (BF16, F32):
+    cases += [lambda dt=dt: delta(1, 2, 2, 128, 128, dt), lambda dt=dt: delta(200, 4, 2, 64, 40, dt),
+              lambda dt=dt: delta(300, 2, 1, 120, 128, dt, [129, 0, 1, 170]),
+              lambda dt=dt: delta(70, 2, 1, 20, 136, dt), lambda dt=dt: tokens(1, 1, 128, 33, dt),
+              lambda dt=dt: tokens(100, 3, 256, 128, dt), lambda dt=dt: norm(37, 5, 24, dt),
+              lambda dt=dt: norm(3000, 3, 8191, dt), lambda dt=dt: norm(1, 300, 1, dt)]
+for i, case in enumerate(cases):
+    results = []
+    for lib in (checked, release):
+        _lib._lib = lib
+        results.append(case())
+        status = gdn.gdn_check_device_error()
+        assert status == 0, (i, status)
+    for a, b in zip(*results):
+        assert torch.equal(a, b), i
+"""
+
+
+def test_checked_build():
+    """The bounds-checked build records nothing on valid calls and computes the same."""
+    tests = os.path.dirname(os.path.abspath(__file__))
+    build_lib.build(checked=True)
+    r = subprocess.run([sys.executable, "-c", CHECKED, os.path.dirname(tests), tests,
+                        build_lib.build()], env=dict(os.environ, GDN_CHECKED="1"),
+                       capture_output=True, text=True, timeout=900)
+    assert r.returncode == 0, r.stdout + r.stderr
