@@ -2,20 +2,23 @@
 // call that the tensor cores do not take (float32, odd head sizes, V > 128).  delta_bwd.h has
 // the formulas.
 //
-// All products go through one tiled product of a block (64 x 64 outputs, 16 of them a thread,
-// operands read through functions, so that gates, masks and transposes need no copies).  What
-// bounds a call of few heads is the latency of the products that wait for one another along a
-// walk: the next 32 steps' operands are on their way in registers while 32 are multiplied, and
-// every load is of a place that exists, with the value chosen behind it, so that no load waits
-// for another.  (Three sequences of 261 to 376 tokens, 12 heads of 48 x 40, float32: 353 us;
-// with 16 steps a tile, two barriers each, and loads inside branches 502 us.)
+// All products go through one tiled product of a block: 64 x 64 outputs, 16 of them a thread,
+// of which half of the threads sum every other 16 steps; operands are read through functions,
+// so that gates, masks and transposes need no copies.  What bounds a call of few heads is the
+// latency of the products that wait for one another along a walk, half of it instructions: the
+// next 32 steps' operands are on their way in registers while 32 are multiplied, and every
+// load is of a place that exists, with the value chosen behind it, so that no load waits for
+// another.  (Three sequences of 261 to 376 tokens, 12 heads of 48 x 40, float32: 336 us; a
+// thread summing all steps, 256 of them, 353; with 16 steps a tile, two barriers each, and loads
+// inside branches 502.  A walk's rows and state kept in shared memory instead of the workspace
+// changed nothing.)
 #include "delta_bwd.h"
 #include "gdn_common.cuh"
 
 namespace gdn {
 namespace {
 
-constexpr int Q = 64, THREADS = 256, COLS = 64;
+constexpr int Q = 64, THREADS = 512, COLS = 64;
 constexpr int DEPTH = 32, TILE = DEPTH * (Q + 4);  // steps and floats of one operand's tile
 constexpr int TILES = 4 * TILE;      // two operands, two buffers
 constexpr int SIDE = Q + 1;          // pitch of square matrices in shared memory
@@ -48,11 +51,11 @@ template <Along ALONG>
 __device__ __forceinline__ void tile_place(int e, int &row, int &step) {
   const int tid = threadIdx.x;
   if (ALONG == STEPS) {  // eight steps of four rows a warp: whole sectors, no bank twice
-    step = tid % 8 + 8 * (e % 4);
-    row = tid / 8 + 32 * (e / 4);
+    step = tid % 8 + 8 * e;
+    row = tid / 8;
   } else {
     row = tid % 64;
-    step = tid / 64 + 4 * e;
+    step = tid / 64 + 8 * e;
   }
 }
 
@@ -62,7 +65,7 @@ __device__ __forceinline__ void tile_place(int e, int &row, int &step) {
 template <Along A_ALONG, Along B_ALONG, typename A, typename B, typename Out>
 __device__ __forceinline__ void product(int M, int N, int K, float *tiles, A a, B b, Out out) {
   constexpr int EACH = DEPTH * Q / THREADS, PITCH = Q + 4;
-  const int ti = threadIdx.x / 16 * 4, tj = threadIdx.x % 16 * 4;
+  const int half = threadIdx.x / 256, ti = threadIdx.x % 256 / 16 * 4, tj = threadIdx.x % 16 * 4;
   for (int i0 = 0; i0 < M; i0 += 64)
     for (int j0 = 0; j0 < N; j0 += 64) {
       float acc[4][4] = {}, x[EACH], y[EACH];
@@ -91,9 +94,9 @@ __device__ __forceinline__ void product(int M, int N, int K, float *tiles, A a, 
         }
         __syncthreads();
         if (k0 + DEPTH < K) fetch(k0 + DEPTH);
-        const int steps = min(DEPTH, K - k0);
+        const int steps = min((half + 1) * DEPTH / 2, K - k0);
 #pragma unroll 8
-        for (int k = 0; k < steps; ++k) {
+        for (int k = half * DEPTH / 2; k < steps; ++k) {
           const float4 u = *reinterpret_cast<const float4 *>(as + k * PITCH + ti);
           const float4 v = *reinterpret_cast<const float4 *>(bs + k * PITCH + tj);
           const float f[4] = {u.x, u.y, u.z, u.w}, g[4] = {v.x, v.y, v.z, v.w};
@@ -104,13 +107,23 @@ __device__ __forceinline__ void product(int M, int N, int K, float *tiles, A a, 
         }
       }
       __syncthreads();  // the tiles have been read
+      // each half is left with two of a thread's rows
+      float *other = tiles + (threadIdx.x ^ 256);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (i0 + ti + i < M && j0 + tj + j < N) out(i0 + ti + i, j0 + tj + j, acc[i][j]);
+        for (int j = 0; j < 4; ++j) tiles[(4 * i + j) * THREADS + threadIdx.x] = half ? acc[i][j] : acc[i + 2][j];
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int row = i0 + ti + i + 2 * half, col = j0 + tj + j;
+          const float sum = (half ? acc[i + 2][j] : acc[i][j]) + other[(4 * i + j) * THREADS];
+          if (row < M && col < N) out(row, col, sum);
+        }
+      __syncthreads();
     }
-  __syncthreads();
 }
 
 // Rows of a token tensor [.., heads, D] of one chunk and head; zero past its end.
@@ -128,14 +141,15 @@ struct Rows {
   }
 };
 
-// grid: chunks, heads.  G, beta, P, A and T = (I + A)^-1 by forward substitution, a column a
-// thread (the columns of the identity, so that row i of T needs the rows before it), which
-// holds it in registers.
+// grid: chunks, heads.  G, beta, P, A and T = (I + A)^-1: its 16 x 16 blocks on the diagonal by
+// forward substitution, a column a thread, then the blocks below, a diagonal at a time,
+// T_(b+d, b) = -T_(b+d, b+d) sum_m A_(b+d, m) T_(m, b).  (All 64 rows by substitution, unrolled,
+// are 40 KB of instructions that wait to be fetched.)
 template <typename E>
 __global__ void __launch_bounds__(THREADS) simt_prepare_kernel(DeltaBwdParams p) {
   extern __shared__ __align__(16) float shared[];
   __shared__ float G[Q], beta[Q];
-  float *tiles = shared, *A = shared + TILES;  // [Q][Q]
+  float *tiles = shared, *A = shared + TILES;  // [Q][SIDE]
   const DeltaChunk ch = delta_chunk(p, blockIdx.x);
   const int head = blockIdx.y, hk = head / (p.H / p.Hg), tid = threadIdx.x;
   if (ch.len <= 0) return;
@@ -166,25 +180,40 @@ __global__ void __launch_bounds__(THREADS) simt_prepare_kernel(DeltaBwdParams p)
     w.P[i * Q + j] = i >= j ? p.scale * s * expf(G[i] - G[j]) : 0.f;
   });
   product<STEPS, STEPS>(Q, Q, p.K, tiles, k, kt, [&](int i, int j, float s) {
-    A[i * Q + j] = i > j ? beta[i] * s * expf(G[i] - G[j]) : 0.f;
+    A[i * SIDE + j] = i > j ? beta[i] * s * expf(G[i] - G[j]) : 0.f;
   });
+  float *T = tiles, *Y = tiles + Q * SIDE;  // (A's products are through)
+  for (int x = tid; x < Q * Q; x += THREADS) T[x / Q * SIDE + x % Q] = 0.f;
+  __syncthreads();
   if (tid < Q) {
-    float x[Q];
+    const int b = tid / 16 * 16, j = tid % 16;
+    float x[16];
 #pragma unroll
-    for (int i = 0; i < Q; ++i) {
-      float s[4] = {i == tid ? 1.f : 0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < 16; ++i) {
+      x[i] = i == j ? 1.f : 0.f;
 #pragma unroll
-      for (int m = 0; m < i; m += 4) {
-        const float4 u = *reinterpret_cast<const float4 *>(A + i * Q + m);
-        s[0] = fmaf(-u.x, x[m], s[0]);
-        if (m + 1 < i) s[1] = fmaf(-u.y, x[m + 1], s[1]);
-        if (m + 2 < i) s[2] = fmaf(-u.z, x[m + 2], s[2]);
-        if (m + 3 < i) s[3] = fmaf(-u.w, x[m + 3], s[3]);
-      }
-      x[i] = (s[0] + s[1]) + (s[2] + s[3]);
-      w.T[i * Q + tid] = x[i];
+      for (int m = 0; m < i; ++m) x[i] = fmaf(-A[(b + i) * SIDE + b + m], x[m], x[i]);
+      T[(b + i) * SIDE + tid] = x[i];
     }
   }
+  __syncthreads();
+  for (int d = 16; d < Q; d += 16) {
+    for (int x = tid; x < (Q - d) * 16; x += THREADS) {
+      const int col = x % (Q - d), b = col / 16 * 16, row = b + d + x / (Q - d);
+      float v = 0.f;
+      for (int m = b; m < b + d; ++m) v = fmaf(A[row * SIDE + m], T[m * SIDE + col], v);
+      Y[row * SIDE + col] = v;
+    }
+    __syncthreads();
+    for (int x = tid; x < (Q - d) * 16; x += THREADS) {
+      const int col = x % (Q - d), b = col / 16 * 16 + d, row = b + x / (Q - d);
+      float v = 0.f;
+      for (int m = b; m < b + 16; ++m) v = fmaf(-T[row * SIDE + m], Y[m * SIDE + col], v);
+      T[row * SIDE + col] = v;
+    }
+    __syncthreads();
+  }
+  for (int x = tid; x < Q * Q; x += THREADS) w.T[x] = T[x / Q * SIDE + x % Q];
 }
 
 // The factors of a chunk's rows in a walk: beta, e^G and e^(G_L - G), which is zero past the
@@ -326,15 +355,22 @@ struct Inputs {
   static constexpr int FLOATS = TILES + 3 * Q * KMAX + 4 * Q * SIDE + 8 * Q;
 };
 
-// sum_c x[i][c] y(i, c) of every row, four threads a row, to out[i].
+constexpr int EACH_ROW = THREADS / Q;  // threads of a row
+// v over a row's threads.
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+  for (int o = 1; o < EACH_ROW; o <<= 1) v += __shfl_xor_sync(~0u, v, o);
+  return v;
+}
+
+// sum_c x[i][c] y(i, c) of every row to out[i].
 template <typename Y>
 __device__ __forceinline__ void row_dots(const float *x, int K, Y y, float *out) {
-  const int i = threadIdx.x / 4;
+  const int i = threadIdx.x / EACH_ROW;
   float s = 0.f;
-  for (int c = threadIdx.x % 4; c < K; c += 4) s = fmaf(x[i * K + c], y(i, c), s);
-  s += __shfl_xor_sync(~0u, s, 1);
-  s += __shfl_xor_sync(~0u, s, 2);
-  if (threadIdx.x % 4 == 0) out[i] = s;
+  for (int c = threadIdx.x % EACH_ROW; c < K; c += EACH_ROW) s = fmaf(x[i * K + c], y(i, c), s);
+  s = row_sum(s);
+  if (threadIdx.x % EACH_ROW == 0) out[i] = s;
   __syncthreads();
 }
 
@@ -403,28 +439,25 @@ __global__ void __launch_bounds__(THREADS) simt_inputs_kernel(DeltaBwdParams p) 
     product<STEPS, ROWS>(Q, K, Q, s.tiles,
                          [&](int i, int j) { return s.A[i * SIDE + j] + s.A[j * SIDE + i]; }, k,
                          [&](int i, int c, float x) { s.dk[i * K + c] += x; });
-    // dr.v of every row, and dv; M's and B's sums, four threads a row
-    const int row = tid / 4;
+    // dr.v of every row, and dv; M's and B's sums
+    const int row = tid / EACH_ROW;
     float sum = 0.f, m = 0.f, b = 0.f;
-    for (int c = tid % 4; c < V; c += 4) {
+    for (int c = tid % EACH_ROW; c < V; c += EACH_ROW) {
       const float d = w.dr[(int64_t)row * V + c];
       sum = fmaf(d, v(row, c), sum);
       if (row < ch.len)
         static_cast<E *>(p.dv)[((ch.token + row) * p.H + head) * V + c] =
             from_f32<E>(f.beta[row] * d);
     }
-    for (int j = tid % 4; j < Q; j += 4) {
+    for (int j = tid % EACH_ROW; j < Q; j += EACH_ROW) {
       m += s.M[row * SIDE + j] + f.beta[row] * s.B[row * SIDE + j];
       m -= s.M[j * SIDE + row] + f.beta[j] * s.B[j * SIDE + row];
       b += s.B[row * SIDE + j];
     }
-#pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-      sum += __shfl_xor_sync(~0u, sum, o);
-      m += __shfl_xor_sync(~0u, m, o);
-      b += __shfl_xor_sync(~0u, b, o);
-    }
-    if (tid % 4 == 0) {
+    sum = row_sum(sum);
+    m = row_sum(m);
+    b = row_sum(b);
+    if (tid % EACH_ROW == 0) {
       dG[row] = m + qd[row] + f.beta[row] * kh[row] - kD[row];
       if (row < ch.len) p.dbeta[(ch.token + row) * p.H + head] = sum + kh[row] + b;
     }
@@ -471,7 +504,7 @@ template <typename E>
 cudaError_t launch(const DeltaBwdParams &p, cudaStream_t stream) {
   const dim3 walks((p.V + COLS - 1) / COLS, p.H, p.N);
   const int smem = Inputs::FLOATS * (int)sizeof(float);
-  constexpr int PREPARE = (TILES + Q * Q) * (int)sizeof(float);
+  constexpr int PREPARE = (TILES + Q * SIDE) * (int)sizeof(float);
   cudaError_t e = cudaFuncSetAttribute(simt_inputs_kernel<E>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess)
