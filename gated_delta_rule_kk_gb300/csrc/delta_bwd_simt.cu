@@ -8,12 +8,13 @@
 // latency of the products that wait for one another along a walk, half of it instructions: the
 // next 32 steps' operands are on their way in registers while 32 are multiplied, and every
 // load is of a place that exists, with the value chosen behind it, so that no load waits for
-// another.  (Three sequences of 261 to 376 tokens, 12 heads of 48 x 40, float32: 336 us; a
+// another.  (Three sequences of 261 to 376 tokens, 12 heads of 48 x 40, float32: 329 us; a
 // thread summing all steps, 256 of them, 353; with 16 steps a tile, two barriers each, and loads
 // inside branches 502.  A walk's rows and state kept in shared memory instead of the workspace
 // changed nothing.)
 #include "delta_bwd.h"
 #include "gdn_common.cuh"
+#include "rows.cuh"
 
 namespace gdn {
 namespace {
@@ -101,9 +102,10 @@ __device__ __forceinline__ void product(int M, int N, int K, float *tiles, A a, 
           const float4 v = *reinterpret_cast<const float4 *>(bs + k * PITCH + tj);
           const float f[4] = {u.x, u.y, u.z, u.w}, g[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(f[i], g[j], acc[i][j]);
+          for (int i = 0; i < 4; ++i) {
+            const float both[4] = {f[i], f[i], f[i], f[i]};
+            fma_row<4>(acc[i], both, g);
+          }
         }
       }
       __syncthreads();  // the tiles have been read
