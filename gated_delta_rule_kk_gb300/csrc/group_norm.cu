@@ -25,6 +25,7 @@ norm_fwd_kernel(NormParams p) {
   int turn = 0;
   NormCursor<T> xc(p, m, p.x, p.xs, p.xb, VEC), zc(p, m, p.z, p.zs, p.zb, VEC);
   NormCursor<T> yc(p, m, p.y, p.ys, p.yb, VEC);
+  const NormWeights<T, VEC> weight(p, m, p.weight), bias(p, m, p.bias);
   NormRow<T, VEC, PP> x[AHEAD], z[Z ? AHEAD : 1];
 #pragma unroll
   for (int i = 0; i < AHEAD; ++i) {
@@ -60,12 +61,12 @@ norm_fwd_kernel(NormParams p) {
         vmul<VEC>(u[j], u[j], r);
         if (p.weight != nullptr) {
           float w[VEC];
-          norm_weights<T, VEC>(p, m, p.weight, j, w);
+          weight.get(p, m, j, w);
           vmul<VEC>(u[j], u[j], w);
         }
         if (p.bias != nullptr) {
           float b[VEC];
-          norm_weights<T, VEC>(p, m, p.bias, j, b);
+          bias.get(p, m, j, b);
           vadd<VEC>(u[j], u[j], b);
         }
         if constexpr (Z) {

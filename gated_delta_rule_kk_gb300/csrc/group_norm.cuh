@@ -191,31 +191,39 @@ __device__ __forceinline__ void norm_act(int act, const float *z, float *out, fl
   }
 }
 
-// A piece of weights or biases (zero past the group), which lies as wide as the rows'.
+// A team's weights or biases: a piece of them (zero past the group) lies as wide as the rows'.
 template <typename T, int VEC>
-__device__ __forceinline__ void norm_weights(const NormParams &p, const NormTeam &m,
-                                             const void *from, int piece, float *w) {
-  const int c = (m.lane + piece * p.team) * VEC;
-  if (!m.live || c >= p.W) {
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) w[e] = 0.f;
-    return;
+struct NormWeights {
+  const unsigned char *at;  // NULL: none
+  int step;                 // bytes from piece to piece
+  __device__ __forceinline__ NormWeights(const NormParams &p, const NormTeam &m, const void *from) {
+    const int size = p.w_f32 ? 4 : (int)sizeof(T);
+    at = static_cast<const unsigned char *>(from);
+    if (at != nullptr) at += ((p.shared ? 0 : (int64_t)m.g * p.W) + m.lane * VEC) * size;
+    step = VEC * p.team * size;
   }
-  const int64_t at = (p.shared ? 0 : (int64_t)m.g * p.W) + c;
-  if (p.w_f32) {
-    constexpr int N = VEC >= 4 ? 4 : VEC;
+  __device__ __forceinline__ void get(const NormParams &p, const NormTeam &m, int piece, float *w) const {
+    if (!m.live || !m.in(p, piece * VEC * p.team, VEC)) {
 #pragma unroll
-    for (int e = 0; e < VEC; e += N) {
-      Row<float, N> r;
-      r.load(static_cast<const float *>(from) + at + e);
-      r.widen(w + e);
+      for (int e = 0; e < VEC; ++e) w[e] = 0.f;
+      return;
     }
-  } else {
-    Row<T, VEC> r;
-    r.load(static_cast<const T *>(from) + at);
-    r.widen(w);
+    const unsigned char *here = at + piece * step;
+    if (p.w_f32) {
+      constexpr int N = VEC >= 4 ? 4 : VEC;
+#pragma unroll
+      for (int e = 0; e < VEC; e += N) {
+        Row<float, N> r;
+        r.load(reinterpret_cast<const float *>(here) + e);
+        r.widen(w + e);
+      }
+    } else {
+      Row<T, VEC> r;
+      r.load(reinterpret_cast<const T *>(here));
+      r.widen(w);
+    }
   }
-}
+};
 
 // A team's way through one tensor: where the next token's pieces of it are.  (A place is
 // worked out once where tokens lie one stride apart, then moved on.)

@@ -26,6 +26,7 @@ norm_bwd_kernel(NormParams p) {
   NormCursor<T> gc(p, m, p.dy, p.gs, p.gb, VEC), xc(p, m, p.x, p.xs, p.xb, VEC);
   NormCursor<T> zc(p, m, p.z, p.zs, p.zb, VEC), dxc(p, m, p.y, p.ys, p.yb, VEC);
   NormCursor<T> dzc(p, m, p.dz, p.ds, p.db, VEC);
+  const NormWeights<T, VEC> weight(p, m, p.weight), bias(p, m, p.bias);
   NormRow<T, VEC, PP> x[AHEAD], z[Z ? AHEAD : 1], g[AHEAD];
 #pragma unroll
   for (int i = 0; i < AHEAD; ++i) {
@@ -70,7 +71,7 @@ norm_bwd_kernel(NormParams p) {
       for (int j = 0; j < PP; ++j) {
         vmul<VEC>(n[j], n[j], r);
         float w[VEC], v[VEC];
-        if (p.weight != nullptr) norm_weights<T, VEC>(p, m, p.weight, j, w);
+        if (p.weight != nullptr) weight.get(p, m, j, w);
         const bool gated = Z && !p.gate_first, alone = !Z && p.act != GDN_ACT_NONE;
         if (gated || alone) {  // m
           if (p.weight != nullptr) {
@@ -81,7 +82,7 @@ norm_bwd_kernel(NormParams p) {
           }
           if (p.bias != nullptr) {
             float b[VEC];
-            norm_weights<T, VEC>(p, m, p.bias, j, b);
+            bias.get(p, m, j, b);
             vadd<VEC>(v, v, b);
           }
           if constexpr (Z) {
