@@ -13,14 +13,14 @@
 namespace gdn {
 namespace {
 
-template <typename T, int VEC, int PP, bool Z, bool WIDE>
+template <typename T, int VEC, int PP, bool Z, bool WHOLE, bool WIDE>
 __global__ void __launch_bounds__(
     norm_block(PP * VEC, WIDE),
     WIDE ? 1 : norm_fwd_per_sm(PP * VEC, norm_words(sizeof(T), VEC, PP), Z))
 norm_fwd_kernel(NormParams p) {
   constexpr int AHEAD = WIDE ? 1 : norm_fwd_ahead(norm_words(sizeof(T), VEC, PP), Z);
   __shared__ float buf[2][NORM_WARPS][2];
-  const NormTeam m(p);
+  const NormTeam<WHOLE> m(p);
   if (!bounds_ok(p.team * p.rows * p.span <= (int)blockDim.x, p.err)) return;
   int turn = 0;
   NormCursor<T> xc(p, m, p.x, p.xs, p.xb, VEC), zc(p, m, p.z, p.zs, p.zb, VEC);
@@ -83,11 +83,6 @@ norm_fwd_kernel(NormParams p) {
 
 // ---------------------------------------------------------------- host
 
-// How a call is shared out: channels a piece, pieces a thread, threads a block and blocks.
-struct NormPlan {
-  int vec, pieces, threads, blocks;
-};
-
 // `t` passes the last token by a few steps of less than 2^18, and has to stay within 31 bits.
 constexpr int64_t NORM_MAX_TOKENS = MAX_TOKENS - (1 << 20);
 
@@ -98,7 +93,7 @@ NormPlan norm_plan(NormParams &p, bool bf16, int vec, bool bwd) {
   while (n < most && (all + n - 1) / n > 32) n += n < 4 ? n : 2;
   p.team = 1;
   while (p.team * n < all) p.team *= 2;
-  NormPlan plan{vec, n, std::max(NORM_THREADS, p.team), 0};
+  NormPlan plan{vec, n, std::max(NORM_THREADS, p.team), 0, false};
   const int per_sm = bwd ? norm_bwd_per_sm(vec * n)
                          : norm_fwd_per_sm(vec * n, norm_words(bf16 ? 2 : 4, vec, n), p.z != nullptr);
   const int teams = plan.threads / p.team;
@@ -111,6 +106,7 @@ NormPlan norm_plan(NormParams &p, bool bf16, int vec, bool bwd) {
   const int64_t down = std::max<int64_t>(1, std::min(held, wanted));
   p.step = (int)down * p.rows;
   plan.blocks = (int)(down * p.blocks_per_row);
+  plan.whole = p.team * n == all && teams == p.rows * p.span && p.G % p.span == 0;
   return plan;
 }
 
@@ -228,17 +224,16 @@ size_t bwd_workspace(const group_norm_bwd_args &a, const NormParams &p, const No
 
 }  // namespace
 
-cudaError_t launch_norm_fwd(const NormParams &p, bool bf16, int vec, int pieces, int threads,
-                            int blocks, cudaStream_t stream) {
-  return norm_forms(bf16, vec, pieces, p.z != nullptr, [&](auto t, auto v, auto n, auto z) {
+cudaError_t launch_norm_fwd(const NormParams &p, bool bf16, const NormPlan &plan, cudaStream_t stream) {
+  return norm_forms(bf16, plan, p.z != nullptr, [&](auto t, auto v, auto n, auto z, auto whole) {
     using T = decltype(t);
     constexpr int VEC = decltype(v)::value, PP = decltype(n)::value;
-    constexpr bool Z = decltype(z)::value;
-    if (threads <= NORM_THREADS) {
-      norm_fwd_kernel<T, VEC, PP, Z, false><<<blocks, threads, 0, stream>>>(p);
+    constexpr bool Z = decltype(z)::value, WHOLE = decltype(whole)::value;
+    if (plan.threads <= NORM_THREADS) {
+      norm_fwd_kernel<T, VEC, PP, Z, WHOLE, false><<<plan.blocks, plan.threads, 0, stream>>>(p);
     } else {  // only with the most pieces a thread
       if constexpr (PP == norm_pieces(VEC))
-        norm_fwd_kernel<T, VEC, PP, Z, true><<<blocks, threads, 0, stream>>>(p);
+        norm_fwd_kernel<T, VEC, PP, Z, WHOLE, true><<<plan.blocks, plan.threads, 0, stream>>>(p);
       else
         return cudaErrorInvalidConfiguration;
     }
@@ -271,8 +266,7 @@ gdn_status_t group_norm_fwd(const group_norm_args *a, gdn_stream_t stream) {
   const NormPlan plan = norm_plan(p, bf16, vec, false);
   p.err = device_error_word();
   if (p.err == nullptr) return launch_status(cudaGetLastError(), "device error word");
-  return launch_status(launch_norm_fwd(p, bf16, plan.vec, plan.pieces, plan.threads, plan.blocks,
-                                       reinterpret_cast<cudaStream_t>(stream)),
+  return launch_status(launch_norm_fwd(p, bf16, plan, reinterpret_cast<cudaStream_t>(stream)),
                        "norm launch");
 }
 
@@ -310,8 +304,7 @@ gdn_status_t group_norm_bwd(const group_norm_bwd_args *a, gdn_stream_t stream) {
   }
   p.err = device_error_word();
   if (p.err == nullptr) return launch_status(cudaGetLastError(), "device error word");
-  cudaError_t e = launch_norm_bwd(p, a->dtype == GDN_BF16, plan.vec, plan.pieces, plan.threads,
-                                  plan.blocks, s);
+  cudaError_t e = launch_norm_bwd(p, a->dtype == GDN_BF16, plan, s);
   if (e == cudaSuccess && need > 0)
     e = launch_norm_sums(p.part, part_rows(p, plan), part_columns(p), a->dweight, a->dbias, s);
   return launch_status(e, "norm gradient launch");

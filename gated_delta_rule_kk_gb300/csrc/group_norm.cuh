@@ -36,7 +36,9 @@ struct NormParams {
   int team, rows, span, blocks_per_row, step;
 };
 
-// A team's place: its group, its first token, and whether it has any.
+// A team's place: its group, its first token, and whether it has any.  WHOLE: the teams fill
+// their blocks and the pieces their groups, so that only tokens end.
+template <bool WHOLE>
 struct NormTeam {
   int lane, g, t, index;
   bool live;
@@ -46,11 +48,11 @@ struct NormTeam {
     const int row = index / p.span;
     g = blockIdx.x % p.blocks_per_row * p.span + index % p.span;
     t = blockIdx.x / p.blocks_per_row * p.rows + row;
-    live = row < p.rows && g < p.G;
+    live = WHOLE || (row < p.rows && g < p.G);
   }
   // whether this thread's piece `from` channels behind its first is one of the group's
   __device__ __forceinline__ bool in(const NormParams &p, int from, int vec) const {
-    return lane * vec + from < p.W;
+    return WHOLE || lane * vec + from < p.W;
   }
 };
 
@@ -196,13 +198,15 @@ template <typename T, int VEC>
 struct NormWeights {
   const unsigned char *at;  // NULL: none
   int step;                 // bytes from piece to piece
-  __device__ __forceinline__ NormWeights(const NormParams &p, const NormTeam &m, const void *from) {
+  template <bool WHOLE>
+  __device__ __forceinline__ NormWeights(const NormParams &p, const NormTeam<WHOLE> &m, const void *from) {
     const int size = p.w_f32 ? 4 : (int)sizeof(T);
     at = static_cast<const unsigned char *>(from);
     if (at != nullptr) at += ((p.shared ? 0 : (int64_t)m.g * p.W) + m.lane * VEC) * size;
     step = VEC * p.team * size;
   }
-  __device__ __forceinline__ void get(const NormParams &p, const NormTeam &m, int piece, float *w) const {
+  template <bool WHOLE>
+  __device__ __forceinline__ void get(const NormParams &p, const NormTeam<WHOLE> &m, int piece, float *w) const {
     if (!m.live || !m.in(p, piece * VEC * p.team, VEC)) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) w[e] = 0.f;
@@ -231,7 +235,8 @@ template <typename T>
 struct NormCursor {
   T *at;
   int64_t stride, batch, move;
-  __device__ __forceinline__ NormCursor(const NormParams &p, const NormTeam &m, const void *base,
+  template <bool WHOLE>
+  __device__ __forceinline__ NormCursor(const NormParams &p, const NormTeam<WHOLE> &m, const void *base,
                                         int64_t stride_, int64_t batch_, int vec)
       : stride(stride_), batch(batch_), move(p.step * stride_) {
     at = static_cast<T *>(const_cast<void *>(base)) + (int64_t)m.g * p.W + m.lane * vec;
@@ -253,14 +258,16 @@ struct NormCursor {
 template <typename T, int VEC, int PP>
 struct NormRow {
   Row<T, VEC> r[PP];
-  __device__ __forceinline__ void load(const NormParams &p, const NormTeam &m, NormCursor<T> &c, int t) {
+  template <bool WHOLE>
+  __device__ __forceinline__ void load(const NormParams &p, const NormTeam<WHOLE> &m, NormCursor<T> &c, int t) {
     const T *at = c.next(p, t);
     if (!m.live || t >= p.tokens) return;
 #pragma unroll
     for (int j = 0; j < PP; ++j)
       if (m.in(p, j * VEC * p.team, VEC)) r[j].load(at + j * VEC * p.team);
   }
-  __device__ __forceinline__ void store(const NormParams &p, const NormTeam &m, NormCursor<T> &c,
+  template <bool WHOLE>
+  __device__ __forceinline__ void store(const NormParams &p, const NormTeam<WHOLE> &m, NormCursor<T> &c,
                                         int t) const {
     T *at = c.next(p, t);
     if (!m.live || t >= p.tokens) return;
@@ -276,8 +283,8 @@ struct NormRow {
 
 // Takes u's mean off (where wanted) and returns 1 / root.  Pieces past the group hold zero and
 // stay so.
-template <int VEC, int PP>
-__device__ __forceinline__ float norm_root(const NormParams &p, const NormTeam &m,
+template <int VEC, int PP, bool WHOLE>
+__device__ __forceinline__ float norm_root(const NormParams &p, const NormTeam<WHOLE> &m,
                                            float (&u)[PP][VEC], float (*buf)[NORM_WARPS][2],
                                            int &turn) {
   const float inv = 1.f / (float)p.W;
@@ -301,38 +308,49 @@ __device__ __forceinline__ float norm_root(const NormParams &p, const NormTeam &
   return rsqrtf(fmaf(v[0], inv, p.eps));
 }
 
-cudaError_t launch_norm_fwd(const NormParams &p, bool bf16, int vec, int pieces, int threads,
-                            int blocks, cudaStream_t stream);
-cudaError_t launch_norm_bwd(const NormParams &p, bool bf16, int vec, int pieces, int threads,
-                            int blocks, cudaStream_t stream);
+// How a call is shared out: channels a piece, pieces a thread, threads a block, blocks, and
+// whether teams and pieces come out even.
+struct NormPlan {
+  int vec, pieces, threads, blocks;
+  bool whole;
+};
+cudaError_t launch_norm_fwd(const NormParams &p, bool bf16, const NormPlan &plan, cudaStream_t stream);
+cudaError_t launch_norm_bwd(const NormParams &p, bool bf16, const NormPlan &plan, cudaStream_t stream);
 // dw and db (or NULL) [columns] from part [rows][2][columns].
 cudaError_t launch_norm_sums(const float *part, int rows, int columns, float *dw, float *db,
                              cudaStream_t stream);
 
-// Calls f with the element type, VEC, PP and whether there is a z as compile-time values.
+// Calls f with the element type, VEC, PP, whether there is a z and whether all comes out even
+// (looked at for pieces of 16 bytes only) as compile-time values.
 template <typename F>
-cudaError_t norm_forms(bool bf16, int vec, int pieces, bool z, F &&f) {
-  auto gate = [&](auto t, auto v, auto n) {
-    return z ? f(t, v, n, std::true_type()) : f(t, v, n, std::false_type());
+cudaError_t norm_forms(bool bf16, const NormPlan &plan, bool z, F &&f) {
+  auto gate = [&](auto t, auto v, auto n, auto whole) {
+    return z ? f(t, v, n, std::true_type(), whole) : f(t, v, n, std::false_type(), whole);
   };
-  auto few = [&](auto t, auto v) {  // PP of 1, 2 (and 4 for four channels a piece)
-    if (pieces == 1) return gate(t, v, std::integral_constant<int, 1>());
-    if (decltype(v)::value == 8 || pieces == 2) return gate(t, v, std::integral_constant<int, 2>());
-    return gate(t, v, std::integral_constant<int, decltype(v)::value == 8 ? 2 : 4>());
+  const int pieces = plan.pieces;
+  auto few = [&](auto t, auto v, auto whole) {  // PP of 1, 2 (and 4 for four channels a piece)
+    if (pieces == 1) return gate(t, v, std::integral_constant<int, 1>(), whole);
+    if (decltype(v)::value == 8 || pieces == 2)
+      return gate(t, v, std::integral_constant<int, 2>(), whole);
+    return gate(t, v, std::integral_constant<int, decltype(v)::value == 8 ? 2 : 4>(), whole);
   };
   auto many = [&](auto t, auto v) {
-    if (pieces == 1) return gate(t, v, std::integral_constant<int, 1>());
-    if (pieces == 2) return gate(t, v, std::integral_constant<int, 2>());
-    if (pieces == 4) return gate(t, v, std::integral_constant<int, 4>());
-    if (pieces == 6) return gate(t, v, std::integral_constant<int, 6>());
-    return gate(t, v, std::integral_constant<int, 8>());
+    const std::false_type whole;
+    if (pieces == 1) return gate(t, v, std::integral_constant<int, 1>(), whole);
+    if (pieces == 2) return gate(t, v, std::integral_constant<int, 2>(), whole);
+    if (pieces == 4) return gate(t, v, std::integral_constant<int, 4>(), whole);
+    if (pieces == 6) return gate(t, v, std::integral_constant<int, 6>(), whole);
+    return gate(t, v, std::integral_constant<int, 8>(), whole);
+  };
+  auto both = [&](auto t, auto v) {
+    return plan.whole ? few(t, v, std::true_type()) : few(t, v, std::false_type());
   };
   if (bf16) {
-    if (vec == 8) return few(__nv_bfloat16(), std::integral_constant<int, 8>());
-    if (vec == 2) return many(__nv_bfloat16(), std::integral_constant<int, 2>());
+    if (plan.vec == 8) return both(__nv_bfloat16(), std::integral_constant<int, 8>());
+    if (plan.vec == 2) return many(__nv_bfloat16(), std::integral_constant<int, 2>());
     return many(__nv_bfloat16(), std::integral_constant<int, 1>());
   }
-  if (vec == 4) return few(0.f, std::integral_constant<int, 4>());
+  if (plan.vec == 4) return both(0.f, std::integral_constant<int, 4>());
   return many(0.f, std::integral_constant<int, 1>());
 }
 

@@ -12,12 +12,12 @@
 namespace gdn {
 namespace {
 
-template <typename T, int VEC, int PP, bool Z, bool WIDE>
+template <typename T, int VEC, int PP, bool Z, bool WHOLE, bool WIDE>
 __global__ void __launch_bounds__(norm_block(PP * VEC, WIDE), WIDE ? 1 : norm_bwd_per_sm(PP * VEC))
 norm_bwd_kernel(NormParams p) {
   __shared__ float buf[2][NORM_WARPS][2];
   extern __shared__ float sums[];  // [threads][PP * VEC]
-  const NormTeam m(p);
+  const NormTeam<WHOLE> m(p);
   if (!bounds_ok(p.team * p.rows * p.span <= (int)blockDim.x, p.err)) return;
   int turn = 0;
   const float inv = 1.f / (float)p.W;
@@ -180,18 +180,17 @@ __global__ void __launch_bounds__(1024) norm_sums_kernel(const float *part, int 
 
 }  // namespace
 
-cudaError_t launch_norm_bwd(const NormParams &p, bool bf16, int vec, int pieces, int threads,
-                            int blocks, cudaStream_t stream) {
-  const int smem = p.part ? threads * pieces * vec * (int)sizeof(float) : 0;
-  return norm_forms(bf16, vec, pieces, p.z != nullptr, [&](auto t, auto v, auto n, auto z) {
+cudaError_t launch_norm_bwd(const NormParams &p, bool bf16, const NormPlan &plan, cudaStream_t stream) {
+  const int smem = p.part ? plan.threads * plan.pieces * plan.vec * (int)sizeof(float) : 0;
+  return norm_forms(bf16, plan, p.z != nullptr, [&](auto t, auto v, auto n, auto z, auto whole) {
     using T = decltype(t);
     constexpr int VEC = decltype(v)::value, PP = decltype(n)::value;
-    constexpr bool Z = decltype(z)::value;
-    if (threads <= NORM_THREADS) {
-      norm_bwd_kernel<T, VEC, PP, Z, false><<<blocks, threads, smem, stream>>>(p);
+    constexpr bool Z = decltype(z)::value, WHOLE = decltype(whole)::value;
+    if (plan.threads <= NORM_THREADS) {
+      norm_bwd_kernel<T, VEC, PP, Z, WHOLE, false><<<plan.blocks, plan.threads, smem, stream>>>(p);
     } else {  // only with the most pieces a thread
       if constexpr (PP == norm_pieces(VEC))
-        norm_bwd_kernel<T, VEC, PP, Z, true><<<blocks, threads, smem, stream>>>(p);
+        norm_bwd_kernel<T, VEC, PP, Z, WHOLE, true><<<plan.blocks, plan.threads, smem, stream>>>(p);
       else
         return cudaErrorInvalidConfiguration;
     }
