@@ -25,7 +25,7 @@ norm_fwd_kernel(NormParams p) {
   int turn = 0;
   NormCursor<T> xc(p, m, p.x, p.xs, p.xb, VEC), zc(p, m, p.z, p.zs, p.zb, VEC);
   NormCursor<T> yc(p, m, p.y, p.ys, p.yb, VEC);
-  const NormWeights<T, VEC> weight(p, m, p.weight), bias(p, m, p.bias);
+  const NormWeights<T, VEC, PP, false> weight(p, m, p.weight), bias(p, m, p.bias);
   NormRow<T, VEC, PP> x[AHEAD], z[Z ? AHEAD : 1];
 #pragma unroll
   for (int i = 0; i < AHEAD; ++i) {
@@ -225,10 +225,10 @@ size_t bwd_workspace(const group_norm_bwd_args &a, const NormParams &p, const No
 }  // namespace
 
 cudaError_t launch_norm_fwd(const NormParams &p, bool bf16, const NormPlan &plan, cudaStream_t stream) {
-  return norm_forms(bf16, plan, p.z != nullptr, [&](auto t, auto v, auto n, auto z, auto whole) {
+  return norm_forms(bf16, plan, p, [&](auto t, auto v, auto n, auto gate, auto whole) {
     using T = decltype(t);
     constexpr int VEC = decltype(v)::value, PP = decltype(n)::value;
-    constexpr bool Z = decltype(z)::value, WHOLE = decltype(whole)::value;
+    constexpr bool Z = decltype(gate)::value != NO_GATE, WHOLE = decltype(whole)::value;
     if (plan.threads <= NORM_THREADS) {
       norm_fwd_kernel<T, VEC, PP, Z, WHOLE, false><<<plan.blocks, plan.threads, 0, stream>>>(p);
     } else {  // only with the most pieces a thread

@@ -194,19 +194,30 @@ __device__ __forceinline__ void norm_act(int act, const float *z, float *out, fl
 }
 
 // A team's weights or biases: a piece of them (zero past the group) lies as wide as the rows'.
-template <typename T, int VEC>
+// KEEP: those of the rows' own type stay in registers; others are read for every token, from L1.
+template <typename T, int VEC, int PP, bool KEEP>
 struct NormWeights {
   const unsigned char *at;  // NULL: none
   int step;                 // bytes from piece to piece
+  Row<T, VEC> kept[KEEP ? PP : 1];
   template <bool WHOLE>
   __device__ __forceinline__ NormWeights(const NormParams &p, const NormTeam<WHOLE> &m, const void *from) {
     const int size = p.w_f32 ? 4 : (int)sizeof(T);
     at = static_cast<const unsigned char *>(from);
     if (at != nullptr) at += ((p.shared ? 0 : (int64_t)m.g * p.W) + m.lane * VEC) * size;
     step = VEC * p.team * size;
+    if constexpr (KEEP) {
+#pragma unroll
+      for (int j = 0; j < PP; ++j) {
+        kept[j].zero();
+        if (at != nullptr && !p.w_f32 && m.live && m.in(p, j * VEC * p.team, VEC))
+          kept[j].load(reinterpret_cast<const T *>(at + j * step));
+      }
+    }
   }
   template <bool WHOLE>
   __device__ __forceinline__ void get(const NormParams &p, const NormTeam<WHOLE> &m, int piece, float *w) const {
+    if (KEEP && !p.w_f32) return kept[KEEP ? piece : 0].widen(w);
     if (!m.live || !m.in(p, piece * VEC * p.team, VEC)) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) w[e] = 0.f;
@@ -320,12 +331,17 @@ cudaError_t launch_norm_bwd(const NormParams &p, bool bf16, const NormPlan &plan
 cudaError_t launch_norm_sums(const float *part, int rows, int columns, float *dw, float *db,
                              cudaStream_t stream);
 
-// Calls f with the element type, VEC, PP, whether there is a z and whether all comes out even
-// (looked at for pieces of 16 bytes only) as compile-time values.
+// Where z stands.
+enum NormGate { NO_GATE, GATE_AFTER, GATE_BEFORE };
+
+// Calls f with the element type, VEC, PP, the gate and whether all comes out even (looked at for
+// pieces of 16 bytes only) as compile-time values.
 template <typename F>
-cudaError_t norm_forms(bool bf16, const NormPlan &plan, bool z, F &&f) {
+cudaError_t norm_forms(bool bf16, const NormPlan &plan, const NormParams &p, F &&f) {
   auto gate = [&](auto t, auto v, auto n, auto whole) {
-    return z ? f(t, v, n, std::true_type(), whole) : f(t, v, n, std::false_type(), whole);
+    if (p.z == nullptr) return f(t, v, n, std::integral_constant<NormGate, NO_GATE>(), whole);
+    if (p.gate_first) return f(t, v, n, std::integral_constant<NormGate, GATE_BEFORE>(), whole);
+    return f(t, v, n, std::integral_constant<NormGate, GATE_AFTER>(), whole);
   };
   const int pieces = plan.pieces;
   auto few = [&](auto t, auto v, auto whole) {  // PP of 1, 2 (and 4 for four channels a piece)
