@@ -55,6 +55,24 @@ struct DeltaChunk {
 };
 
 #ifdef __CUDACC__
+// Launches a kernel that may begin while the one before it on the stream ends; it waits
+// (griddepcontrol.wait) before it reads anything.
+template <typename... P, typename... A>
+cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t stream,
+                          const A &...args) {
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Chunk c; len 0 if there is none.
 __device__ __forceinline__ DeltaChunk delta_chunk(const DeltaBwdParams &p, int64_t c) {
   DeltaChunk k{0, 0, 0, 0};

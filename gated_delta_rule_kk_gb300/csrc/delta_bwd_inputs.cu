@@ -174,6 +174,7 @@ __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdPar
   __shared__ uint32_t tmem_at;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rep = p.H / p.Hg, tiles = (p.V + VT - 1) / VT;
+  ptx::griddep_wait();
   const int64_t chunks = p.cu ? p.first[p.N] : p.chunks;  // (-1 with bad offsets)
   if (!bounds_ok(chunks <= p.chunks && gridDim.x <= DELTA_MAX_BLOCKS, p.err)) return;
   if (threadIdx.x == 0) {
@@ -622,11 +623,8 @@ cudaError_t launch(const DeltaBwdParams &p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int64_t most = std::min<int64_t>(std::min(sm_count(), DELTA_MAX_BLOCKS), p.chunks * p.Hg);
   const unsigned blocks = (unsigned)most;
-  if (grouped)
-    tc_inputs_kernel<KP, true><<<blocks, 32 * IN_WARPS, InputsShared<KP>::BYTES, stream>>>(p);
-  else
-    tc_inputs_kernel<KP, false><<<blocks, 32 * IN_WARPS, InputsShared<KP>::BYTES, stream>>>(p);
-  return cudaGetLastError();
+  return launch_behind(grouped ? tc_inputs_kernel<KP, true> : tc_inputs_kernel<KP, false>, dim3(blocks),
+                       32 * IN_WARPS, InputsShared<KP>::BYTES, stream, p);
 }
 
 }  // namespace

@@ -14,6 +14,7 @@
 // changed nothing.)
 #include "delta_bwd.h"
 #include "gdn_common.cuh"
+#include "ptx.cuh"
 #include "rows.cuh"
 
 namespace gdn {
@@ -152,6 +153,7 @@ __global__ void __launch_bounds__(THREADS) simt_prepare_kernel(DeltaBwdParams p)
   extern __shared__ __align__(16) float shared[];
   __shared__ float G[Q], beta[Q];
   float *tiles = shared, *A = shared + TILES;  // [Q][SIDE]
+  ptx::griddep_wait();
   const DeltaChunk ch = delta_chunk(p, blockIdx.x);
   const int head = blockIdx.y, hk = head / (p.H / p.Hg), tid = threadIdx.x;
   if (ch.len <= 0) return;
@@ -243,6 +245,7 @@ __global__ void __launch_bounds__(THREADS) simt_states_kernel(DeltaBwdParams p) 
   const int v0 = blockIdx.x * COLS, nv = min(COLS, p.V - v0), head = blockIdx.y;
   const int hk = head / (p.H / p.Hg), K = p.K, V = p.V;
   int64_t first;
+  ptx::griddep_wait();
   if (!delta_good(p)) return;
   const int n = delta_turn(p, blockIdx.z), count = delta_chunks(p, n, &first);
   if (count == 0) return;
@@ -287,6 +290,7 @@ __global__ void __launch_bounds__(THREADS) simt_grads_kernel(DeltaBwdParams p) {
   const int v0 = blockIdx.x * COLS, nv = min(COLS, p.V - v0), head = blockIdx.y;
   const int hk = head / (p.H / p.Hg), K = p.K, V = p.V;
   int64_t first;
+  ptx::griddep_wait();
   if (!delta_good(p)) return;
   const int n = delta_turn(p, blockIdx.z), count = delta_chunks(p, n, &first);
   const int64_t state = ((int64_t)n * p.H + head) * K * V;
@@ -383,6 +387,7 @@ __global__ void __launch_bounds__(THREADS) simt_inputs_kernel(DeltaBwdParams p) 
   extern __shared__ __align__(16) float shared[];
   __shared__ Factors f;
   const Inputs s(shared);
+  ptx::griddep_wait();
   const DeltaChunk ch = delta_chunk(p, blockIdx.x);
   const int hk = blockIdx.y, rep = p.H / p.Hg, tid = threadIdx.x, K = p.K, V = p.V;
   if (ch.len <= 0) return;
@@ -513,11 +518,17 @@ cudaError_t launch(const DeltaBwdParams &p, cudaStream_t stream) {
     e = cudaFuncSetAttribute(simt_prepare_kernel<E>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              PREPARE);
   if (e != cudaSuccess) return e;
-  simt_prepare_kernel<E><<<dim3((unsigned)p.chunks, p.H), THREADS, PREPARE, stream>>>(p);
-  simt_states_kernel<E><<<walks, THREADS, 0, stream>>>(p);
-  simt_grads_kernel<E><<<walks, THREADS, 0, stream>>>(p);
-  simt_inputs_kernel<E><<<dim3((unsigned)p.chunks, p.Hg), THREADS, smem, stream>>>(p);
-  return cudaGetLastError();
+  const dim3 all((unsigned)p.chunks, p.H);
+  if (p.cu != nullptr) {
+    e = launch_behind(simt_prepare_kernel<E>, all, THREADS, PREPARE, stream, p);
+  } else {  // the call's first kernel
+    simt_prepare_kernel<E><<<all, THREADS, PREPARE, stream>>>(p);
+    e = cudaGetLastError();
+  }
+  if (e == cudaSuccess) e = launch_behind(simt_states_kernel<E>, walks, THREADS, 0, stream, p);
+  if (e == cudaSuccess) e = launch_behind(simt_grads_kernel<E>, walks, THREADS, 0, stream, p);
+  if (e != cudaSuccess) return e;
+  return launch_behind(simt_inputs_kernel<E>, dim3((unsigned)p.chunks, p.Hg), THREADS, smem, stream, p);
 }
 
 }  // namespace

@@ -24,6 +24,7 @@ struct PrepareShared {
 template <int KP>
 __global__ void __launch_bounds__(PREP, 3) tc_prepare_kernel(DeltaBwdParams p) {
   extern __shared__ __align__(128) unsigned char shared[];
+  ptx::griddep_wait();
   bf16 *q = reinterpret_cast<bf16 *>(shared), *k = q + Q * KP;
   constexpr int PITCH = PrepareShared<KP>::PITCH;
   float(*A)[PITCH] = reinterpret_cast<float(*)[PITCH]>(shared + PrepareShared<KP>::IMAGES);
@@ -177,7 +178,9 @@ cudaError_t launch(const DeltaBwdParams &p, cudaStream_t stream) {
   const cudaError_t e = cudaFuncSetAttribute(tc_prepare_kernel<KP>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
   if (e != cudaSuccess) return e;
-  tc_prepare_kernel<KP><<<dim3((unsigned)p.chunks, p.H), PREP, BYTES, stream>>>(p);
+  const dim3 grid((unsigned)p.chunks, p.H);
+  if (p.cu != nullptr) return launch_behind(tc_prepare_kernel<KP>, grid, PREP, BYTES, stream, p);
+  tc_prepare_kernel<KP><<<grid, PREP, BYTES, stream>>>(p);  // the call's first kernel
   return cudaGetLastError();
 }
 

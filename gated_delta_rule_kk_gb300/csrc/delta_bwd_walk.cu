@@ -403,6 +403,7 @@ __device__ __forceinline__ bool begin_walk(const DeltaBwdParams &p, Walk<KP, BAC
   w.g = w.lane >> 2;
   w.t = w.lane & 3;
   w.ok = true;
+  ptx::griddep_wait();
   if (!delta_good(p)) return false;
   w.n = delta_turn(p, blockIdx.z);
   w.count = delta_chunks(p, w.n, &w.first);
@@ -653,9 +654,9 @@ cudaError_t launch(const DeltaBwdParams &p, cudaStream_t stream) {
     e = cudaFuncSetAttribute(tc_grads_kernel<KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, GRADS);
   if (e != cudaSuccess) return e;
   const dim3 grid((p.V + VT - 1) / VT, p.H, p.N);
-  tc_states_kernel<KP><<<grid, 32 * (CARRY + 2), STATES, stream>>>(p);
-  tc_grads_kernel<KP><<<grid, 32 * (2 * CARRY + 2), GRADS, stream>>>(p);
-  return cudaGetLastError();
+  e = launch_behind(tc_states_kernel<KP>, grid, 32 * (CARRY + 2), STATES, stream, p);
+  if (e != cudaSuccess) return e;
+  return launch_behind(tc_grads_kernel<KP>, grid, 32 * (2 * CARRY + 2), GRADS, stream, p);
 }
 
 }  // namespace
