@@ -12,24 +12,28 @@ namespace {
 // block, T_(b+d, b) = -T_(b+d, b+d) sum_m A_(b+d, m) T_(m, b), as products of pairs of
 // bfloat16 pieces: transposed, so that the sum's accumulators are the left operand of the
 // product behind it.  (As float32 sums from shared memory, two loads a multiplication, they
-// took a third of the kernel's instructions: 80 us at 2 x 4096 tokens, 16 heads of 128.)
+// took a third of the kernel's instructions: 80 us at 2 x 4096 tokens, 16 heads of 128; now 53.)
+// Barriers between the phases are what a warp waits for most: four blocks an SM, T in the place
+// of the images before it (three blocks: 59 us).
 constexpr int PREP = 256;
 template <int KP>
 struct PrepareShared {
-  static constexpr int IMAGES = 2 * Block<KP>::SQUARE;  // q and k, then P and A, then T
   static constexpr int PITCH = Q + 8;  // of A and T in float32
-  static constexpr int BYTES = IMAGES + (2 * Q * PITCH + 2 * Q) * 4;
+  // q and k, then P's and A's images, then T and behind it its image; A
+  static constexpr int T_IMAGE = Q * PITCH * 4, IMAGES = T_IMAGE + Block<KP>::SQUARE;
+  static constexpr int BYTES = IMAGES + (Q * PITCH + 2 * Q) * 4;
+  static_assert(IMAGES >= 2 * Block<KP>::SQUARE && IMAGES >= 2 * Q * KP * 2, "");
 };
 
 template <int KP>
-__global__ void __launch_bounds__(PREP, 3) tc_prepare_kernel(DeltaBwdParams p) {
+__global__ void __launch_bounds__(PREP, 4) tc_prepare_kernel(DeltaBwdParams p) {
   extern __shared__ __align__(128) unsigned char shared[];
   ptx::griddep_wait();
   bf16 *q = reinterpret_cast<bf16 *>(shared), *k = q + Q * KP;
   constexpr int PITCH = PrepareShared<KP>::PITCH;
   float(*A)[PITCH] = reinterpret_cast<float(*)[PITCH]>(shared + PrepareShared<KP>::IMAGES);
-  float(*T)[PITCH] = A + Q;
-  float *G = reinterpret_cast<float *>(T + Q), *beta = G + Q;
+  float(*T)[PITCH] = reinterpret_cast<float(*)[PITCH]>(shared);
+  float *G = reinterpret_cast<float *>(A + Q), *beta = G + Q;
   const DeltaChunk ch = delta_chunk(p, blockIdx.x);
   const int head = blockIdx.y, hk = head / (p.H / p.Hg);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -110,6 +114,7 @@ __global__ void __launch_bounds__(PREP, 3) tc_prepare_kernel(DeltaBwdParams p) {
     }
   __syncthreads();
   keep<PREP>(w.P(), shared, 2 * Block<KP>::SQUARE);
+  __syncthreads();  // T takes their place
   if (tid < Q) {
     const int b = tid / 16 * 16, j = tid % 16;
     float x[16];
@@ -162,14 +167,14 @@ __global__ void __launch_bounds__(PREP, 3) tc_prepare_kernel(DeltaBwdParams p) {
     }
     __syncthreads();
   }
-  bf16 *Th = reinterpret_cast<bf16 *>(shared), *Tl = Th + Q * Q;
+  bf16 *Th = reinterpret_cast<bf16 *>(shared + PrepareShared<KP>::T_IMAGE), *Tl = Th + Q * Q;
   for (int i = tid; i < Q * Q / 2; i += PREP) {
     const int row = i / 32, col = i % 32 * 2;
     put_pair(Th, Tl, at<64>(row, col), row >= col ? T[row][col] : 0.f,
              row >= col + 1 ? T[row][col + 1] : 0.f);
   }
   __syncthreads();
-  keep<PREP>(w.T(), shared, Block<KP>::SQUARE);
+  keep<PREP>(w.T(), Th, Block<KP>::SQUARE);
 }
 
 template <int KP>

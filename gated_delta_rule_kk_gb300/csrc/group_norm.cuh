@@ -7,12 +7,14 @@
 // in the gradient, its sums over tokens in registers.  The next tokens' rows are on their way
 // while one is computed, and each tensor's place moves on by one addition.
 //
-// The floor is the rows' bytes, but at 16 channels a lane the instructions are what bounds it
-// (issue slots 70% full, DRAM 60%): hence arithmetic on two values an instruction and weights
-// in the rows' own type.  Forward with a gate, bf16: 2 x 4096 tokens of 16 heads of 128 take
-// 24.6 us (4.1 TB/s of 6.8), 32068 tokens of 8 groups of 512 take 122 us (4.3 TB/s); the
-// gradient of the first 51.4 us (3.3 TB/s).  With one token ahead, weights held in registers
-// and scalar arithmetic they took 28.7, 139.6 and 59.5 us.
+// The floor is the rows' bytes, but the instructions come close to it (issue slots 70% full):
+// hence arithmetic on two values an instruction, weights in the rows' own type, and kernels of
+// their own for groups that threads and pieces divide evenly, without checks of their ends.
+// bf16: 2 x 4096 tokens of 16 heads of 128 with a gate take 22 us (4.6 TB/s of 6.8), 32068
+// tokens of 8 groups of 512 98 us (5.3 TB/s; 119 with the checks); the gradient of the first
+// 47 us (3.6 TB/s), with 16 warps an SM, as a token's values take 128 registers.  With one
+// token ahead, scalar arithmetic and places worked out for every token they took 28.7, 139.6
+// and 59.5 us.
 #pragma once
 
 #include <type_traits>

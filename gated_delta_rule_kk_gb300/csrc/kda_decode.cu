@@ -12,6 +12,9 @@
 // chunk, which the scalar gate's kernel takes, would want the keys' products under every
 // channel's own decay: more work than the tokens themselves.)
 //
+// 256 requests of 32 heads of 128 x 128, bf16 states: 99 us (547 MB at 5.5 TB/s, 81% of the copy
+// rate); the ring's eight computing warps an SM issue on 69% of the cycles.
+//
 // What a head's rows share (decay, k, q of each token, v, beta, k . q) is formed once for an
 // item, a warp a token, into shared memory.
 #include <math.h>
