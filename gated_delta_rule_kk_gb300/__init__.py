@@ -1,6 +1,7 @@
 """Gated delta-rule (GDN / KDA) chunked forward and decode for GB300 (sm_103a),
-with the short causal convolution in front of such layers and the state space
-scan beside them.
+their gradient over chunks and KDA's tokens, with the short causal convolution in
+front of such layers, the norm with its gate behind them and the state space scan
+beside them.
 
 The arithmetic lives in the CUDA library built from ``csrc/`` (see
 ``build_lib.py``); this package holds its ctypes binding and the seeded

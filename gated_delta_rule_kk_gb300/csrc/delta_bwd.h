@@ -16,7 +16,7 @@
 //   dG_L += e^(G_L) <h, D> + sum k.dk_s,
 // where dq_h, dk_h and dk_s are the terms with h and D; dg is dG summed from the chunk's end.
 // (dA = -dr n^T holds as n solves (I + A) n = r: neither the gradient of T nor w = T beta e^G k
-// is formed.)  Four launches: T and P of every chunk; the states forward; their gradients
+// is formed.)  Four launches (five with packed sequences): T and P of every chunk; the states forward; their gradients
 // backward; everything else, every chunk by itself.
 #pragma once
 

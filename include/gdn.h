@@ -303,6 +303,9 @@ gdn_status_t gdn_chunk_host_workspace_size(const gdn_chunk_args *args, size_t *b
  *                                          written
  * A per-token gate may be anything up to -infinity (the state is forgotten: e^g is zero below
  * -104); a chunk-local sum has to be finite.
+ * A NaN or an infinity in v or do may reach every token of its chunk and, of its sequence,
+ * those that its state or the state's gradient reaches; other sequences and heads (but for dq
+ * and dk of its key head) are as without it.
  * With T == 0 the per-token arrays may be NULL (dh0 = dht, or zeros).  Outputs must not
  * overlap inputs.  A sum over heads, tokens or channels always runs in the same order, so
  * results do not change from run to run.
