@@ -23,17 +23,18 @@ norm_fwd_kernel(NormParams p) {
   const NormTeam<WHOLE> m(p);
   if (!bounds_ok(p.team * p.rows * p.span <= (int)blockDim.x, p.err)) return;
   int turn = 0;
-  NormCursor<T> xc(p, m, p.x, p.xs, p.xb, VEC), zc(p, m, p.z, p.zs, p.zb, VEC);
-  NormCursor<T> yc(p, m, p.y, p.ys, p.yb, VEC);
+  NormCursor<T, WHOLE> xc(p, m, p.x, p.xs, p.xb, VEC), zc(p, m, p.z, p.zs, p.zb, VEC);
+  NormCursor<T, WHOLE> yc(p, m, p.y, p.ys, p.yb, VEC);
   const NormWeights<T, VEC, PP, false> weight(p, m, p.weight), bias(p, m, p.bias);
   NormRow<T, VEC, PP> x[AHEAD], z[Z ? AHEAD : 1];
 #pragma unroll
   for (int i = 0; i < AHEAD; ++i) {
     x[i].zero();
-    x[i].load(p, m, xc, m.t + i * p.step);
+    const int t = m.t + i * p.step;
+    x[i].load(p, m, xc, t, m.has(p, t));
     if constexpr (Z) {
       z[i].zero();
-      z[i].load(p, m, zc, m.t + i * p.step);
+      z[i].load(p, m, zc, t, m.has(p, t));
     }
   }
   // every team of a block takes as many turns: the sums are the block's
@@ -52,8 +53,10 @@ norm_fwd_kernel(NormParams p) {
           if (p.gate_first) vmul<VEC>(u[j], u[j], gate[j]);
         }
       }
-      x[i].load(p, m, xc, t + AHEAD * p.step);
-      if constexpr (Z) z[i].load(p, m, zc, t + AHEAD * p.step);
+      const int later = t + AHEAD * p.step;
+      const bool more = m.has(p, later);
+      x[i].load(p, m, xc, later, more);
+      if constexpr (Z) z[i].load(p, m, zc, later, more);
       const float r = norm_root<VEC, PP>(p, m, u, buf, turn);
       NormRow<T, VEC, PP> y;
 #pragma unroll
@@ -76,7 +79,7 @@ norm_fwd_kernel(NormParams p) {
         }
         y.r[j].round(u[j]);
       }
-      y.store(p, m, yc, t);
+      y.store(p, m, yc, t, m.has(p, t));
     }
   }
 }
@@ -106,7 +109,7 @@ NormPlan norm_plan(NormParams &p, bool bf16, int vec, bool bwd) {
   const int64_t down = std::max<int64_t>(1, std::min(held, wanted));
   p.step = (int)down * p.rows;
   plan.blocks = (int)(down * p.blocks_per_row);
-  plan.whole = p.team * n == all && teams == p.rows * p.span && p.G % p.span == 0;
+  plan.whole = p.flat && p.team * n == all && teams == p.rows * p.span && p.G % p.span == 0;
   return plan;
 }
 

@@ -31,7 +31,7 @@ struct NormParams {
   int64_t gs, gb, xs, xb, zs, zb, ys, yb, ds, db;
   int tokens, T, G, W, D;     // all tokens, tokens of a batch row
   int shared, w_f32, center, gate_first, act;
-  int flat;                   // tokens of all batch rows one stride apart
+  int flat;                   // tokens of all batch rows lie one stride apart
   float eps;
   // teams: `team` threads each; `rows` tokens and `span` groups a block, blocks_per_row
   // blocks side by side over the groups; `step` tokens at once
@@ -39,7 +39,8 @@ struct NormParams {
 };
 
 // A team's place: its group, its first token, and whether it has any.  WHOLE: the teams fill
-// their blocks and the pieces their groups, so that only tokens end.
+// their blocks and the pieces their groups, so that only tokens end, and those of all batch
+// rows lie one stride apart.
 template <bool WHOLE>
 struct NormTeam {
   int lane, g, t, index;
@@ -51,6 +52,9 @@ struct NormTeam {
     g = blockIdx.x % p.blocks_per_row * p.span + index % p.span;
     t = blockIdx.x / p.blocks_per_row * p.rows + row;
     live = WHOLE || (row < p.rows && g < p.G);
+  }
+  __device__ __forceinline__ bool has(const NormParams &p, int token) const {
+    return live && token < p.tokens;
   }
   // whether this thread's piece `from` channels behind its first is one of the group's
   __device__ __forceinline__ bool in(const NormParams &p, int from, int vec) const {
@@ -243,21 +247,20 @@ struct NormWeights {
 };
 
 // A team's way through one tensor: where the next token's pieces of it are.  (A place is
-// worked out once where tokens lie one stride apart, then moved on.)
-template <typename T>
+// worked out once where tokens lie one stride apart, as WHOLE has them, then moved on.)
+template <typename T, bool WHOLE>
 struct NormCursor {
   T *at;
   int64_t stride, batch, move;
-  template <bool WHOLE>
-  __device__ __forceinline__ NormCursor(const NormParams &p, const NormTeam<WHOLE> &m, const void *base,
-                                        int64_t stride_, int64_t batch_, int vec)
+  __device__ __forceinline__ NormCursor(const NormParams &p, const NormTeam<WHOLE> &m,
+                                        const void *base, int64_t stride_, int64_t batch_, int vec)
       : stride(stride_), batch(batch_), move(p.step * stride_) {
     at = static_cast<T *>(const_cast<void *>(base)) + (int64_t)m.g * p.W + m.lane * vec;
-    if (p.flat) at += m.t * stride;
+    if (WHOLE || p.flat) at += m.t * stride;
   }
   // token t's place (of tokens taken in turn)
   __device__ __forceinline__ T *next(const NormParams &p, int t) {
-    if (p.flat) {
+    if (WHOLE || p.flat) {
       T *here = at;
       at += move;
       return here;
@@ -267,26 +270,25 @@ struct NormCursor {
   }
 };
 
-// A token's pieces of one tensor, as they lie in memory.
+// A token's pieces of one tensor, as they lie in memory; of token t where it is `there`.
 template <typename T, int VEC, int PP>
 struct NormRow {
   Row<T, VEC> r[PP];
   template <bool WHOLE>
-  __device__ __forceinline__ void load(const NormParams &p, const NormTeam<WHOLE> &m, NormCursor<T> &c, int t) {
+  __device__ __forceinline__ void load(const NormParams &p, const NormTeam<WHOLE> &m,
+                                       NormCursor<T, WHOLE> &c, int t, bool there) {
     const T *at = c.next(p, t);
-    if (!m.live || t >= p.tokens) return;
 #pragma unroll
     for (int j = 0; j < PP; ++j)
-      if (m.in(p, j * VEC * p.team, VEC)) r[j].load(at + j * VEC * p.team);
+      if (there && m.in(p, j * VEC * p.team, VEC)) r[j].load(at + j * VEC * p.team);
   }
   template <bool WHOLE>
-  __device__ __forceinline__ void store(const NormParams &p, const NormTeam<WHOLE> &m, NormCursor<T> &c,
-                                        int t) const {
+  __device__ __forceinline__ void store(const NormParams &p, const NormTeam<WHOLE> &m,
+                                        NormCursor<T, WHOLE> &c, int t, bool there) const {
     T *at = c.next(p, t);
-    if (!m.live || t >= p.tokens) return;
 #pragma unroll
     for (int j = 0; j < PP; ++j)
-      if (m.in(p, j * VEC * p.team, VEC)) r[j].store(at + j * VEC * p.team);
+      if (there && m.in(p, j * VEC * p.team, VEC)) r[j].store(at + j * VEC * p.team);
   }
   __device__ __forceinline__ void zero() {
 #pragma unroll

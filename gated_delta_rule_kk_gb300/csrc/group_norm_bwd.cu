@@ -25,9 +25,9 @@ norm_bwd_kernel(NormParams p) {
   constexpr bool Z = GATE != NO_GATE, BEFORE = GATE == GATE_BEFORE;
   constexpr int AHEAD = WIDE ? 1 : norm_bwd_ahead(norm_words(sizeof(T), VEC, PP));
   float dw[PP][VEC], db[PP][VEC];
-  NormCursor<T> gc(p, m, p.dy, p.gs, p.gb, VEC), xc(p, m, p.x, p.xs, p.xb, VEC);
-  NormCursor<T> zc(p, m, p.z, p.zs, p.zb, VEC), dxc(p, m, p.y, p.ys, p.yb, VEC);
-  NormCursor<T> dzc(p, m, p.dz, p.ds, p.db, VEC);
+  NormCursor<T, WHOLE> gc(p, m, p.dy, p.gs, p.gb, VEC), xc(p, m, p.x, p.xs, p.xb, VEC);
+  NormCursor<T, WHOLE> zc(p, m, p.z, p.zs, p.zb, VEC), dxc(p, m, p.y, p.ys, p.yb, VEC);
+  NormCursor<T, WHOLE> dzc(p, m, p.dz, p.ds, p.db, VEC);
   // (held where there is room: 51.3 -> 49.4 us; the forward gains nothing from it)
   const NormWeights<T, VEC, PP, PP * VEC <= 8> weight(p, m, p.weight), bias(p, m, p.bias);
   NormRow<T, VEC, PP> x[AHEAD], z[Z ? AHEAD : 1], g[AHEAD];
@@ -35,11 +35,12 @@ norm_bwd_kernel(NormParams p) {
   for (int i = 0; i < AHEAD; ++i) {
     x[i].zero();
     g[i].zero();
-    g[i].load(p, m, gc, m.t + i * p.step);
-    x[i].load(p, m, xc, m.t + i * p.step);
+    const int t = m.t + i * p.step;
+    g[i].load(p, m, gc, t, m.has(p, t));
+    x[i].load(p, m, xc, t, m.has(p, t));
     if constexpr (Z) {
       z[i].zero();
-      z[i].load(p, m, zc, m.t + i * p.step);
+      z[i].load(p, m, zc, t, m.has(p, t));
     }
   }
 #pragma unroll
@@ -51,7 +52,7 @@ norm_bwd_kernel(NormParams p) {
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i, t0 += p.step, t += p.step) {
       if (t0 >= p.tokens) break;
-      const bool there = m.live && t < p.tokens;
+      const bool there = m.has(p, t);
       float n[PP][VEC], d[PP][VEC], gate[BEFORE ? PP : 1][VEC], slope[BEFORE ? PP : 1][VEC];
       // (what is wanted behind the root's sums stays as it lies in memory till then)
       const NormRow<T, VEC, PP> x_raw = x[i], g_raw = g[i], z_raw = z[Z ? i : 0];
@@ -64,9 +65,11 @@ norm_bwd_kernel(NormParams p) {
           vmul<VEC>(n[j], n[j], gate[j]);
         }
       }
-      g[i].load(p, m, gc, t + AHEAD * p.step);
-      x[i].load(p, m, xc, t + AHEAD * p.step);
-      if constexpr (Z) z[i].load(p, m, zc, t + AHEAD * p.step);
+      const int later = t + AHEAD * p.step;
+      const bool more = m.has(p, later);
+      g[i].load(p, m, gc, later, more);
+      x[i].load(p, m, xc, later, more);
+      if constexpr (Z) z[i].load(p, m, zc, later, more);
       const float r = norm_root<VEC, PP>(p, m, n, buf, turn);
       float dots[2] = {0.f, 0.f}, total[2] = {0.f, 0.f};  // of dn n and of dn
       NormRow<T, VEC, PP> out;
@@ -109,9 +112,15 @@ norm_bwd_kernel(NormParams p) {
         vdot<VEC>(dots, d[j], n[j]);
         if (p.center) vsum<VEC>(total, d[j]);
       }
-      if constexpr (GATE == GATE_AFTER) out.store(p, m, dzc, t);
+      if constexpr (GATE == GATE_AFTER) out.store(p, m, dzc, t, there);
       float s[2] = {dots[0] + dots[1], total[0] + total[1]};
-      team_sum(s, p.team, buf, turn);
+      if (p.center) {
+        team_sum(s, p.team, buf, turn);
+      } else {
+        float one[1] = {s[0]};
+        team_sum(one, p.team, buf, turn);
+        s[0] = one[0];
+      }
       const float a = -s[0] * inv, mean = s[1] * inv;
       NormRow<T, VEC, PP> dx;
 #pragma unroll
@@ -129,8 +138,8 @@ norm_bwd_kernel(NormParams p) {
         }
         dx.r[j].round(d[j]);
       }
-      dx.store(p, m, dxc, t);
-      if constexpr (BEFORE) out.store(p, m, dzc, t);
+      dx.store(p, m, dxc, t, there);
+      if constexpr (BEFORE) out.store(p, m, dzc, t, there);
     }
   }
   if (p.part == nullptr) return;
