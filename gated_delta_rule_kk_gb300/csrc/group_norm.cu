@@ -109,7 +109,8 @@ NormPlan norm_plan(NormParams &p, bool bf16, int vec, bool bwd) {
   const int64_t down = std::max<int64_t>(1, std::min(held, wanted));
   p.step = (int)down * p.rows;
   plan.blocks = (int)(down * p.blocks_per_row);
-  plan.whole = p.flat && p.team * n == all && teams == p.rows * p.span && p.G % p.span == 0;
+  // (three pieces are taken by the kernel for four)
+  plan.whole = p.flat && n != 3 && p.team * n == all && teams == p.rows * p.span && p.G % p.span == 0;
   return plan;
 }
 

@@ -464,6 +464,36 @@ def test_norm(B, T, groups, width, dtype, gap, z, first, act, center, shared):
         assert_each_close(got[3], dz, "dz", 1e-2 if few else 3 * NORM)
 
 
+@pytest.mark.parametrize("width", [32, 64, 96, 128, 192, 256, 384, 512, 1024, 2048])
+@pytest.mark.parametrize("groups", [1, 4, 12])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_norm_of_even_groups(width, groups, dtype):
+    """Groups that teams and pieces divide, with as many groups as blocks have teams and other
+    numbers of them; then batch rows that lie further apart."""
+    i = norm_inputs(width + groups, 2, 70, groups, width, dtype, True)
+    d = cuda(i)
+    apart = {k: torch.zeros(3, 80, *d[k].shape[2:], dtype=dtype, device="cuda") for k in ("x", "z", "dy")}
+    for k, t in apart.items():
+        t[1:, 5:75] = d[k]
+        apart[k] = t[1:, 5:75]
+    for z, how in ((True, dict(center=False, activation="silu")),
+                   (True, dict(activation="sigmoid", gate_first=True)), (False, dict(activation="silu"))):
+        ref = L.group_norm(i["x"], groups, i["weight"], i["bias"], i["z"] if z else None, **how)
+        grads = L.group_norm_grad(i["dy"], i["x"], groups, i["weight"], i["bias"],
+                                  i["z"] if z else None, **how)
+        for t in (d, apart):
+            gate = t["z"] if z else None
+            y = gdn.group_norm_fwd(t["x"], groups, d["weight"], d["bias"], gate, **how)
+            got = gdn.group_norm_bwd(t["dy"], t["x"], groups, d["weight"], d["bias"], gate, **how)
+            ok()
+            assert_each_close(y, ref, "y", NORM)
+            assert_each_close(got[0], grads[0], "dx", 3 * NORM)
+            assert_each_close(got[1], grads[1].sum(0), "dw", NORM)
+            assert_each_close(got[2], grads[2].sum(0), "db", NORM)
+            if z:
+                assert_each_close(got[3], grads[3], "dz", 3 * NORM)
+
+
 def test_norm_without_weights_and_with_float32_ones():
     i = norm_inputs(1, 2, 5, 4, 32, BF16, weight=False, bias=False, z=False)
     d = cuda(i)
