@@ -13,18 +13,18 @@
 namespace gdn {
 namespace {
 
-template <typename T, int VEC, int PP, bool Z, bool WHOLE, bool WIDE>
+template <typename T, int VEC, int PP, bool Z, int TEAM, bool WIDE>
 __global__ void __launch_bounds__(
     norm_block(PP * VEC, WIDE),
     WIDE ? 1 : norm_fwd_per_sm(PP * VEC, norm_words(sizeof(T), VEC, PP), Z))
 norm_fwd_kernel(NormParams p) {
   constexpr int AHEAD = WIDE ? 1 : norm_fwd_ahead(norm_words(sizeof(T), VEC, PP), Z);
   __shared__ float buf[2][NORM_WARPS][2];
-  const NormTeam<WHOLE> m(p);
+  const NormTeam<TEAM> m(p);
   if (!bounds_ok(p.team * p.rows * p.span <= (int)blockDim.x, p.err)) return;
   int turn = 0;
-  NormCursor<T, WHOLE> xc(p, m, p.x, p.xs, p.xb, VEC), zc(p, m, p.z, p.zs, p.zb, VEC);
-  NormCursor<T, WHOLE> yc(p, m, p.y, p.ys, p.yb, VEC);
+  NormCursor<T, TEAM> xc(p, m, p.x, p.xs, p.xb, VEC), zc(p, m, p.z, p.zs, p.zb, VEC);
+  NormCursor<T, TEAM> yc(p, m, p.y, p.ys, p.yb, VEC);
   const NormWeights<T, VEC, PP, false> weight(p, m, p.weight), bias(p, m, p.bias);
   NormRow<T, VEC, PP> x[AHEAD], z[Z ? AHEAD : 1];
 #pragma unroll
@@ -96,7 +96,7 @@ NormPlan norm_plan(NormParams &p, bool bf16, int vec, bool bwd) {
   while (n < most && (all + n - 1) / n > 32) n += n < 4 ? n : 2;
   p.team = 1;
   while (p.team * n < all) p.team *= 2;
-  NormPlan plan{vec, n, std::max(NORM_THREADS, p.team), 0, false};
+  NormPlan plan{vec, n, std::max(NORM_THREADS, p.team), 0, 0};
   const int per_sm = bwd ? norm_bwd_per_sm(vec * n)
                          : norm_fwd_per_sm(vec * n, norm_words(bf16 ? 2 : 4, vec, n), p.z != nullptr);
   const int teams = plan.threads / p.team;
@@ -110,7 +110,9 @@ NormPlan norm_plan(NormParams &p, bool bf16, int vec, bool bwd) {
   p.step = (int)down * p.rows;
   plan.blocks = (int)(down * p.blocks_per_row);
   // (three pieces are taken by the kernel for four)
-  plan.whole = p.flat && n != 3 && p.team * n == all && teams == p.rows * p.span && p.G % p.span == 0;
+  const bool even = p.flat && n != 3 && p.team * n == all && teams == p.rows * p.span && p.G % p.span == 0;
+  const bool made = p.team == 32 || (n == 1 && (p.team == 8 || p.team == 16));
+  plan.team = even && made && vec * (bf16 ? 2 : 4) == 16 ? p.team : 0;
   return plan;
 }
 
@@ -229,15 +231,16 @@ size_t bwd_workspace(const group_norm_bwd_args &a, const NormParams &p, const No
 }  // namespace
 
 cudaError_t launch_norm_fwd(const NormParams &p, bool bf16, const NormPlan &plan, cudaStream_t stream) {
-  return norm_forms(bf16, plan, p, [&](auto t, auto v, auto n, auto gate, auto whole) {
+  return norm_forms(bf16, plan, p, [&](auto t, auto v, auto n, auto gate, auto team) {
     using T = decltype(t);
     constexpr int VEC = decltype(v)::value, PP = decltype(n)::value;
-    constexpr bool Z = decltype(gate)::value != NO_GATE, WHOLE = decltype(whole)::value;
+    constexpr bool Z = decltype(gate)::value != NO_GATE;
+    constexpr int TEAM = decltype(team)::value;
     if (plan.threads <= NORM_THREADS) {
-      norm_fwd_kernel<T, VEC, PP, Z, WHOLE, false><<<plan.blocks, plan.threads, 0, stream>>>(p);
+      norm_fwd_kernel<T, VEC, PP, Z, TEAM, false><<<plan.blocks, plan.threads, 0, stream>>>(p);
     } else {  // only with the most pieces a thread
       if constexpr (PP == norm_pieces(VEC))
-        norm_fwd_kernel<T, VEC, PP, Z, WHOLE, true><<<plan.blocks, plan.threads, 0, stream>>>(p);
+        norm_fwd_kernel<T, VEC, PP, Z, 0, true><<<plan.blocks, plan.threads, 0, stream>>>(p);
       else
         return cudaErrorInvalidConfiguration;
     }

@@ -9,10 +9,11 @@
 //
 // The floor is the rows' bytes, but the instructions come close to it (issue slots 70% full):
 // hence arithmetic on two values an instruction, weights in the rows' own type, and kernels of
-// their own for groups that threads and pieces divide evenly, without checks of their ends.
-// bf16: 2 x 4096 tokens of 16 heads of 128 with a gate take 22 us (4.6 TB/s of 6.8), 32068
-// tokens of 8 groups of 512 98 us (5.3 TB/s; 119 with the checks); the gradient of the first
-// 47 us (3.6 TB/s), with 16 warps an SM, as a token's values take 128 registers.  With one
+// their own for groups that threads and pieces divide evenly, without checks of their ends and
+// with the team's size known.  bf16: 2 x 4096 tokens of 16 heads of 128 with a gate take 20 us
+// (5.0 TB/s of 6.8), 32068 tokens of 8 groups of 512 90 us (5.9 TB/s; 119 in the kernel for
+// any group); the gradient of the first 43 us (3.9 TB/s), with 16 warps an SM, as a token's
+// values take 128 registers.  With one
 // token ahead, scalar arithmetic and places worked out for every token they took 28.7, 139.6
 // and 59.5 us.
 #pragma once
@@ -38,27 +39,28 @@ struct NormParams {
   int team, rows, span, blocks_per_row, step;
 };
 
-// A team's place: its group, its first token, and whether it has any.  WHOLE: the teams fill
-// their blocks and the pieces their groups, so that only tokens end, and those of all batch
-// rows lie one stride apart.
-template <bool WHOLE>
+// A team's place: its group, its first token, and whether it has any.  With TEAM (threads, else
+// 0) all comes out even: the teams fill their blocks and the pieces their groups, so that only
+// tokens end, and those of all batch rows lie one stride apart.
+template <int TEAM>
 struct NormTeam {
   int lane, g, t, index;
   bool live;
+  static __device__ __forceinline__ int team(const NormParams &p) { return TEAM ? TEAM : p.team; }
   __device__ __forceinline__ explicit NormTeam(const NormParams &p) {
-    lane = threadIdx.x & (p.team - 1);
-    index = threadIdx.x / p.team;
+    lane = threadIdx.x & (team(p) - 1);
+    index = threadIdx.x / team(p);
     const int row = index / p.span;
     g = blockIdx.x % p.blocks_per_row * p.span + index % p.span;
     t = blockIdx.x / p.blocks_per_row * p.rows + row;
-    live = WHOLE || (row < p.rows && g < p.G);
+    live = TEAM || (row < p.rows && g < p.G);
   }
   __device__ __forceinline__ bool has(const NormParams &p, int token) const {
     return live && token < p.tokens;
   }
   // whether this thread's piece `from` channels behind its first is one of the group's
   __device__ __forceinline__ bool in(const NormParams &p, int from, int vec) const {
-    return WHOLE || lane * vec + from < p.W;
+    return TEAM || lane * vec + from < p.W;
   }
 };
 
@@ -180,14 +182,17 @@ __device__ __forceinline__ void norm_act(int act, const float *z, float *out, fl
     }
     return;
   }
-  float s[VEC], rest[VEC];
+  float s[VEC];
   if constexpr (VEC == 1)
     s[0] = __fdividef(1.f, 1.f + __expf(-z[0]));
   else
     sigmoid_row<VEC>(s, z);
-  if constexpr (SLOPE) {
+  [[maybe_unused]] float rest[VEC];
+  if constexpr (SLOPE) {  // 1 - s
+    float less[VEC], one[VEC];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) rest[e] = 1.f - s[e];
+    for (int e = 0; e < VEC; ++e) less[e] = -1.f, one[e] = 1.f;
+    vfma<VEC>(rest, s, less, one);
   }
   if (act == GDN_ACT_SILU) {
     vmul<VEC>(out, z, s);
@@ -206,25 +211,25 @@ struct NormWeights {
   const unsigned char *at;  // NULL: none
   int step;                 // bytes from piece to piece
   Row<T, VEC> kept[KEEP ? PP : 1];
-  template <bool WHOLE>
-  __device__ __forceinline__ NormWeights(const NormParams &p, const NormTeam<WHOLE> &m, const void *from) {
+  template <int TEAM>
+  __device__ __forceinline__ NormWeights(const NormParams &p, const NormTeam<TEAM> &m, const void *from) {
     const int size = p.w_f32 ? 4 : (int)sizeof(T);
     at = static_cast<const unsigned char *>(from);
     if (at != nullptr) at += ((p.shared ? 0 : (int64_t)m.g * p.W) + m.lane * VEC) * size;
-    step = VEC * p.team * size;
+    step = VEC * m.team(p) * size;
     if constexpr (KEEP) {
 #pragma unroll
       for (int j = 0; j < PP; ++j) {
         kept[j].zero();
-        if (at != nullptr && !p.w_f32 && m.live && m.in(p, j * VEC * p.team, VEC))
+        if (at != nullptr && !p.w_f32 && m.live && m.in(p, j * VEC * m.team(p), VEC))
           kept[j].load(reinterpret_cast<const T *>(at + j * step));
       }
     }
   }
-  template <bool WHOLE>
-  __device__ __forceinline__ void get(const NormParams &p, const NormTeam<WHOLE> &m, int piece, float *w) const {
+  template <int TEAM>
+  __device__ __forceinline__ void get(const NormParams &p, const NormTeam<TEAM> &m, int piece, float *w) const {
     if (KEEP && !p.w_f32) return kept[KEEP ? piece : 0].widen(w);
-    if (!m.live || !m.in(p, piece * VEC * p.team, VEC)) {
+    if (!m.live || !m.in(p, piece * VEC * m.team(p), VEC)) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) w[e] = 0.f;
       return;
@@ -247,20 +252,20 @@ struct NormWeights {
 };
 
 // A team's way through one tensor: where the next token's pieces of it are.  (A place is
-// worked out once where tokens lie one stride apart, as WHOLE has them, then moved on.)
-template <typename T, bool WHOLE>
+// worked out once where tokens lie one stride apart, as with TEAM, then moved on.)
+template <typename T, int TEAM>
 struct NormCursor {
   T *at;
   int64_t stride, batch, move;
-  __device__ __forceinline__ NormCursor(const NormParams &p, const NormTeam<WHOLE> &m,
+  __device__ __forceinline__ NormCursor(const NormParams &p, const NormTeam<TEAM> &m,
                                         const void *base, int64_t stride_, int64_t batch_, int vec)
       : stride(stride_), batch(batch_), move(p.step * stride_) {
     at = static_cast<T *>(const_cast<void *>(base)) + (int64_t)m.g * p.W + m.lane * vec;
-    if (WHOLE || p.flat) at += m.t * stride;
+    if (TEAM || p.flat) at += m.t * stride;
   }
   // token t's place (of tokens taken in turn)
   __device__ __forceinline__ T *next(const NormParams &p, int t) {
-    if (WHOLE || p.flat) {
+    if (TEAM || p.flat) {
       T *here = at;
       at += move;
       return here;
@@ -274,21 +279,21 @@ struct NormCursor {
 template <typename T, int VEC, int PP>
 struct NormRow {
   Row<T, VEC> r[PP];
-  template <bool WHOLE>
-  __device__ __forceinline__ void load(const NormParams &p, const NormTeam<WHOLE> &m,
-                                       NormCursor<T, WHOLE> &c, int t, bool there) {
+  template <int TEAM>
+  __device__ __forceinline__ void load(const NormParams &p, const NormTeam<TEAM> &m,
+                                       NormCursor<T, TEAM> &c, int t, bool there) {
     const T *at = c.next(p, t);
 #pragma unroll
     for (int j = 0; j < PP; ++j)
-      if (there && m.in(p, j * VEC * p.team, VEC)) r[j].load(at + j * VEC * p.team);
+      if (there && m.in(p, j * VEC * m.team(p), VEC)) r[j].load(at + j * VEC * m.team(p));
   }
-  template <bool WHOLE>
-  __device__ __forceinline__ void store(const NormParams &p, const NormTeam<WHOLE> &m,
-                                        NormCursor<T, WHOLE> &c, int t, bool there) const {
+  template <int TEAM>
+  __device__ __forceinline__ void store(const NormParams &p, const NormTeam<TEAM> &m,
+                                        NormCursor<T, TEAM> &c, int t, bool there) const {
     T *at = c.next(p, t);
 #pragma unroll
     for (int j = 0; j < PP; ++j)
-      if (there && m.in(p, j * VEC * p.team, VEC)) r[j].store(at + j * VEC * p.team);
+      if (there && m.in(p, j * VEC * m.team(p), VEC)) r[j].store(at + j * VEC * m.team(p));
   }
   __device__ __forceinline__ void zero() {
 #pragma unroll
@@ -298,8 +303,8 @@ struct NormRow {
 
 // Takes u's mean off (where wanted) and returns 1 / root.  Pieces past the group hold zero and
 // stay so.
-template <int VEC, int PP, bool WHOLE>
-__device__ __forceinline__ float norm_root(const NormParams &p, const NormTeam<WHOLE> &m,
+template <int VEC, int PP, int TEAM>
+__device__ __forceinline__ float norm_root(const NormParams &p, const NormTeam<TEAM> &m,
                                            float (&u)[PP][VEC], float (*buf)[NORM_WARPS][2],
                                            int &turn) {
   const float inv = 1.f / (float)p.W;
@@ -309,25 +314,24 @@ __device__ __forceinline__ float norm_root(const NormParams &p, const NormTeam<W
 #pragma unroll
     for (int j = 0; j < PP; ++j) vsum<VEC>(s, u[j]);
     v[0] = s[0] + s[1];
-    team_sum(v, p.team, buf, turn);
+    team_sum(v, m.team(p), buf, turn);
     const float mean = v[0] * inv;
 #pragma unroll
     for (int j = 0; j < PP; ++j)
-      if (m.in(p, j * VEC * p.team, VEC)) vsub<VEC>(u[j], u[j], mean);
+      if (m.in(p, j * VEC * m.team(p), VEC)) vsub<VEC>(u[j], u[j], mean);
   }
   float s[2] = {0.f, 0.f};
 #pragma unroll
   for (int j = 0; j < PP; ++j) vdot<VEC>(s, u[j], u[j]);
   v[0] = s[0] + s[1];
-  team_sum(v, p.team, buf, turn);
+  team_sum(v, m.team(p), buf, turn);
   return rsqrtf(fmaf(v[0], inv, p.eps));
 }
 
-// How a call is shared out: channels a piece, pieces a thread, threads a block, blocks, and
-// whether teams and pieces come out even.
+// How a call is shared out: channels a piece, pieces a thread, threads a block, blocks, and a
+// team's threads where all comes out even and a kernel is made for as many (else 0).
 struct NormPlan {
-  int vec, pieces, threads, blocks;
-  bool whole;
+  int vec, pieces, threads, blocks, team;
 };
 cudaError_t launch_norm_fwd(const NormParams &p, bool bf16, const NormPlan &plan, cudaStream_t stream);
 cudaError_t launch_norm_bwd(const NormParams &p, bool bf16, const NormPlan &plan, cudaStream_t stream);
@@ -338,39 +342,48 @@ cudaError_t launch_norm_sums(const float *part, int rows, int columns, float *dw
 // Where z stands.
 enum NormGate { NO_GATE, GATE_AFTER, GATE_BEFORE };
 
-// Calls f with the element type, VEC, PP, the gate and whether all comes out even (looked at for
-// pieces of 16 bytes only) as compile-time values.
+// Calls f with the element type, VEC, PP, the gate and TEAM as compile-time values.  TEAM is for
+// pieces of 16 bytes, teams of 8 to 32 threads (groups of 64 channels and more in bfloat16),
+// of 32 where a thread takes several pieces.
 template <typename F>
 cudaError_t norm_forms(bool bf16, const NormPlan &plan, const NormParams &p, F &&f) {
-  auto gate = [&](auto t, auto v, auto n, auto whole) {
-    if (p.z == nullptr) return f(t, v, n, std::integral_constant<NormGate, NO_GATE>(), whole);
-    if (p.gate_first) return f(t, v, n, std::integral_constant<NormGate, GATE_BEFORE>(), whole);
-    return f(t, v, n, std::integral_constant<NormGate, GATE_AFTER>(), whole);
+  auto gate = [&](auto t, auto v, auto n, auto team) {
+    if (p.z == nullptr) return f(t, v, n, std::integral_constant<NormGate, NO_GATE>(), team);
+    if (p.gate_first) return f(t, v, n, std::integral_constant<NormGate, GATE_BEFORE>(), team);
+    return f(t, v, n, std::integral_constant<NormGate, GATE_AFTER>(), team);
   };
+  const std::integral_constant<int, 0> any;
   const int pieces = plan.pieces;
-  auto few = [&](auto t, auto v, auto whole) {  // PP of 1, 2 (and 4 for four channels a piece)
-    if (pieces == 1) return gate(t, v, std::integral_constant<int, 1>(), whole);
+  auto one = [&](auto t, auto v) {
+    const std::integral_constant<int, 1> n;
+    if (plan.team == 8) return gate(t, v, n, std::integral_constant<int, 8>());
+    if (plan.team == 16) return gate(t, v, n, std::integral_constant<int, 16>());
+    if (plan.team == 32) return gate(t, v, n, std::integral_constant<int, 32>());
+    return gate(t, v, n, any);
+  };
+  auto several = [&](auto t, auto v, auto n) {
+    if (plan.team == 32) return gate(t, v, n, std::integral_constant<int, 32>());
+    return gate(t, v, n, any);
+  };
+  auto few = [&](auto t, auto v) {  // PP of 1, 2 (and 4 for four channels a piece)
+    if (pieces == 1) return one(t, v);
     if (decltype(v)::value == 8 || pieces == 2)
-      return gate(t, v, std::integral_constant<int, 2>(), whole);
-    return gate(t, v, std::integral_constant<int, decltype(v)::value == 8 ? 2 : 4>(), whole);
+      return several(t, v, std::integral_constant<int, 2>());
+    return several(t, v, std::integral_constant<int, decltype(v)::value == 8 ? 2 : 4>());
   };
   auto many = [&](auto t, auto v) {
-    const std::false_type whole;
-    if (pieces == 1) return gate(t, v, std::integral_constant<int, 1>(), whole);
-    if (pieces == 2) return gate(t, v, std::integral_constant<int, 2>(), whole);
-    if (pieces == 4) return gate(t, v, std::integral_constant<int, 4>(), whole);
-    if (pieces == 6) return gate(t, v, std::integral_constant<int, 6>(), whole);
-    return gate(t, v, std::integral_constant<int, 8>(), whole);
-  };
-  auto both = [&](auto t, auto v) {
-    return plan.whole ? few(t, v, std::true_type()) : few(t, v, std::false_type());
+    if (pieces == 1) return gate(t, v, std::integral_constant<int, 1>(), any);
+    if (pieces == 2) return gate(t, v, std::integral_constant<int, 2>(), any);
+    if (pieces == 4) return gate(t, v, std::integral_constant<int, 4>(), any);
+    if (pieces == 6) return gate(t, v, std::integral_constant<int, 6>(), any);
+    return gate(t, v, std::integral_constant<int, 8>(), any);
   };
   if (bf16) {
-    if (plan.vec == 8) return both(__nv_bfloat16(), std::integral_constant<int, 8>());
+    if (plan.vec == 8) return few(__nv_bfloat16(), std::integral_constant<int, 8>());
     if (plan.vec == 2) return many(__nv_bfloat16(), std::integral_constant<int, 2>());
     return many(__nv_bfloat16(), std::integral_constant<int, 1>());
   }
-  if (plan.vec == 4) return both(0.f, std::integral_constant<int, 4>());
+  if (plan.vec == 4) return few(0.f, std::integral_constant<int, 4>());
   return many(0.f, std::integral_constant<int, 1>());
 }
 

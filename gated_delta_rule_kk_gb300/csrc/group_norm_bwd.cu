@@ -13,21 +13,21 @@
 namespace gdn {
 namespace {
 
-template <typename T, int VEC, int PP, NormGate GATE, bool WHOLE, bool WIDE>
+template <typename T, int VEC, int PP, NormGate GATE, int TEAM, bool WIDE>
 __global__ void __launch_bounds__(norm_block(PP * VEC, WIDE), WIDE ? 1 : norm_bwd_per_sm(PP * VEC))
 norm_bwd_kernel(NormParams p) {
   __shared__ float buf[2][NORM_WARPS][2];
   extern __shared__ float sums[];  // [threads][PP * VEC]
-  const NormTeam<WHOLE> m(p);
+  const NormTeam<TEAM> m(p);
   if (!bounds_ok(p.team * p.rows * p.span <= (int)blockDim.x, p.err)) return;
   int turn = 0;
   const float inv = 1.f / (float)p.W;
   constexpr bool Z = GATE != NO_GATE, BEFORE = GATE == GATE_BEFORE;
   constexpr int AHEAD = WIDE ? 1 : norm_bwd_ahead(norm_words(sizeof(T), VEC, PP));
   float dw[PP][VEC], db[PP][VEC];
-  NormCursor<T, WHOLE> gc(p, m, p.dy, p.gs, p.gb, VEC), xc(p, m, p.x, p.xs, p.xb, VEC);
-  NormCursor<T, WHOLE> zc(p, m, p.z, p.zs, p.zb, VEC), dxc(p, m, p.y, p.ys, p.yb, VEC);
-  NormCursor<T, WHOLE> dzc(p, m, p.dz, p.ds, p.db, VEC);
+  NormCursor<T, TEAM> gc(p, m, p.dy, p.gs, p.gb, VEC), xc(p, m, p.x, p.xs, p.xb, VEC);
+  NormCursor<T, TEAM> zc(p, m, p.z, p.zs, p.zb, VEC), dxc(p, m, p.y, p.ys, p.yb, VEC);
+  NormCursor<T, TEAM> dzc(p, m, p.dz, p.ds, p.db, VEC);
   // (held where there is room: 51.3 -> 49.4 us; the forward gains nothing from it)
   const NormWeights<T, VEC, PP, PP * VEC <= 8> weight(p, m, p.weight), bias(p, m, p.bias);
   NormRow<T, VEC, PP> x[AHEAD], z[Z ? AHEAD : 1], g[AHEAD];
@@ -115,10 +115,10 @@ norm_bwd_kernel(NormParams p) {
       if constexpr (GATE == GATE_AFTER) out.store(p, m, dzc, t, there);
       float s[2] = {dots[0] + dots[1], total[0] + total[1]};
       if (p.center) {
-        team_sum(s, p.team, buf, turn);
+        team_sum(s, m.team(p), buf, turn);
       } else {
         float one[1] = {s[0]};
-        team_sum(one, p.team, buf, turn);
+        team_sum(one, m.team(p), buf, turn);
         s[0] = one[0];
       }
       const float a = -s[0] * inv, mean = s[1] * inv;
@@ -144,7 +144,7 @@ norm_bwd_kernel(NormParams p) {
   }
   if (p.part == nullptr) return;
   // a column's sums over the block's teams that hold it, in their order
-  const int teams = p.rows * p.span, each = p.team * PP * VEC;
+  const int teams = p.rows * p.span, each = m.team(p) * PP * VEC;
   const int columns = p.shared ? p.W : p.D;
   const int groups = p.shared ? 1 : p.span, g0 = blockIdx.x % p.blocks_per_row * p.span;
   float *part = p.part +
@@ -157,7 +157,7 @@ norm_bwd_kernel(NormParams p) {
       for (int j = 0; j < PP; ++j)
 #pragma unroll
         for (int e = 0; e < VEC; ++e)
-          sums[m.index * each + (m.lane + j * p.team) * VEC + e] = which ? db[j][e] : dw[j][e];
+          sums[m.index * each + (m.lane + j * m.team(p)) * VEC + e] = which ? db[j][e] : dw[j][e];
     __syncthreads();
     for (int i = threadIdx.x; i < groups * p.W; i += blockDim.x) {
       const int q = i / p.W, c = i - q * p.W;
@@ -200,16 +200,16 @@ __global__ void __launch_bounds__(1024) norm_sums_kernel(const float *part, int 
 
 cudaError_t launch_norm_bwd(const NormParams &p, bool bf16, const NormPlan &plan, cudaStream_t stream) {
   const int smem = p.part ? plan.threads * plan.pieces * plan.vec * (int)sizeof(float) : 0;
-  return norm_forms(bf16, plan, p, [&](auto t, auto v, auto n, auto gate, auto whole) {
+  return norm_forms(bf16, plan, p, [&](auto t, auto v, auto n, auto gate, auto team) {
     using T = decltype(t);
     constexpr int VEC = decltype(v)::value, PP = decltype(n)::value;
     constexpr NormGate GATE = decltype(gate)::value;
-    constexpr bool WHOLE = decltype(whole)::value;
+    constexpr int TEAM = decltype(team)::value;
     if (plan.threads <= NORM_THREADS) {
-      norm_bwd_kernel<T, VEC, PP, GATE, WHOLE, false><<<plan.blocks, plan.threads, smem, stream>>>(p);
+      norm_bwd_kernel<T, VEC, PP, GATE, TEAM, false><<<plan.blocks, plan.threads, smem, stream>>>(p);
     } else {  // only with the most pieces a thread
       if constexpr (PP == norm_pieces(VEC))
-        norm_bwd_kernel<T, VEC, PP, GATE, WHOLE, true><<<plan.blocks, plan.threads, smem, stream>>>(p);
+        norm_bwd_kernel<T, VEC, PP, GATE, 0, true><<<plan.blocks, plan.threads, smem, stream>>>(p);
       else
         return cudaErrorInvalidConfiguration;
     }
