@@ -12,7 +12,7 @@
 // their own for groups that threads and pieces divide evenly, without checks of their ends and
 // with the team's size known.  bf16: 2 x 4096 tokens of 16 heads of 128 with a gate take 20 us
 // (5.0 TB/s of 6.8), 32068 tokens of 8 groups of 512 90 us (5.9 TB/s; 119 in the kernel for
-// any group); the gradient of the first 43 us (3.9 TB/s), with 16 warps an SM, as a token's
+// any group); the gradient of the first 41 us (4.1 TB/s), with 16 warps an SM, as a token's
 // values take 128 registers.  With one
 // token ahead, scalar arithmetic and places worked out for every token they took 28.7, 139.6
 // and 59.5 us.

@@ -48,99 +48,101 @@ norm_bwd_kernel(NormParams p) {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) dw[j][e] = db[j][e] = 0.f;
   const int first = blockIdx.x / p.blocks_per_row * p.rows;
-  for (int t0 = first, t = m.t; t0 < p.tokens;) {
+  for (int t0 = first, t = m.t; t0 < p.tokens; t0 += p.step, t += p.step) {
+    const bool there = m.has(p, t);
+    float n[PP][VEC], d[PP][VEC], gate[BEFORE ? PP : 1][VEC], slope[BEFORE ? PP : 1][VEC];
+    // (what is wanted behind the root's sums stays as it lies in memory till then)
+    const NormRow<T, VEC, PP> x_raw = x[0], g_raw = g[0], z_raw = z[0];
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i, t0 += p.step, t += p.step) {
-      if (t0 >= p.tokens) break;
-      const bool there = m.has(p, t);
-      float n[PP][VEC], d[PP][VEC], gate[BEFORE ? PP : 1][VEC], slope[BEFORE ? PP : 1][VEC];
-      // (what is wanted behind the root's sums stays as it lies in memory till then)
-      const NormRow<T, VEC, PP> x_raw = x[i], g_raw = g[i], z_raw = z[Z ? i : 0];
-#pragma unroll
-      for (int j = 0; j < PP; ++j) {
-        x_raw.r[j].widen(n[j]);
-        if constexpr (BEFORE) {
-          z_raw.r[j].widen(gate[j]);
-          norm_act<VEC, true>(p.act, gate[j], gate[j], slope[j]);
-          vmul<VEC>(n[j], n[j], gate[j]);
-        }
-      }
-      const int later = t + AHEAD * p.step;
-      const bool more = m.has(p, later);
-      g[i].load(p, m, gc, later, more);
-      x[i].load(p, m, xc, later, more);
-      if constexpr (Z) z[i].load(p, m, zc, later, more);
-      const float r = norm_root<VEC, PP>(p, m, n, buf, turn);
-      float dots[2] = {0.f, 0.f}, total[2] = {0.f, 0.f};  // of dn n and of dn
-      NormRow<T, VEC, PP> out;
-#pragma unroll
-      for (int j = 0; j < PP; ++j) {
-        vmul<VEC>(n[j], n[j], r);
-        g_raw.r[j].widen(d[j]);
-        float w[VEC], v[VEC];
-        if (p.weight != nullptr) weight.get(p, m, j, w);
-        if (GATE == GATE_AFTER || (!Z && p.act != GDN_ACT_NONE)) {  // m
-          if (p.weight != nullptr) {
-            vmul<VEC>(v, n[j], w);
-          } else {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) v[e] = n[j][e];
-          }
-          if (p.bias != nullptr) {
-            float b[VEC];
-            bias.get(p, m, j, b);
-            vadd<VEC>(v, v, b);
-          }
-          float by[VEC], gv[VEC];
-          if constexpr (Z) {
-            z_raw.r[j].widen(gv);
-            norm_act<VEC, true>(p.act, gv, gv, by);
-            vmul<VEC>(v, v, d[j]);
-            vmul<VEC>(v, v, by);
-            out.r[j].round(v);
-            vmul<VEC>(d[j], d[j], gv);
-          } else {
-            norm_act<VEC, true>(p.act, v, v, by);
-            vmul<VEC>(d[j], d[j], by);
-          }
-        }
-        if (there) {
-          vfma<VEC>(dw[j], d[j], n[j], dw[j]);
-          vadd<VEC>(db[j], db[j], d[j]);
-        }
-        if (p.weight != nullptr) vmul<VEC>(d[j], d[j], w);
-        vdot<VEC>(dots, d[j], n[j]);
-        if (p.center) vsum<VEC>(total, d[j]);
-      }
-      if constexpr (GATE == GATE_AFTER) out.store(p, m, dzc, t, there);
-      float s[2] = {dots[0] + dots[1], total[0] + total[1]};
-      if (p.center) {
-        team_sum(s, m.team(p), buf, turn);
-      } else {
-        float one[1] = {s[0]};
-        team_sum(one, m.team(p), buf, turn);
-        s[0] = one[0];
-      }
-      const float a = -s[0] * inv, mean = s[1] * inv;
-      NormRow<T, VEC, PP> dx;
-#pragma unroll
-      for (int j = 0; j < PP; ++j) {
-        vfma<VEC>(d[j], n[j], a, d[j]);
-        if (p.center) vsub<VEC>(d[j], d[j], mean);
-        vmul<VEC>(d[j], d[j], r);
-        if constexpr (BEFORE) {
-          float u[VEC];
-          x_raw.r[j].widen(u);
-          vmul<VEC>(u, u, d[j]);
-          vmul<VEC>(u, u, slope[j]);
-          out.r[j].round(u);
-          vmul<VEC>(d[j], d[j], gate[j]);
-        }
-        dx.r[j].round(d[j]);
-      }
-      dx.store(p, m, dxc, t, there);
-      if constexpr (BEFORE) out.store(p, m, dzc, t, there);
+    for (int i = 1; i < AHEAD; ++i) {
+      x[i - 1] = x[i];
+      g[i - 1] = g[i];
+      if constexpr (Z) z[i - 1] = z[i];
     }
+#pragma unroll
+    for (int j = 0; j < PP; ++j) {
+      x_raw.r[j].widen(n[j]);
+      if constexpr (BEFORE) {
+        z_raw.r[j].widen(gate[j]);
+        norm_act<VEC, true>(p.act, gate[j], gate[j], slope[j]);
+        vmul<VEC>(n[j], n[j], gate[j]);
+      }
+    }
+    const int later = t + AHEAD * p.step;
+    const bool more = m.has(p, later);
+    g[AHEAD - 1].load(p, m, gc, later, more);
+    x[AHEAD - 1].load(p, m, xc, later, more);
+    if constexpr (Z) z[AHEAD - 1].load(p, m, zc, later, more);
+    const float r = norm_root<VEC, PP>(p, m, n, buf, turn);
+    float dots[2] = {0.f, 0.f}, total[2] = {0.f, 0.f};  // of dn n and of dn
+    NormRow<T, VEC, PP> out;
+#pragma unroll
+    for (int j = 0; j < PP; ++j) {
+      vmul<VEC>(n[j], n[j], r);
+      g_raw.r[j].widen(d[j]);
+      float w[VEC], v[VEC];
+      if (p.weight != nullptr) weight.get(p, m, j, w);
+      if (GATE == GATE_AFTER || (!Z && p.act != GDN_ACT_NONE)) {  // m
+        if (p.weight != nullptr) {
+          vmul<VEC>(v, n[j], w);
+        } else {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) v[e] = n[j][e];
+        }
+        if (p.bias != nullptr) {
+          float b[VEC];
+          bias.get(p, m, j, b);
+          vadd<VEC>(v, v, b);
+        }
+        float by[VEC], gv[VEC];
+        if constexpr (Z) {
+          z_raw.r[j].widen(gv);
+          norm_act<VEC, true>(p.act, gv, gv, by);
+          vmul<VEC>(v, v, d[j]);
+          vmul<VEC>(v, v, by);
+          out.r[j].round(v);
+          vmul<VEC>(d[j], d[j], gv);
+        } else {
+          norm_act<VEC, true>(p.act, v, v, by);
+          vmul<VEC>(d[j], d[j], by);
+        }
+      }
+      if (there) {
+        vfma<VEC>(dw[j], d[j], n[j], dw[j]);
+        vadd<VEC>(db[j], db[j], d[j]);
+      }
+      if (p.weight != nullptr) vmul<VEC>(d[j], d[j], w);
+      vdot<VEC>(dots, d[j], n[j]);
+      if (p.center) vsum<VEC>(total, d[j]);
+    }
+    if constexpr (GATE == GATE_AFTER) out.store(p, m, dzc, t, there);
+    float s[2] = {dots[0] + dots[1], total[0] + total[1]};
+    if (p.center) {
+      team_sum(s, m.team(p), buf, turn);
+    } else {
+      float one[1] = {s[0]};
+      team_sum(one, m.team(p), buf, turn);
+      s[0] = one[0];
+    }
+    const float a = -s[0] * inv, mean = s[1] * inv;
+    NormRow<T, VEC, PP> dx;
+#pragma unroll
+    for (int j = 0; j < PP; ++j) {
+      vfma<VEC>(d[j], n[j], a, d[j]);
+      if (p.center) vsub<VEC>(d[j], d[j], mean);
+      vmul<VEC>(d[j], d[j], r);
+      if constexpr (BEFORE) {
+        float u[VEC];
+        x_raw.r[j].widen(u);
+        vmul<VEC>(u, u, d[j]);
+        vmul<VEC>(u, u, slope[j]);
+        out.r[j].round(u);
+        vmul<VEC>(d[j], d[j], gate[j]);
+      }
+      dx.r[j].round(d[j]);
+    }
+    dx.store(p, m, dxc, t, there);
+    if constexpr (BEFORE) out.store(p, m, dzc, t, there);
   }
   if (p.part == nullptr) return;
   // a column's sums over the block's teams that hold it, in their order
