@@ -145,6 +145,26 @@ def test_delta_gradient_of_beta_next_to_zero():
     assert_each_close(dbeta, ref, "dbeta", PIECES)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("name", ["v", "do"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_delta_gradient_keeps_what_is_not_finite_in_its_sequence_and_head(dtype, name, value):
+    i = cuda(delta_inputs(21, 1, 400, 4, 2, 64, 64, dtype, [90, 210, 0, 100]))
+    clean = run_delta(i)
+    i[name] = i[name].clone()
+    i[name][0, 200, 1, 7] = value  # of the second sequence, the first key head's second head
+    got = run_delta(i)
+    ok()
+    for what, a, b in zip(("dq", "dk", "dv", "dg", "dbeta"), clean, got):
+        # (o is linear in v: its gradient is without v)
+        assert torch.equal(a, b) if (name, what) == ("v", "dv") else not b.isfinite().all(), what
+        heads = slice(1, None) if what in ("dq", "dk") else [0, 2, 3]
+        assert torch.equal(a[:, :, heads], b[:, :, heads]), what
+        assert torch.equal(a[:, :90], b[:, :90]) and torch.equal(a[:, 300:], b[:, 300:]), what
+    assert torch.equal(clean[5][[0, 2, 3]], got[5][[0, 2, 3]])
+    assert torch.equal(clean[5][:, [0, 2, 3]], got[5][:, [0, 2, 3]])
+
+
 def test_delta_gradient_of_growing_states():
     """Gates above zero: the running sums grow to +20 within a chunk."""
     i = delta_inputs(10, 1, 130, 2, 2, 64, 64, BF16)
@@ -709,6 +729,17 @@ def test_graphs_that_share_a_workspace():
             x.fill_(7)
         graphs[k].replay()
         for a, b in zip((*held[k][0], *held[k][1][:3]), (*want[k], *norm[:3])):
+            assert torch.equal(a, b)
+    ok()
+
+
+@pytest.mark.parametrize("dtype,K", [(BF16, 128), (BF16, 40), (F32, 40), (F32, 128)])
+def test_a_workspace_may_hold_anything(dtype, K):
+    i = cuda(delta_inputs(45, 1, 330, 4, 2, K, 72, dtype, [100, 1, 0, 229]))
+    want = run_delta(i)
+    for byte in (0, 255):  # (all bits set: every float a NaN)
+        room = torch.full((64 << 20,), byte, dtype=torch.uint8, device="cuda")
+        for a, b in zip(want, run_delta(i, workspace=room)):
             assert torch.equal(a, b)
     ok()
 
