@@ -12,8 +12,8 @@
 // their own for groups that threads and pieces divide evenly, without checks of their ends and
 // with the team's size known.  bf16: 2 x 4096 tokens of 16 heads of 128 with a gate take 20 us
 // (5.0 TB/s of 6.8), 32068 tokens of 8 groups of 512 90 us (5.9 TB/s; 119 in the kernel for
-// any group); the gradient of the first 41 us (4.1 TB/s), with 16 warps an SM, as a token's
-// values take 128 registers.  With one
+// any group); the gradient of the first 33 us (5.0 TB/s), with 16 warps an SM, as a token's
+// values take some 115 registers.  With one
 // token ahead, scalar arithmetic and places worked out for every token they took 28.7, 139.6
 // and 59.5 us.
 #pragma once
@@ -79,6 +79,7 @@ constexpr int norm_fwd_ahead(int words, bool z) { return words > 8 ? 1 : words >
 constexpr int norm_fwd_per_sm(int elements, int words, bool z) {
   return words > 8 || (elements > 8 && z) ? 2 : words > 4 || z ? 3 : elements > 2 ? 4 : 6;
 }
+// (of the gradient's kernels for any group; the even ones have a ring)
 constexpr int norm_bwd_ahead(int words) { return words > 4 ? 1 : 2; }
 constexpr int norm_bwd_per_sm(int elements) { return elements > 8 ? 1 : elements > 2 ? 2 : 4; }
 // A block's threads: NORM_THREADS, or what the widest groups want.

@@ -13,34 +13,64 @@
 namespace gdn {
 namespace {
 
+// Tokens on their way in the even kernels, in shared memory, each thread's pieces in places of
+// its own (so that no thread waits for another): 36 KB a block and piece.  In registers there
+// is room for two of them beside a token's values.  (2 x 4096 tokens of 16 heads of 128: 33.4 us,
+// with two in registers 41.0, with four in shared memory 34.7, with three blocks an SM 43.)
+constexpr int STAGES = 3;
+constexpr int norm_bwd_ring(int pieces) { return STAGES * 3 * pieces * NORM_THREADS * 16; }
+
 template <typename T, int VEC, int PP, NormGate GATE, int TEAM, bool WIDE>
 __global__ void __launch_bounds__(norm_block(PP * VEC, WIDE), WIDE ? 1 : norm_bwd_per_sm(PP * VEC))
 norm_bwd_kernel(NormParams p) {
   __shared__ float buf[2][NORM_WARPS][2];
-  extern __shared__ float sums[];  // [threads][PP * VEC]
+  extern __shared__ __align__(16) float sums[];  // [threads][PP * VEC], or the ring
   const NormTeam<TEAM> m(p);
   if (!bounds_ok(p.team * p.rows * p.span <= (int)blockDim.x, p.err)) return;
   int turn = 0;
   const float inv = 1.f / (float)p.W;
   constexpr bool Z = GATE != NO_GATE, BEFORE = GATE == GATE_BEFORE;
-  constexpr int AHEAD = WIDE ? 1 : norm_bwd_ahead(norm_words(sizeof(T), VEC, PP));
+  constexpr bool RING = TEAM != 0;
+  constexpr int AHEAD = WIDE || RING ? 1 : norm_bwd_ahead(norm_words(sizeof(T), VEC, PP));
   float dw[PP][VEC], db[PP][VEC];
   NormCursor<T, TEAM> gc(p, m, p.dy, p.gs, p.gb, VEC), xc(p, m, p.x, p.xs, p.xb, VEC);
   NormCursor<T, TEAM> zc(p, m, p.z, p.zs, p.zb, VEC), dxc(p, m, p.y, p.ys, p.yb, VEC);
   NormCursor<T, TEAM> dzc(p, m, p.dz, p.ds, p.db, VEC);
   // (held where there is room: 51.3 -> 49.4 us; the forward gains nothing from it)
   const NormWeights<T, VEC, PP, PP * VEC <= 8> weight(p, m, p.weight), bias(p, m, p.bias);
+  // dy, x and z of one of the next tokens: to the ring, and from it
   NormRow<T, VEC, PP> x[AHEAD], z[Z ? AHEAD : 1], g[AHEAD];
+  auto place = [&](int stage, int which, int j) {
+    return reinterpret_cast<T *>(sums) +
+           (((stage * 3 + which) * PP + j) * NORM_THREADS + threadIdx.x) * VEC;
+  };
+  auto send = [&](int stage, int t) {
+    const bool in = m.has(p, t);
+    const T *from[3] = {gc.next(p, t), xc.next(p, t), Z ? zc.next(p, t) : nullptr};
+    const void *any[3] = {p.dy, p.x, p.z};
 #pragma unroll
-  for (int i = 0; i < AHEAD; ++i) {
-    x[i].zero();
-    g[i].zero();
-    const int t = m.t + i * p.step;
-    g[i].load(p, m, gc, t, m.has(p, t));
-    x[i].load(p, m, xc, t, m.has(p, t));
-    if constexpr (Z) {
-      z[i].zero();
-      z[i].load(p, m, zc, t, m.has(p, t));
+    for (int which = 0; which < (Z ? 3 : 2); ++which)
+#pragma unroll
+      for (int j = 0; j < PP; ++j)
+        ptx::cp_async16(place(stage, which, j), in ? from[which] + j * VEC * m.team(p) : any[which], in);
+    ptx::cp_async_commit();
+  };
+  if constexpr (RING) {
+#pragma unroll
+    for (int i = 0; i < STAGES; ++i) send(i, m.t + i * p.step);
+  } else {
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const int t = m.t + i * p.step;
+      const bool in = m.has(p, t);
+      x[i].zero();
+      g[i].zero();
+      g[i].load(p, m, gc, t, in);
+      x[i].load(p, m, xc, t, in);
+      if constexpr (Z) {
+        z[i].zero();
+        z[i].load(p, m, zc, t, in);
+      }
     }
   }
 #pragma unroll
@@ -48,9 +78,18 @@ norm_bwd_kernel(NormParams p) {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) dw[j][e] = db[j][e] = 0.f;
   const int first = blockIdx.x / p.blocks_per_row * p.rows;
-  for (int t0 = first, t = m.t; t0 < p.tokens; t0 += p.step, t += p.step) {
+  for (int t0 = first, t = m.t, stage = 0; t0 < p.tokens; t0 += p.step, t += p.step) {
     const bool there = m.has(p, t);
     float n[PP][VEC], d[PP][VEC], gate[BEFORE ? PP : 1][VEC], slope[BEFORE ? PP : 1][VEC];
+    if constexpr (RING) {
+      ptx::cp_async_wait<STAGES - 1>();
+#pragma unroll
+      for (int j = 0; j < PP; ++j) {
+        g[0].r[j].load(place(stage, 0, j));
+        x[0].r[j].load(place(stage, 1, j));
+        if constexpr (Z) z[0].r[j].load(place(stage, 2, j));
+      }
+    }
     // (what is wanted behind the root's sums stays as it lies in memory till then)
     const NormRow<T, VEC, PP> x_raw = x[0], g_raw = g[0], z_raw = z[0];
 #pragma unroll
@@ -68,11 +107,16 @@ norm_bwd_kernel(NormParams p) {
         vmul<VEC>(n[j], n[j], gate[j]);
       }
     }
-    const int later = t + AHEAD * p.step;
-    const bool more = m.has(p, later);
-    g[AHEAD - 1].load(p, m, gc, later, more);
-    x[AHEAD - 1].load(p, m, xc, later, more);
-    if constexpr (Z) z[AHEAD - 1].load(p, m, zc, later, more);
+    if constexpr (RING) {
+      send(stage, t + STAGES * p.step);
+      stage = stage + 1 == STAGES ? 0 : stage + 1;
+    } else {
+      const int later = t + AHEAD * p.step;
+      const bool more = m.has(p, later);
+      g[AHEAD - 1].load(p, m, gc, later, more);
+      x[AHEAD - 1].load(p, m, xc, later, more);
+      if constexpr (Z) z[AHEAD - 1].load(p, m, zc, later, more);
+    }
     const float r = norm_root<VEC, PP>(p, m, n, buf, turn);
     float dots[2] = {0.f, 0.f}, total[2] = {0.f, 0.f};  // of dn n and of dn
     NormRow<T, VEC, PP> out;
@@ -144,6 +188,7 @@ norm_bwd_kernel(NormParams p) {
     dx.store(p, m, dxc, t, there);
     if constexpr (BEFORE) out.store(p, m, dzc, t, there);
   }
+  if constexpr (RING) ptx::cp_async_wait<0>();
   if (p.part == nullptr) return;
   // a column's sums over the block's teams that hold it, in their order
   const int teams = p.rows * p.span, each = m.team(p) * PP * VEC;
@@ -201,17 +246,24 @@ __global__ void __launch_bounds__(1024) norm_sums_kernel(const float *part, int 
 }  // namespace
 
 cudaError_t launch_norm_bwd(const NormParams &p, bool bf16, const NormPlan &plan, cudaStream_t stream) {
-  const int smem = p.part ? plan.threads * plan.pieces * plan.vec * (int)sizeof(float) : 0;
+  const int sums = p.part ? plan.threads * plan.pieces * plan.vec * (int)sizeof(float) : 0;
   return norm_forms(bf16, plan, p, [&](auto t, auto v, auto n, auto gate, auto team) {
     using T = decltype(t);
     constexpr int VEC = decltype(v)::value, PP = decltype(n)::value;
     constexpr NormGate GATE = decltype(gate)::value;
     constexpr int TEAM = decltype(team)::value;
     if (plan.threads <= NORM_THREADS) {
+      int smem = sums;
+      if constexpr (TEAM != 0) {  // (the ring is more than the sums)
+        smem = norm_bwd_ring(PP);
+        const cudaError_t e = cudaFuncSetAttribute(norm_bwd_kernel<T, VEC, PP, GATE, TEAM, false>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+      }
       norm_bwd_kernel<T, VEC, PP, GATE, TEAM, false><<<plan.blocks, plan.threads, smem, stream>>>(p);
     } else {  // only with the most pieces a thread
       if constexpr (PP == norm_pieces(VEC))
-        norm_bwd_kernel<T, VEC, PP, GATE, 0, true><<<plan.blocks, plan.threads, smem, stream>>>(p);
+        norm_bwd_kernel<T, VEC, PP, GATE, 0, true><<<plan.blocks, plan.threads, sums, stream>>>(p);
       else
         return cudaErrorInvalidConfiguration;
     }
