@@ -110,7 +110,18 @@ __device__ __forceinline__ int delta_chunks(const DeltaBwdParams &p, int n, int6
 
 // A token's log-gate for the running sums: what lies below e^-104 is zero in float32, and
 // sums that pass through lesser values (or through -infinity) would lose the gates behind.
+// The sums are formed in 64 bits and kept as two floats, G and what its rounding left: with
+// many gates that forget in a chunk they reach thousands, where a float's half step is some
+// 1e-4 of e^(G_i - G_j) between tokens that hardly forget.
 __device__ __forceinline__ float delta_gate(float g) { return g < -104.f ? -104.f : g; }
+
+// G_i - G_j of sums with their rests.
+__device__ __forceinline__ float delta_gap(float Gi, float rest_i, float Gj, float rest_j) {
+  return (Gi - Gj) + (rest_i - rest_j);
+}
+__device__ __forceinline__ float delta_gap(float2 Gi, float2 Gj) {
+  return delta_gap(Gi.x, Gi.y, Gj.x, Gj.y);
+}
 
 // Whether the offsets were good (the table kernel marks bad ones).
 __device__ __forceinline__ bool delta_good(const DeltaBwdParams &p) {

@@ -37,7 +37,7 @@ struct InputsShared {
                        STAGE = D_AT + STATE;
   static constexpr int STAGES = 2 * KQ, MATS = STAGES + 2 * STAGE, SUMS = MATS + 2 * Block<KP>::SQUARE;
   // a head's sums by quarters of the columns or rows, and its gates; two sets, taken in turn
-  static constexpr int SUM_SET = (4 * 6 + 1 + 4) * Q;
+  static constexpr int SUM_SET = (4 * 6 + 1 + 5) * Q;
   static constexpr int BYTES = SUMS + 2 * SUM_SET * 4;
 };
 
@@ -425,9 +425,13 @@ __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdPar
     const uint32_t quarter = tmem + ((uint32_t)(32 * wm) << 16);
     bf16 *PL = reinterpret_cast<bf16 *>(shared + S::MATS), *AL = PL + 2 * Q * Q;
     int m = 0, n = 0;
-    float gate = 0.f;
+    float gate = 0.f, less = 0.f;
     InputsWalk it(chunks, p.Hg);
-    if (it.there() && tid < 4 * Q) gate = Block<KP>(p, it.c, it.hk * rep).sc()[tid];
+    auto fetch_gates = [&](int64_t c, int head) {
+      if (tid < 4 * Q) gate = Block<KP>(p, c, head).sc()[tid];
+      if (tid < Q) less = Block<KP>(p, c, head).rest(tid);
+    };
+    if (it.there()) fetch_gates(it.c, it.hk * rep);
     for (; it.there(); ++n) {
       const int64_t c = it.c;
       const int hk = it.hk;
@@ -438,19 +442,17 @@ __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdPar
       const bf16 *q = reinterpret_cast<const bf16 *>(shared + (n & 1) * S::KQ), *k = q + Q * PITCH;
       for (int head = hk * rep; head < (hk + 1) * rep; ++head, ++m) {
         // by quarters: q.dq_h, k.dk_h / beta, k.dk_s, rows of M, rows of B; columns of M by wm;
-        // dr.n; gates
+        // dr.n; gates and the sums' rests
         float *sums = reinterpret_cast<float *>(shared + S::SUMS) + (m & 1) * S::SUM_SET;
         float *qd = sums, *kh = qd + 4 * Q, *kD = kh + 4 * Q, *rM = kD + 4 * Q, *rB = rM + 4 * Q;
         float *cM = rB + 4 * Q, *rn = cM + 4 * Q, *sc = rn + Q;
-        const float *G = sc, *beta = sc + Q, *eG = sc + 2 * Q, *eR = sc + 3 * Q;
+        const float *G = sc, *beta = sc + Q, *eG = sc + 2 * Q, *eR = sc + 3 * Q, *rest = sc + 4 * Q;
         const bool last = head + 1 == (hk + 1) * rep;
         if (m >= 2) wait(&counted[m & 1], m / 2 - 1);  // the sums' place is free
-        if (tid < 4 * Q) {
-          sc[tid] = gate;
-          // the next head's gates, on their way meanwhile
-          if (!last || it.there())
-            gate = Block<KP>(p, last ? it.c : c, last ? it.hk * rep : head + 1).sc()[tid];
-        }
+        if (tid < 4 * Q) sc[tid] = gate;
+        if (tid < Q) sc[4 * Q + tid] = less;
+        // the next head's gates, on their way meanwhile
+        if (!last || it.there()) fetch_gates(last ? it.c : c, last ? it.hk * rep : head + 1);
         ptx::fence_proxy_async_smem();
         finishers_meet();
         if (tid == 0) {  // the head before is through: P and A to where dP L and dA L beta will be
@@ -507,7 +509,7 @@ __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdPar
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int row = 16 * wm + g + 8 * e;
-            const float be = beta[row], Gr = G[row];
+            const float be = beta[row], Gr = G[row], less_r = rest[row];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               const int col = 16 * wn + 8 * j + 2 * t;
@@ -520,7 +522,7 @@ __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdPar
                 const float raw = dA[j][2 * e + u], own = dP[j][2 * e + u];
                 if (row == col + u) rn[row] = raw;
                 const bool in = row >= col + u && row < len, below = in && row > col + u;
-                const float L = in ? __expf(Gr - G[col + u]) : 0.f;
+                const float L = in ? __expf(delta_gap(Gr, less_r, G[col + u], rest[col + u])) : 0.f;
                 pl[u] = in ? L * p.scale * own : 0.f;
                 al[u] = below ? -be * L * raw : 0.f;
                 const float B = below ? -raw * (u ? Ah.y + Al.y : Ah.x + Al.x) : 0.f;

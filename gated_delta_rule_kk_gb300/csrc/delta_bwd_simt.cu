@@ -26,7 +26,8 @@ constexpr int TILES = 4 * TILE;      // two operands, two buffers
 constexpr int SIDE = Q + 1;          // pitch of square matrices in shared memory
 
 // A chunk and head's floats: running log-gates and beta, T, P, n and dr [64][V], the state
-// and its gradient [K][V].
+// and its gradient [K][V].  T is read as a lower triangle; above it, in the last columns of its
+// first two rows, lies what the gates' rounding left.
 struct Block {
   float *G, *beta, *T, *P, *n, *dr, *h, *D;
   __device__ Block(const DeltaBwdParams &p, int64_t chunk, int head) {
@@ -39,6 +40,11 @@ struct Block {
     dr = n + (int64_t)Q * p.V;
     h = dr + (int64_t)Q * p.V;
     D = h + (int64_t)p.K * p.V;
+  }
+  __device__ __forceinline__ float &rest(int i) const { return T[i / 32 * Q + 32 + i % 32]; }
+  __device__ __forceinline__ float lower(int i, int j) const {
+    const float x = T[i * Q + j];
+    return i >= j ? x : 0.f;
   }
 };
 
@@ -151,7 +157,7 @@ struct Rows {
 template <typename E>
 __global__ void __launch_bounds__(THREADS) simt_prepare_kernel(DeltaBwdParams p) {
   extern __shared__ __align__(16) float shared[];
-  __shared__ float G[Q], beta[Q];
+  __shared__ float G[Q], beta[Q], rest[Q];
   float *tiles = shared, *A = shared + TILES;  // [Q][SIDE]
   ptx::griddep_wait();
   const DeltaChunk ch = delta_chunk(p, blockIdx.x);
@@ -164,13 +170,24 @@ __global__ void __launch_bounds__(THREADS) simt_prepare_kernel(DeltaBwdParams p)
     G[tid] = tid < ch.len || p.g_is_cumsum ? p.g[at] : 0.f;
     if (!p.g_is_cumsum) G[tid] = delta_gate(G[tid]);
     beta[tid] = tid < ch.len ? p.beta[at] : 0.f;
+    rest[tid] = 0.f;
   }
   __syncthreads();
-  if (tid == 0 && !p.g_is_cumsum) {  // (in 64 bits: differences of the sums are taken)
-    double sum = 0.;
-    for (int i = 0; i < Q; ++i) {
-      sum += G[i];
-      G[i] = (float)sum;
+  if (tid < 32 && !p.g_is_cumsum) {  // (one thread after another, in 64 bits: 30 us more)
+    double sum[2] = {G[tid], G[tid + 32]};
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const double x = __shfl_up_sync(~0u, sum[e], o);
+        if (tid >= o) sum[e] += x;
+      }
+    sum[1] += __shfl_sync(~0u, sum[0], 31);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float f = (float)sum[e];
+      G[tid + 32 * e] = f;
+      rest[tid + 32 * e] = (float)(sum[e] - f);
     }
   }
   __syncthreads();
@@ -181,10 +198,10 @@ __global__ void __launch_bounds__(THREADS) simt_prepare_kernel(DeltaBwdParams p)
   const Rows<E> q(p.q, ch.token, p.Hg, hk, p.K, ch.len), k(p.k, ch.token, p.Hg, hk, p.K, ch.len);
   auto kt = [&](int c, int j) { return k(j, c); };
   product<STEPS, STEPS>(Q, Q, p.K, tiles, q, kt, [&](int i, int j, float s) {
-    w.P[i * Q + j] = i >= j ? p.scale * s * expf(G[i] - G[j]) : 0.f;
+    w.P[i * Q + j] = i >= j ? p.scale * s * expf(delta_gap(G[i], rest[i], G[j], rest[j])) : 0.f;
   });
   product<STEPS, STEPS>(Q, Q, p.K, tiles, k, kt, [&](int i, int j, float s) {
-    A[i * SIDE + j] = i > j ? beta[i] * s * expf(G[i] - G[j]) : 0.f;
+    A[i * SIDE + j] = i > j ? beta[i] * s * expf(delta_gap(G[i], rest[i], G[j], rest[j])) : 0.f;
   });
   float *T = tiles, *Y = tiles + Q * SIDE;  // (A's products are through)
   for (int x = tid; x < Q * Q; x += THREADS) T[x / Q * SIDE + x % Q] = 0.f;
@@ -217,7 +234,10 @@ __global__ void __launch_bounds__(THREADS) simt_prepare_kernel(DeltaBwdParams p)
     }
     __syncthreads();
   }
-  for (int x = tid; x < Q * Q; x += THREADS) w.T[x] = T[x / Q * SIDE + x % Q];
+  for (int x = tid; x < Q * Q; x += THREADS) {
+    const int i = x / Q, j = x % Q;
+    w.T[x] = i < 2 && j >= 32 ? rest[i * 32 + j - 32] : T[i * SIDE + j];
+  }
 }
 
 // The factors of a chunk's rows in a walk: beta, e^G and e^(G_L - G), which is zero past the
@@ -228,10 +248,10 @@ struct Factors {
     __syncthreads();  // the ones before have been read
     if (threadIdx.x < Q) {
       const int i = threadIdx.x;
-      const float G = w.G[i], GL = w.G[len - 1];
+      const float G = w.G[i], R = delta_gap(w.G[len - 1], w.rest(len - 1), G, w.rest(i));
       beta[i] = w.beta[i];
       eG[i] = expf(G);
-      eR[i] = i < len ? expf(GL - G) : 0.f;
+      eR[i] = i < len ? expf(R) : 0.f;
     }
     __syncthreads();
   }
@@ -269,7 +289,7 @@ __global__ void __launch_bounds__(THREADS) simt_states_kernel(DeltaBwdParams p) 
                            w.n[(int64_t)i * V + v0 + j] = f.beta[i] * (v(i, v0 + j) - f.eG[i] * s);
                          });
     auto rows = [&](int i, int j) { return w.n[(int64_t)i * V + v0 + j]; };
-    product<STEPS, ROWS>(Q, nv, Q, tiles, [&](int i, int m) { return w.T[i * Q + m]; }, rows,
+    product<STEPS, ROWS>(Q, nv, Q, tiles, [&](int i, int m) { return w.lower(i, m); }, rows,
                          [&](int i, int j, float s) { w.n[(int64_t)i * V + v0 + j] = s; });
     if (c + 1 == count) break;
     const Block next(p, first + c + 1, head);
@@ -319,7 +339,7 @@ __global__ void __launch_bounds__(THREADS) simt_grads_kernel(DeltaBwdParams p) {
     product<STEPS, ROWS>(Q, nv, K, tiles, k, [&](int i, int j) { return w.D[(int64_t)i * V + v0 + j]; },
                          [&](int i, int j, float s) { w.dr[(int64_t)i * V + v0 + j] += f.eR[i] * s; });
     auto rows = [&](int i, int j) { return w.dr[(int64_t)i * V + v0 + j]; };
-    product<ROWS, ROWS>(Q, nv, Q, tiles, [&](int i, int m) { return w.T[m * Q + i]; }, rows,
+    product<ROWS, ROWS>(Q, nv, Q, tiles, [&](int i, int m) { return w.lower(m, i); }, rows,
                         [&](int i, int j, float s) { w.dr[(int64_t)i * V + v0 + j] = s; });
     if (c == 0 && p.dh0 == nullptr) break;
     float *prev = c > 0 ? Block(p, first + c - 1, head).D : nullptr;
@@ -393,7 +413,8 @@ __global__ void __launch_bounds__(THREADS) simt_inputs_kernel(DeltaBwdParams p) 
   if (ch.len <= 0) return;
   if (!bounds_ok(ch.n < p.N && ch.token + ch.len <= (int64_t)p.B * p.T, p.err)) return;
   const Rows<E> q(p.q, ch.token, p.Hg, hk, K, ch.len), k(p.k, ch.token, p.Hg, hk, K, ch.len);
-  float *qd = s.sums, *kh = qd + Q, *kD = kh + Q, *G = kD + Q, *dG = G + Q, *part = dG + Q;
+  float *qd = s.sums, *kh = qd + Q, *kD = kh + Q, *G = kD + Q, *dG = G + Q, *rest = dG + Q;
+  float *part = rest + Q;
   for (int x = tid; x < Q * K; x += THREADS) s.dq[x] = s.dk[x] = 0.f;
   __syncthreads();
   for (int head = hk * rep; head < (hk + 1) * rep; ++head) {
@@ -401,7 +422,10 @@ __global__ void __launch_bounds__(THREADS) simt_inputs_kernel(DeltaBwdParams p) 
     const Rows<E> go(p.dout, ch.token, p.H, head, V, ch.len), v(p.v, ch.token, p.H, head, V, ch.len);
     f.load(w, ch.len);
     const float keep = f.eG[ch.len - 1];
-    if (tid < Q) G[tid] = w.G[tid];
+    if (tid < Q) {
+      G[tid] = w.G[tid];
+      rest[tid] = w.rest(tid);
+    }
     __syncthreads();
     auto kt = [&](int c, int j) { return k(j, c); };
     auto n = [&](int i, int c) { return w.n[(int64_t)i * V + c]; };
@@ -411,13 +435,15 @@ __global__ void __launch_bounds__(THREADS) simt_inputs_kernel(DeltaBwdParams p) 
     auto Dt = [&](int c, int kc) { return w.D[(int64_t)kc * V + c]; };
     product<STEPS, STEPS>(Q, Q, K, s.tiles, q, kt, [&](int i, int j, float x) { s.P[i * SIDE + j] = x; });
     product<STEPS, STEPS>(Q, Q, V, s.tiles, go, nt, [&](int i, int j, float x) {
-      const float L = i >= j && i < ch.len ? p.scale * expf(G[i] - G[j]) : 0.f;
+      const bool in = i >= j && i < ch.len;
+      const float L = in ? p.scale * expf(delta_gap(G[i], rest[i], G[j], rest[j])) : 0.f;
       s.M[i * SIDE + j] = L * x * s.P[i * SIDE + j];
       s.P[i * SIDE + j] = L * x;
     });
     product<STEPS, STEPS>(Q, Q, K, s.tiles, k, kt, [&](int i, int j, float x) { s.A[i * SIDE + j] = x; });
     product<STEPS, STEPS>(Q, Q, V, s.tiles, dr, nt, [&](int i, int j, float x) {
-      const float L = i > j && i < ch.len ? expf(G[i] - G[j]) : 0.f;
+      const bool in = i > j && i < ch.len;
+      const float L = in ? expf(delta_gap(G[i], rest[i], G[j], rest[j])) : 0.f;
       s.B[i * SIDE + j] = -L * x * s.A[i * SIDE + j];
       s.A[i * SIDE + j] = -L * x * f.beta[i];
     });

@@ -21,7 +21,7 @@ struct PrepareShared {
   static constexpr int PITCH = Q + 8;  // of A and T in float32
   // q and k, then P's and A's images, then T and behind it its image; A
   static constexpr int T_IMAGE = Q * PITCH * 4, IMAGES = T_IMAGE + Block<KP>::SQUARE;
-  static constexpr int BYTES = IMAGES + (Q * PITCH + 2 * Q) * 4;
+  static constexpr int BYTES = IMAGES + (Q * PITCH + 3 * Q) * 4;
   static_assert(IMAGES >= 2 * Block<KP>::SQUARE && IMAGES >= 2 * Q * KP * 2, "");
 };
 
@@ -33,7 +33,8 @@ __global__ void __launch_bounds__(PREP, 4) tc_prepare_kernel(DeltaBwdParams p) {
   constexpr int PITCH = PrepareShared<KP>::PITCH;
   float(*A)[PITCH] = reinterpret_cast<float(*)[PITCH]>(shared + PrepareShared<KP>::IMAGES);
   float(*T)[PITCH] = reinterpret_cast<float(*)[PITCH]>(shared);
-  float *G = reinterpret_cast<float *>(A + Q), *beta = G + Q;
+  float2 *G = reinterpret_cast<float2 *>(A + Q);  // sums and their rests
+  float *beta = reinterpret_cast<float *>(G + Q);
   const DeltaChunk ch = delta_chunk(p, blockIdx.x);
   const int head = blockIdx.y, hk = head / (p.H / p.Hg);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -46,7 +47,7 @@ __global__ void __launch_bounds__(PREP, 4) tc_prepare_kernel(DeltaBwdParams p) {
   fetch_rows<KP, PREP>(k, p.k, ch, p.Hg, hk, p.K, 0);
   ptx::cp_async_commit();
   if (warp == 0) {
-    float g[2];
+    float g[2], less[2] = {0.f, 0.f};
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int i = lane + 32 * e;
@@ -55,7 +56,7 @@ __global__ void __launch_bounds__(PREP, 4) tc_prepare_kernel(DeltaBwdParams p) {
       if (!p.g_is_cumsum) g[e] = delta_gate(g[e]);
       beta[i] = i < ch.len ? p.beta[where] : 0.f;
     }
-    if (!p.g_is_cumsum) {  // (in 64 bits: differences of the sums are taken)
+    if (!p.g_is_cumsum) {
       double sum[2] = {g[0], g[1]};
 #pragma unroll
       for (int e = 0; e < 2; ++e)
@@ -66,18 +67,21 @@ __global__ void __launch_bounds__(PREP, 4) tc_prepare_kernel(DeltaBwdParams p) {
         }
       sum[1] += __shfl_sync(~0u, sum[0], 31);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) g[e] = (float)sum[e];
+      for (int e = 0; e < 2; ++e) {
+        g[e] = (float)sum[e];
+        less[e] = (float)(sum[e] - g[e]);
+      }
     }
-    G[lane] = g[0];
-    G[lane + 32] = g[1];
+    G[lane] = make_float2(g[0], less[0]);
+    G[lane + 32] = make_float2(g[1], less[1]);
   }
   ptx::cp_async_wait<0>();
   __syncthreads();
   if (tid < Q) {
-    w.sc()[tid] = G[tid];
+    w.sc()[tid] = G[tid].x;
     w.sc()[Q + tid] = beta[tid];
-    w.sc()[2 * Q + tid] = expf(G[tid]);
-    w.sc()[3 * Q + tid] = expf(G[Q - 1] - G[tid]);
+    w.sc()[2 * Q + tid] = expf(G[tid].x);
+    w.sc()[3 * Q + tid] = expf(delta_gap(G[Q - 1], G[tid]));
   }
   const int wm = warp & 3, g = lane >> 2, t = lane & 3;
   const bool of_q = warp < 4;
@@ -103,7 +107,8 @@ __global__ void __launch_bounds__(PREP, 4) tc_prepare_kernel(DeltaBwdParams p) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const bool in = of_q ? row >= col + e : row > col + e;
-        v[e] = in ? (of_q ? p.scale : 1.f) * s[j][2 * r + e] * __expf(G[row] - G[col + e]) : 0.f;
+        v[e] = in ? (of_q ? p.scale : 1.f) * s[j][2 * r + e] * __expf(delta_gap(G[row], G[col + e]))
+                  : 0.f;
       }
       if (of_q) {
         put_pair(Ph, Pl, at<64>(row, col), v[0], v[1]);
@@ -172,6 +177,8 @@ __global__ void __launch_bounds__(PREP, 4) tc_prepare_kernel(DeltaBwdParams p) {
     const int row = i / 32, col = i % 32 * 2;
     put_pair(Th, Tl, at<64>(row, col), row >= col ? T[row][col] : 0.f,
              row >= col + 1 ? T[row][col + 1] : 0.f);
+    if (row < 8 && col >= 48)
+      *reinterpret_cast<float *>(Th + at<64>(row, col)) = G[row * 8 + (col - 48) / 2].y;
   }
   __syncthreads();
   keep<PREP>(w.T(), Th, Block<KP>::SQUARE);

@@ -84,7 +84,9 @@ __device__ __forceinline__ float2 get_pair(const bf16 *s, int place) {
 // A chunk and head in the workspace (bytes; KP = K rounded up to 64 or 128): G, beta, e^G and
 // e^(G_L - G) of its tokens (past its end G = G_L and beta = 0), then matrices, each hi then
 // lo: T, P and A without beta as images; by value tiles n, dr [32][64] and h, D [32][KP], value columns first, as
-// 8 x 8 tiles of 128 bytes (a warp holds such a tile as a word a lane, in this order).
+// 8 x 8 tiles of 128 bytes (a warp holds such a tile as a word a lane, in this order).  What G's
+// rounding left lies in the first rows of T's upper right block, which is zero and which no walk
+// reads.
 template <int KP>
 struct Block {
   static constexpr int SC = 4 * Q * 4, SQUARE = 2 * Q * Q * 2, ROWS = 2 * Q * VT * 2,
@@ -95,6 +97,11 @@ struct Block {
       : base(p.blocks + (chunk * p.H + head) * p.block), tiles((p.V + VT - 1) / VT) {}
   __device__ float *sc() const { return reinterpret_cast<float *>(base); }
   __device__ unsigned char *T() const { return base + SC; }
+  // where token i's rest lies in T's first image
+  static __device__ __forceinline__ int rest_at(int i) { return at<64>(i >> 3, 48 + 2 * (i & 7)); }
+  __device__ float rest(int i) const {
+    return *reinterpret_cast<const float *>(reinterpret_cast<const bf16 *>(T()) + rest_at(i));
+  }
   __device__ unsigned char *P() const { return base + SC + SQUARE; }
   __device__ unsigned char *n(int v) const { return base + SC + 3 * SQUARE + v * ROWS; }
   __device__ unsigned char *dr(int v) const { return n(tiles) + v * ROWS; }

@@ -1,0 +1,72 @@
+"""Calls of the delta rule layers' operators that their other tests do not make.
+
+Bounds.  In norm, float32 results of the tensor cores as tests/test_layer_gpu.py derives
+(1e-5).  Of float32 inputs: a product's sum of up to 64 terms rounds by 2^-24 a step, sqrt(64)
+of them in quadrature, and six products follow one another: 7e-6 at most if all rounded the same
+way, sqrt(6) x 8 x 2^-24 = 1.2e-6 as they do; e^x is off by 2^-24 |x|, where |x| e^x is below
+one.  1e-5 as well.  Element for element as there: 3e-3 RMS with pieces, 1e-4 without.
+
+Pieces end at bfloat16's smallest step, 2^-133, half of which an operand is off by besides.
+Each token that reaches dh0 adds two products to it, of do with q and of dr with k, whose rows
+of q and k have length 1: in norm sqrt(V) 2^-134 each.  (Counts where e^G is 1e-35.)
+"""
+import numpy as np
+import pytest
+import torch
+
+import gated_delta_rule_kk_gb300 as gdn
+from gated_delta_rule_kk_gb300 import Status
+from oracle import layer as L
+
+from _layer import delta_inputs
+from _mixer import assert_each_close, cuda
+from _util import TOL_F32, _np
+from test_layer_gpu import PIECES, run_delta
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def ok():
+    assert gdn.gdn_check_device_error() == Status.OK
+
+
+def check_norms(got, i, reach=64, **kw):
+    """Every result element for element, the float32 ones within 1e-5 of their norm; ``reach``
+    tokens of a sequence reach its initial state."""
+    ref = L.gdn_grad(i["do"], i["q"], i["k"], i["v"], i["g"], i["beta"], i["scale"], i["h0"],
+                     i["dht"], i["cu"], **kw)
+    pieces = i["q"].dtype is BF16
+    step = reach * 2 * 2.0 ** -134 * np.sqrt(ref[5].size / ref[5].shape[2]) if pieces else 0.0
+    off = {}
+    for name, x, r in zip(("dq", "dk", "dv", "dg", "dbeta", "dh0"), got, ref):
+        if name != "dh0" or not pieces:
+            assert_each_close(x, r, name, PIECES if pieces else TOL_F32)
+        if x.dtype is F32:
+            room = 1e-5 * np.linalg.norm(r) + (step if name == "dh0" else 0.0)
+            off[name] = np.linalg.norm(_np(x) - r) / max(room, 1e-300)
+    assert max(off.values()) <= 1.0, {k: f"{v:.2f} times the allowed error" for k, v in off.items()}
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("every", [2, 3, 4, 8, 21])
+@pytest.mark.parametrize("gate", [-float("inf"), -1e4, -80.0, -30.0])
+def test_delta_gradient_of_many_gates_that_forget(dtype, every, gate):
+    """The running sums reach some -3300 in a chunk; the tokens between two such gates are
+    coupled by differences of them."""
+    i = delta_inputs(every, 1, 150, 2, 2, 64, 64, dtype, [90, 60])
+    i["g"][:, ::every] = gate
+    got = run_delta(cuda(i))
+    ok()
+    check_norms(got, i, reach=every)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_delta_gradient_of_many_gates_that_forget_and_shared_heads(dtype):
+    i = delta_inputs(3, 2, 200, 4, 2, 96, 40, dtype)
+    i["g"][:, 1::3] = -60.0
+    i["g"][:, :, 1] = -5.0
+    got = run_delta(cuda(i))
+    ok()
+    check_norms(got, i)
