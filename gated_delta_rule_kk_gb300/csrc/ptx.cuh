@@ -60,6 +60,16 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t *bar, uint32_t parity
   return false;
 }
 
+// Polls of a wait by a warp of `role` in a kernel whose warps have roles.  A test's build
+// (-DGDN_WAITS_OUT=r) lets the waits of role r run out at once, and the others soon.
+__device__ __forceinline__ uint32_t role_polls(int role) {
+#ifdef GDN_WAITS_OUT
+  return role == GDN_WAITS_OUT ? 0 : 1u << 12;
+#else
+  return 1u << 22;
+#endif
+}
+
 // Bulk global -> shared copy of `bytes` (multiple of 16, both addresses
 // 16-byte aligned) that signals completion on `bar` as transaction bytes.
 __device__ __forceinline__ void bulk_g2s(void *smem_dst, const void *gmem_src, uint32_t bytes,

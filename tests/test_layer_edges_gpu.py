@@ -10,12 +10,16 @@ Pieces end at bfloat16's smallest step, 2^-133, half of which an operand is off 
 Each token that reaches dh0 adds two products to it, of do with q and of dr with k, whose rows
 of q and k have length 1: in norm sqrt(V) 2^-134 each.  (Counts where e^G is 1e-35.)
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
 
 import gated_delta_rule_kk_gb300 as gdn
-from gated_delta_rule_kk_gb300 import Status
+from gated_delta_rule_kk_gb300 import Status, build_lib
 from oracle import layer as L
 
 from _layer import delta_inputs
@@ -70,3 +74,85 @@ def test_delta_gradient_of_many_gates_that_forget_and_shared_heads(dtype):
     got = run_delta(cuda(i))
     ok()
     check_norms(got, i)
+
+
+# ---------------------------------------------------------------- waits that run out
+
+@pytest.fixture(scope="module")
+def waiting_out(tmp_path_factory):
+    """By role, the library whose warps of that role find every wait run out."""
+    build_lib.build()
+    jobs, links, libs = [], [], {}
+    for role in range(4):
+        folder, objs = str(tmp_path_factory.mktemp(f"role{role}")), []
+        for src in build_lib._sources():
+            name = os.path.basename(src)[:-3] + ".o"
+            if "role_polls" in open(src).read():
+                objs.append(os.path.join(folder, name))
+                jobs.append([build_lib._nvcc(), *build_lib.NVCC_FLAGS, f"-DGDN_WAITS_OUT={role}", "-c",
+                             src, "-o", objs[-1]])
+            else:
+                objs.append(os.path.join(build_lib.BUILD_DIR, name))
+        libs[role] = os.path.join(folder, f"libgdn_waits_out_{role}.so")
+        links.append([build_lib._nvcc(), *build_lib.ARCH, "-shared", "-cudart", "shared", "-o", libs[role],
+                      *objs])
+    for commands in (jobs, links):
+        for p in [subprocess.Popen(c) for c in commands]:
+            assert p.wait() == 0
+    return libs
+
+
+def run_waiting_out(script, role, libs):
+    tests = os.path.dirname(os.path.abspath(__file__))
+    r = subprocess.run([sys.executable, "-c", PRELUDE + script, os.path.dirname(tests), tests,
+                        build_lib.build(), libs[role], str(role)],
+                       capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stdout + r.stderr
+
+
+PRELUDE = r"""
+import sys
+sys.path[:0] = [sys.argv[1], sys.argv[2]]
+import torch
+from gated_delta_rule_kk_gb300 import _lib, Status
+import gated_delta_rule_kk_gb300 as gdn
+from _layer import delta_inputs, kda_inputs
+from _mixer import cuda
+
+release, other, role = _lib.load(sys.argv[3]), _lib.load(sys.argv[4]), int(sys.argv[5])
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def call(lib, f, status):
+    _lib._lib = lib
+    out = f()
+    got = gdn.gdn_check_device_error()
+    assert got == status, (got, status)
+    return out
+"""
+
+KDA_WAITS = r"""
+d = cuda(kda_inputs(5, 300, 2, 2, 4, 128, 128, BF16, BF16))
+before = d["state"].clone()
+
+
+def tokens(state):
+    gdn.kda_decode(d["q"], d["k"], d["v"], d["a"], d["b"], d["A_log"], d["dt_bias"], state,
+                   slot_indices=d["slots"])
+    return state
+
+
+after = call(release, lambda: tokens(before.clone()), Status.OK)
+mid = call(other, lambda: tokens(before.clone()), Status.TIMEOUT)
+same, done = ((mid == x).all(-1) for x in (before, after))
+assert (same | done).all(), int((~(same | done)).sum())
+if role in (0, 3):  # nothing is taken, or nothing stored
+    assert same.all()
+assert torch.equal(call(release, lambda: tokens(before.clone()), Status.OK), after)
+"""
+
+
+@pytest.mark.parametrize("role", [0, 1, 2, 3])
+def test_kda_tokens_whose_waits_run_out_leave_states_whole(role, waiting_out):
+    """Warps that take tiles, prepare, load or store: every row is the call's, or as it was."""
+    run_waiting_out(KDA_WAITS, role, waiting_out)
