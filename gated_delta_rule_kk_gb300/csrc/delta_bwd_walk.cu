@@ -155,7 +155,9 @@ struct Walk {
   bool ok;
 
   __device__ __forceinline__ void wait(uint64_t *bar, int use) {
-    ok = ptx::mbar_wait_bounded(bar, (uint32_t)(use & 1), ok ? 1u << 22 : 1u) && ok;
+    // (carry, hand on, load, store)
+    const int who = role == 0 ? 0 : BACK && role == 1 ? 1 : 2 + sw;
+    ok = ptx::mbar_wait_bounded(bar, (uint32_t)(use & 1), ok ? ptx::role_polls(who) : 1u) && ok;
   }
   __device__ __forceinline__ void arrive(uint64_t *bar) const {
     __syncwarp();
@@ -184,7 +186,8 @@ struct Walk {
 
   // The loading warp.
   __device__ __forceinline__ void load(const DeltaBwdParams &p) {
-    for (int i = 0; i < count; ++i) {
+    int i = 0;
+    for (; i < count; ++i) {
       if (i >= 2) wait(&empty[i & 1], i / 2 - 1);
       if (!__all_sync(~0u, ok)) break;
       const int c = chunk(i);
@@ -204,10 +207,12 @@ struct Walk {
                       p.V, v0, rows);
       ptx::cp_async_mbar_arrive(&full[i & 1]);
     }
-    // the last copies land before the warp ends, whoever else waits for them
+    // the last copies asked for land before the warp ends, whoever else waits for them and
+    // whatever ran out
     ptx::cp_async_commit();
     ptx::cp_async_wait<0>();
-    for (int i = max(0, count - 2); i < count && ok; ++i) wait(&full[i & 1], i / 2);
+    for (int k = max(0, i - 2); k < i; ++k)
+      ok = ptx::mbar_wait_bounded(&full[k & 1], (uint32_t)(k / 2 & 1), 1u << 22) && ok;
   }
 
   __device__ __forceinline__ void load_state(const DeltaBwdParams &p, const float *from,

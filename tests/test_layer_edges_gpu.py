@@ -156,3 +156,45 @@ assert torch.equal(call(release, lambda: tokens(before.clone()), Status.OK), aft
 def test_kda_tokens_whose_waits_run_out_leave_states_whole(role, waiting_out):
     """Warps that take tiles, prepare, load or store: every row is the call's, or as it was."""
     run_waiting_out(KDA_WAITS, role, waiting_out)
+
+
+DELTA_WAITS = r"""
+import ctypes
+from gated_delta_rule_kk_gb300._lib import GdnChunkBwdArgs
+H, Hg, K = 4, 2, 128
+d = cuda(delta_inputs(6, 1, 2000, H, Hg, K, K, BF16, [900, 1100]))
+
+
+def gradient():  # its outputs between guards of 7
+    outs = {}
+    for n, t in dict(dq="q", dk="k", dv="v", dg="g", dbeta="beta", dh0="h0").items():
+        room = torch.full((d[t].numel() + (2 << 16),), 7.0, dtype=d[t].dtype, device="cuda")
+        outs[n] = room, room[1 << 16:-(1 << 16)]
+    a = GdnChunkBwdArgs(dtype=1, B=1, T=2000, H=H, Hg=Hg, K=K, V=K, N=2, chunk_size=64,
+                        **{n: d[n].data_ptr() for n in ("q", "k", "v", "g", "beta", "h0", "dht")},
+                        do_=d["do"].data_ptr(), cu_seqlens=d["cu"].data_ptr(),
+                        **{n: t.data_ptr() for n, (_, t) in outs.items()})
+    n = ctypes.c_size_t(0)
+    assert _lib._lib.gdn_chunk_bwd_workspace_size(ctypes.byref(a), ctypes.byref(n)) == Status.OK
+    room = torch.zeros(n.value + (1 << 20), dtype=torch.uint8, device="cuda")
+    a.workspace, a.workspace_bytes = room.data_ptr(), n.value
+    assert _lib._lib.gdn_chunk_bwd(ctypes.byref(a), torch.cuda.current_stream().cuda_stream) == Status.OK
+    torch.cuda.synchronize()
+    assert not room[n.value:].any()
+    for r, _ in outs.values():
+        assert (r[:1 << 16] == 7).all() and (r[-(1 << 16):] == 7).all()
+    return [t for _, t in outs.values()]
+
+
+want = call(release, gradient, Status.OK)
+call(other, gradient, Status.TIMEOUT)
+for a, b in zip(want, call(release, gradient, Status.OK)):
+    assert torch.equal(a, b)
+"""
+
+
+@pytest.mark.parametrize("role", [0, 1, 2, 3])
+def test_delta_gradient_whose_waits_run_out_ends(role, waiting_out):
+    """Warps that carry (finish), hand on (multiply), load or store (count): the call ends with
+    an error, nothing is written elsewhere and the next call is right."""
+    run_waiting_out(DELTA_WAITS, role, waiting_out)
