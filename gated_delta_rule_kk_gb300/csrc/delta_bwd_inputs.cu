@@ -170,6 +170,8 @@ __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdPar
   constexpr int NT = KP / 32, PITCH = S::PITCH;  // tiles of 8 columns of a warp's quarter of [64][KP]
   extern __shared__ __align__(128) unsigned char shared[];
   __shared__ uint64_t st_full[2], st_empty[2], x_full, x_empty, kq_full[2], pa_full, begun, summed[2], counted[2];
+  __shared__ uint64_t through;
+  __shared__ int pa_asked;
   __shared__ InputsItem place[2];
   __shared__ float hD[4];
   __shared__ uint32_t tmem_at;
@@ -187,6 +189,8 @@ __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdPar
     ptx::mbar_init(&x_empty, IN_FINISH);
     ptx::mbar_init(&pa_full, 1);
     ptx::mbar_init(&begun, 1);
+    ptx::mbar_init(&through, 1);
+    pa_asked = 0;
     for (int s = 0; s < 2; ++s) {
       ptx::mbar_init(&kq_full[s], 1);
       ptx::mbar_init(&summed[s], IN_FINISH);
@@ -204,8 +208,14 @@ __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdPar
   ptx::tc_fence_after();
   const uint32_t tmem = tmem_at;
   bool ok = true;
+  // roles: finish; multiply and <h, D>; stages; the clerk
+  const int role = warp == 0 ? 2 : warp < 3 ? 1 : warp == 3 ? 3 : 0;
   auto wait = [&](uint64_t *bar, int use) {
-    ok = ptx::mbar_wait_bounded(bar, (uint32_t)(use & 1), ok ? 1u << 22 : 1u) && ok;
+    ok = ptx::mbar_wait_bounded(bar, (uint32_t)(use & 1), ok ? ptx::role_polls(role) : 1u) && ok;
+  };
+  // for what was asked for and may still be on its way, whatever ran out
+  auto settle = [&](uint64_t *bar, int use) {
+    ok = ptx::mbar_wait_bounded(bar, (uint32_t)(use & 1), 1u << 22) && ok;
   };
   auto stage = [&](int s) { return shared + S::STAGES + (s & 1) * S::STAGE; };
   if (warp == 0) {  // stages: what the workspace has, and do's rows as a left operand of tcgen05
@@ -243,7 +253,7 @@ __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdPar
       }
     }
     // the last copies land before the warp ends, whoever else waits for them
-    for (int k = max(0, s - 2); k < s && ok; ++k) wait(&st_full[k & 1], k / 2);
+    for (int k = max(0, s - 2); k < s; ++k) settle(&st_full[k & 1], k / 2);
   } else if (warp == 1) {  // the five products
     const uint32_t wide = ptx::idesc_bf16(64, KP, 0, 1), wide_t = ptx::idesc_bf16(64, KP, 1, 1);
     const uint32_t square = ptx::idesc_bf16(64, Q, 0, 1), square_t = ptx::idesc_bf16(64, Q, 1, 1);
@@ -294,7 +304,9 @@ __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdPar
           __syncwarp();
         }
       }
-    if (m >= 1 && ok) wait(&x_full, m - 1);  // nothing is left on its way
+    // no product is left on its way when tensor memory is given back
+    if (lane == 0) ptx::mma_commit(&through);
+    settle(&through, 0);
   } else if (warp == 2) {  // <h, D>
     int m = 0, s = 0;
     for (InputsWalk it(chunks, p.Hg); it.there(); it.next())
@@ -417,7 +429,7 @@ __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdPar
         if (lane == 0) ptx::mbar_arrive(&counted[m & 1]);
       }
     }
-    for (int k = max(0, n - 2); k < n && ok; ++k) wait(&kq_full[k & 1], k / 2);  // all have landed
+    for (int k = max(0, n - 2); k < n; ++k) settle(&kq_full[k & 1], k / 2);  // all have landed
   } else {
     // Sixteen warps finish a head: rows 16 wm (their quarter of tensor memory), quarter wn of
     // the columns.
@@ -437,8 +449,9 @@ __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdPar
       const int hk = it.hk;
       it.next();  // (from here on the next one)
       wait(&kq_full[n & 1], n / 2);
+      // (without its wait the place may be anything: no row is written)
       const int64_t token = place[n & 1].token;
-      const int len = place[n & 1].len;
+      const int len = ok ? place[n & 1].len : 0;
       const bf16 *q = reinterpret_cast<const bf16 *>(shared + (n & 1) * S::KQ), *k = q + Q * PITCH;
       for (int head = hk * rep; head < (hk + 1) * rep; ++head, ++m) {
         // by quarters: q.dq_h, k.dk_h / beta, k.dk_s, rows of M, rows of B; columns of M by wm;
@@ -458,6 +471,7 @@ __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdPar
         if (tid == 0) {  // the head before is through: P and A to where dP L and dA L beta will be
           if (head == hk * rep) ptx::mbar_arrive(&begun);
           if (ok) {
+            pa_asked = m + 1;
             ptx::mbar_arrive_expect_tx(&pa_full, 2 * Block<KP>::SQUARE);
             ptx::bulk_g2s(PL, Block<KP>(p, c, head).P(), 2 * Block<KP>::SQUARE, &pa_full);
           }
@@ -467,11 +481,21 @@ __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdPar
         float dq[NT][4], dk[NT][4], dP[2][4], dA[2][4];
         {
           float xs[NT][4];
-          take_fragments<NT>(quarter + XQ + wn * (KP / 4), dq);
-          take_fragments<NT>(quarter + XK + wn * (KP / 4), dk);
-          take_fragments<NT>(quarter + XS + wn * (KP / 4), xs);
-          take_fragments<2>(quarter + DP + wn * 16, dP);
-          take_fragments<2>(quarter + DA + wn * 16, dA);
+          if (__all_sync(~0u, ok)) {
+            take_fragments<NT>(quarter + XQ + wn * (KP / 4), dq);
+            take_fragments<NT>(quarter + XK + wn * (KP / 4), dk);
+            take_fragments<NT>(quarter + XS + wn * (KP / 4), xs);
+            take_fragments<2>(quarter + DP + wn * 16, dP);
+            take_fragments<2>(quarter + DA + wn * 16, dA);
+          } else {  // products may be on their way
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                dq[j][e] = dk[j][e] = xs[j][e] = 0.f;
+                if (j < 2) dP[j][e] = dA[j][e] = 0.f;
+              }
+          }
           ptx::tc_fence_before();
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&x_empty);
@@ -610,6 +634,7 @@ __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdPar
       }
     }
   }
+  if (threadIdx.x == 128 && pa_asked > 0) settle(&pa_full, pa_asked - 1);  // (that thread asked)
   if (!ok && lane == 0) record_error(p.err, GDN_ERR_TIMEOUT);
   ptx::tc_fence_before();
   __syncthreads();
