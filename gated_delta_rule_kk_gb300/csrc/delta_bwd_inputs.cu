@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdPar
         wait(&summed[m & 1], m / 2);
         const float *sums = reinterpret_cast<const float *>(shared + S::SUMS) + (m & 1) * S::SUM_SET;
         const float *qd = sums, *kh = qd + 4 * Q, *kD = kh + 4 * Q, *rM = kD + 4 * Q, *rB = rM + 4 * Q;
-        const float *cM = rB + 4 * Q, *rn = cM + 4 * Q, *beta = rn + 2 * Q, *eG = beta + Q;
+        const float *cM = rB + 4 * Q, *rn = cM + 4 * Q, *beta = rn + 3 * Q, *eG = beta + Q;
         const float state = hD[m & 3];
         float d[2], db[2], all = 0.f;
 #pragma unroll
@@ -459,11 +459,15 @@ __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdPar
         float *sums = reinterpret_cast<float *>(shared + S::SUMS) + (m & 1) * S::SUM_SET;
         float *qd = sums, *kh = qd + 4 * Q, *kD = kh + 4 * Q, *rM = kD + 4 * Q, *rB = rM + 4 * Q;
         float *cM = rB + 4 * Q, *rn = cM + 4 * Q, *sc = rn + Q;
-        const float *G = sc, *beta = sc + Q, *eG = sc + 2 * Q, *eR = sc + 3 * Q, *rest = sc + 4 * Q;
+        // (sums and rests side by side)
+        const float2 *G = reinterpret_cast<const float2 *>(sc);
+        const float *beta = sc + 2 * Q, *eG = sc + 3 * Q, *eR = sc + 4 * Q;
         const bool last = head + 1 == (hk + 1) * rep;
         if (m >= 2) wait(&counted[m & 1], m / 2 - 1);  // the sums' place is free
-        if (tid < 4 * Q) sc[tid] = gate;
-        if (tid < Q) sc[4 * Q + tid] = less;
+        if (tid < Q)
+          reinterpret_cast<float2 *>(sc)[tid] = make_float2(gate, less);
+        else if (tid < 4 * Q)
+          sc[Q + tid] = gate;
         // the next head's gates, on their way meanwhile
         if (!last || it.there()) fetch_gates(last ? it.c : c, last ? it.hk * rep : head + 1);
         ptx::fence_proxy_async_smem();
@@ -533,11 +537,13 @@ __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdPar
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int row = 16 * wm + g + 8 * e;
-            const float be = beta[row], Gr = G[row], less_r = rest[row];
+            const float be = beta[row];
+            const float2 Gr = G[row];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               const int col = 16 * wn + 8 * j + 2 * t;
               const int spot = at<64>(row, col);
+              const float4 Gc = *reinterpret_cast<const float4 *>(G + col);
               const float2 Ph = get_pair(PL, spot), Pl = get_pair(PL + Q * Q, spot);
               const float2 Ah = get_pair(AL, spot), Al = get_pair(AL + Q * Q, spot);
               float pl[2], al[2];
@@ -546,7 +552,7 @@ __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdPar
                 const float raw = dA[j][2 * e + u], own = dP[j][2 * e + u];
                 if (row == col + u) rn[row] = raw;
                 const bool in = row >= col + u && row < len, below = in && row > col + u;
-                const float L = in ? __expf(delta_gap(Gr, less_r, G[col + u], rest[col + u])) : 0.f;
+                const float L = in ? __expf(delta_gap(Gr, u ? make_float2(Gc.z, Gc.w) : make_float2(Gc.x, Gc.y))) : 0.f;
                 pl[u] = in ? L * p.scale * own : 0.f;
                 al[u] = below ? -be * L * raw : 0.f;
                 const float B = below ? -raw * (u ? Ah.y + Al.y : Ah.x + Al.x) : 0.f;
