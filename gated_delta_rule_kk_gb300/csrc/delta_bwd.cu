@@ -76,6 +76,13 @@ __global__ void __launch_bounds__(1024) delta_table_kernel(DeltaBwdParams p) {
   }
 }
 
+// Without tokens the states' gradients pass through, where the offsets are all zero.
+__global__ void __launch_bounds__(256) delta_none_kernel(DeltaBwdParams p, int64_t values) {
+  if (!offsets_ok(p.cu, p.N, 0, p.err)) return;
+  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < values; i += gridDim.x * 256ll)
+    p.dh0[i] = p.dht ? p.dht[i] : 0.f;
+}
+
 gdn_status_t check_args(const gdn_chunk_bwd_args &a, bool sizes_only) {
   CHECK_DTYPE(a.dtype, "dtype");
   CHECK_THAT(a.B >= 1 && a.T >= 0 && a.H >= 1 && a.Hg >= 1 && a.K >= 1 && a.V >= 1 && a.N >= 1,
@@ -170,12 +177,14 @@ gdn_status_t gdn_chunk_bwd(const gdn_chunk_bwd_args *a, gdn_stream_t stream) {
   if (st != GDN_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   DeltaBwdParams p = make_params(*a);
-  if (p.T == 0) {  // no token: the states' gradients pass through
-    if (p.dh0 == nullptr) return GDN_OK;
-    const size_t n = (size_t)p.N * p.H * p.K * p.V * sizeof(float);
-    return launch_status(p.dht ? cudaMemcpyAsync(p.dh0, p.dht, n, cudaMemcpyDeviceToDevice, s)
-                               : cudaMemsetAsync(p.dh0, 0, n, s),
-                         "state gradient copy");
+  if (p.T == 0) {
+    if (p.dh0 == nullptr && p.cu == nullptr) return GDN_OK;
+    p.err = device_error_word();
+    if (p.err == nullptr) return launch_status(cudaGetLastError(), "device error word");
+    const int64_t values = p.dh0 ? (int64_t)p.N * p.H * p.K * p.V : 0;
+    const int64_t blocks = std::min<int64_t>(4 * sm_count(), std::max<int64_t>(1, (values + 255) / 256));
+    delta_none_kernel<<<(unsigned)blocks, 256, 0, s>>>(p, values);
+    return launch_status(cudaGetLastError(), "state gradient copy");
   }
   const bool bf16 = a->dtype == GDN_BF16;
   const size_t need = workspace_bytes(p, bf16);

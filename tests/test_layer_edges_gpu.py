@@ -10,6 +10,7 @@ Pieces end at bfloat16's smallest step, 2^-133, half of which an operand is off 
 Each token that reaches dh0 adds two products to it, of do with q and of dr with k, whose rows
 of q and k have length 1: in norm sqrt(V) 2^-134 each.  (Counts where e^G is 1e-35.)
 """
+import ctypes
 import os
 import subprocess
 import sys
@@ -19,7 +20,8 @@ import pytest
 import torch
 
 import gated_delta_rule_kk_gb300 as gdn
-from gated_delta_rule_kk_gb300 import Status, build_lib
+from gated_delta_rule_kk_gb300 import Status, _lib, build_lib
+from gated_delta_rule_kk_gb300._lib import GdnChunkBwdArgs
 from oracle import layer as L
 
 from _layer import delta_inputs
@@ -74,6 +76,39 @@ def test_delta_gradient_of_many_gates_that_forget_and_shared_heads(dtype):
     got = run_delta(cuda(i))
     ok()
     check_norms(got, i)
+
+
+def test_delta_gradient_without_tokens_checks_its_offsets():
+    i = delta_inputs(15, 1, 0, 2, 2, 64, 64, BF16, [0, 0])
+    d = cuda(i)
+    assert torch.equal(run_delta(d)[5], d["dht"])
+    ok()
+    for cu in ([0, 5, 0], [0, 0, 3], [1, 1, 1]):
+        d["cu"] = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        run_delta(d)
+        assert gdn.gdn_check_device_error() == Status.BAD_SEQLENS, cu
+
+
+@pytest.mark.parametrize("dht", [False, True])
+def test_delta_gradient_of_bad_offsets_without_tokens_writes_nothing(dht):
+    """Also through the C entry, with and without a gradient of the last states."""
+    states = torch.ones(2, 2, 8, 8, device="cuda")
+    dh0 = torch.full_like(states, 7.0)
+    a = GdnChunkBwdArgs(dtype=1, B=1, T=0, H=2, Hg=2, K=8, V=8, N=2, chunk_size=64,
+                        dht=states.data_ptr() if dht else None, dh0=dh0.data_ptr())
+    for cu, status in (([0, 5, 0], Status.BAD_SEQLENS), ([0, 0, 1], Status.BAD_SEQLENS),
+                       ([0, 0, 0], Status.OK)):
+        at = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        a.cu_seqlens = at.data_ptr()
+        st = _lib.load().gdn_chunk_bwd(ctypes.byref(a), torch.cuda.current_stream().cuda_stream)
+        assert st == Status.OK and gdn.gdn_check_device_error() == status
+        want = 7.0 if status else float(dht)
+        assert torch.equal(dh0, torch.full_like(dh0, want))
+    a.cu_seqlens, a.B = None, 2
+    dh0.fill_(7)
+    assert _lib.load().gdn_chunk_bwd(ctypes.byref(a), torch.cuda.current_stream().cuda_stream) == Status.OK
+    assert torch.equal(dh0, torch.full_like(dh0, float(dht)))
+    ok()
 
 
 # ---------------------------------------------------------------- waits that run out
