@@ -109,8 +109,7 @@ NormPlan norm_plan(NormParams &p, bool bf16, int vec, bool bwd) {
   const int64_t down = std::max<int64_t>(1, std::min(held, wanted));
   p.step = (int)down * p.rows;
   plan.blocks = (int)(down * p.blocks_per_row);
-  // (three pieces are taken by the kernel for four)
-  const bool even = p.flat && n != 3 && p.team * n == all && teams == p.rows * p.span && p.G % p.span == 0;
+  const bool even = p.flat && p.team * n == all && teams == p.rows * p.span && p.G % p.span == 0;
   const bool made = p.team == 32 || (n == 1 && (p.team == 8 || p.team == 16));
   plan.team = even && made && vec * (bf16 ? 2 : 4) == 16 ? p.team : 0;
   return plan;
