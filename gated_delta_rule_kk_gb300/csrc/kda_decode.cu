@@ -375,21 +375,20 @@ __global__ void __launch_bounds__(32 * KD_WARPS) kda_decode_kernel(KdParams p) {
 // Many states stream through a ring of bulk copies: `stages` tiles, each with its item's
 // coefficients beside it.  Warps: KD_WARPS that take the tiles in place, KD_PREP that form
 // the coefficients (every KD_PREP-th item each), one that loads and one that stores tiles.
-// Every wait is bounded.  A warp whose wait ran out touches no stage any more and says so
-// before it arrives anywhere, and no tile is stored behind that: a state is the call's, or as it
-// was.
+// Every wait is bounded.  A warp whose wait ran out leaves: it touches no stage and arrives
+// nowhere any more, so that the others' waits run out behind it.  (An arrival without its wait
+// would let a stage be asked for before its copy has landed, which its barrier does not bear, or
+// be stored before it is done.)  A state is the call's then, or as it was.
 template <typename S, int LPR, int PP, int TM>
 __global__ void __launch_bounds__(KD_THREADS, KD_PER_SM)
 kda_decode_ring_kernel(KdParams p, int items) {
   extern __shared__ __align__(128) unsigned char ring[];
   __shared__ uint64_t full[KD_STAGES], ready[KD_STAGES], done[KD_STAGES], empty[KD_STAGES];
-  __shared__ int failed;
   constexpr int WARP_ROWS = KD_ROWS * 32 / LPR;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int role = warp < KD_WARPS ? 0 : warp < KD_WARPS + KD_PREP ? 1 : warp - KD_WARPS - KD_PREP + 2;
   const int coef_bytes = KdCoef(p.K, p.rows, p.T).bytes(), stages = p.stages;
   if (tid == 0) {
-    failed = 0;
     for (int s = 0; s < stages; ++s) {
       ptx::mbar_init(&full[s], 1);
       ptx::mbar_init(&ready[s], 1);
@@ -408,12 +407,6 @@ kda_decode_ring_kernel(KdParams p, int items) {
   auto wait = [&](uint64_t *bar, int use) {
     ok = ptx::mbar_wait_bounded(bar, (uint32_t)(use & 1), ok ? ptx::role_polls(role) : 1u) && ok;
   };
-  // whether this warp's waits have all ended well; else the block is told
-  auto fine = [&] {
-    const bool all = __all_sync(~0u, ok);
-    if (!all && lane == 0) *(volatile int *)&failed = 1;
-    return all;
-  };
   auto bytes_of = [&](const KdItem &it) {
     return (uint32_t)((it.end - it.v) * p.K * (int)sizeof(S));
   };
@@ -428,15 +421,15 @@ kda_decode_ring_kernel(KdParams p, int items) {
       const KdItem it = walk.place(p);
       wait(&ready[s], n / stages);
       wait(&full[s], n / stages);
-      const bool whole = fine();
-      if (whole && coef(s)[KdCoef(p.K, p.rows, p.T).good()] != 0.f) {
+      if (!__all_sync(~0u, ok)) break;
+      if (coef(s)[KdCoef(p.K, p.rows, p.T).good()] != 0.f) {
         if (warp * WARP_ROWS < it.end - it.v) {
           S *tile = reinterpret_cast<S *>(ring + s * KD_TILE);
           KdTile<S, LPR, PP> rows;
           rows.load(tile, warp * WARP_ROWS, it.end - it.v, p.K);
           rows.template take<TM>(p, it, tile, warp * WARP_ROWS, coef(s));
         }
-      } else if (whole) {
+      } else {
         kd_refuse(p, it, tid, 32 * KD_WARPS);
       }
       ptx::fence_proxy_async_smem();
@@ -452,14 +445,13 @@ kda_decode_ring_kernel(KdParams p, int items) {
       KdToken<S, LPR, PP> token;
       token.load(p, it, 0);
       if (n >= stages) wait(&done[s], n / stages - 1);
-      if (fine()) {
-        token.put(p, it, 0, coef(s));
-        for (int t = 1; t < p.T; ++t) {
-          token.load(p, it, t);
-          token.put(p, it, t, coef(s));
-        }
-        if (lane == 0) coef(s)[KdCoef(p.K, p.rows, p.T).good()] = kd_good(p, it) ? 1.f : 0.f;
+      if (!__all_sync(~0u, ok)) break;
+      token.put(p, it, 0, coef(s));
+      for (int t = 1; t < p.T; ++t) {
+        token.load(p, it, t);
+        token.put(p, it, t, coef(s));
       }
+      if (lane == 0) coef(s)[KdCoef(p.K, p.rows, p.T).good()] = kd_good(p, it) ? 1.f : 0.f;
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&ready[s]);
     }
@@ -468,7 +460,7 @@ kda_decode_ring_kernel(KdParams p, int items) {
       const int s = n % stages;
       const KdItem it = walk.item(p);
       if (n >= stages) wait(&empty[s], n / stages - 1);
-      if (!fine()) break;
+      if (!__all_sync(~0u, ok)) break;
       if (lane == 0) {
         if (kd_good(p, it)) {
           ptx::mbar_arrive_expect_tx(&full[s], bytes_of(it));
@@ -487,9 +479,9 @@ kda_decode_ring_kernel(KdParams p, int items) {
       const int s = n % stages;
       const KdItem it = walk.item(p);
       wait(&done[s], n / stages);
+      if (!__all_sync(~0u, ok)) break;
       if (lane == 0) {
-        if (kd_good(p, it) && ok && !*(volatile int *)&failed)
-          ptx::bulk_s2g(kd_tile_at<S>(p, it), ring + s * KD_TILE, bytes_of(it));
+        if (kd_good(p, it)) ptx::bulk_s2g(kd_tile_at<S>(p, it), ring + s * KD_TILE, bytes_of(it));
         ptx::bulk_commit();
         if (n > 0) {  // the store before has read its tile
           ptx::bulk_wait_read<1>();
