@@ -21,7 +21,9 @@
 // Backward, what q and do add (E = P^T do and U = (scale e^G q)^T do) does not wait for D: a
 // second set of warps forms it beside the ones that carry D.  One more warp loads chunks, two
 // stages deep, and one stores the states: the bulk copies' issue alone took a carrying warp
-// 500 cycles a chunk.  Every wait is bounded.
+// 500 cycles a chunk.  Every wait is bounded; a warp whose wait ran out asks for nothing and
+// arrives nowhere any more (a stage would be asked for before its copies have landed, which its
+// barrier does not bear), so that the others' waits run out behind it.
 #include <algorithm>
 
 #include "delta_bwd_tc.cuh"
@@ -161,7 +163,7 @@ struct Walk {
   }
   __device__ __forceinline__ void arrive(uint64_t *bar) const {
     __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(bar);
+    if (lane == 0 && ok) ptx::mbar_arrive(bar);
   }
   // The two warps of 16 value columns meet.
   __device__ __forceinline__ void meet() const {
@@ -275,8 +277,9 @@ struct Walk {
   __device__ __forceinline__ void store(Image image) {
     for (int i = 0; i < count; ++i) {
       wait(ready, i);
+      if (!__all_sync(~0u, ok)) break;
       if (lane == 0) {
-        if (ok) ptx::bulk_s2g(image(i), tiles(Sh::S_AT), Block<KP>::STATE);
+        ptx::bulk_s2g(image(i), tiles(Sh::S_AT), Block<KP>::STATE);
         ptx::bulk_commit();
         ptx::bulk_wait_read<0>();
         ptx::mbar_arrive(stored);
