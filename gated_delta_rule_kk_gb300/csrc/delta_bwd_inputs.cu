@@ -12,7 +12,9 @@
 // One block an SM, persistent, 20 warps: loads; the tcgen05 issuer; <h, D>; one that fetches
 // q and k and adds up dbeta and dg; sixteen that finish.  (q and k come as a bulk copy a row:
 // as 16-byte copies by all threads they held those up for 4500 cycles a chunk.)  Every wait is
-// bounded; a role whose wait ran out issues nothing more.
+// bounded; a warp whose wait ran out asks for nothing and arrives nowhere any more (a stage would
+// be asked for before its copies have landed, which its barrier does not bear), so that the
+// others' waits run out behind it.
 // At 2 x 4096 tokens, 16 heads of 128, 129 us: 628 MB at 4.9 TB/s (72% of the copy rate), the
 // tensor pipes busy 47% of the time; the finishing warps' phases, which wait for each other,
 // set the pace.  (All on warp-level instructions, 16 warps a chunk, phase after phase: 245 us,
@@ -333,13 +335,13 @@ __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdPar
             for (int e = 0; e < 8; ++e) sum = fmaf(x[0][e], y[0][e], sum);
           }
           __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&st_empty[s & 1]);
+          if (lane == 0 && ok) ptx::mbar_arrive(&st_empty[s & 1]);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
         // (with the accumulators taken over, x_full's phase before is over)
         if (m >= 1) wait(&x_empty, m - 1);
-        if (lane == 0) {
+        if (lane == 0 && ok) {
           hD[m & 3] = sum;
           ptx::mbar_arrive(&x_full);
         }
@@ -426,7 +428,7 @@ __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdPar
         for (int e = 0; e < 2; ++e)
           if (lane + 32 * e < ch.len) p.dg[(ch.token + lane + 32 * e) * p.H + head] = d[e];
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&counted[m & 1]);
+        if (lane == 0 && ok) ptx::mbar_arrive(&counted[m & 1]);
       }
     }
     for (int k = max(0, n - 2); k < n; ++k) settle(&kq_full[k & 1], k / 2);  // all have landed
@@ -472,13 +474,11 @@ __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdPar
         if (!last || it.there()) fetch_gates(last ? it.c : c, last ? it.hk * rep : head + 1);
         ptx::fence_proxy_async_smem();
         finishers_meet();
-        if (tid == 0) {  // the head before is through: P and A to where dP L and dA L beta will be
+        if (tid == 0 && ok) {  // the head before is through: P and A to where dP L and dA L beta will be
           if (head == hk * rep) ptx::mbar_arrive(&begun);
-          if (ok) {
-            pa_asked = m + 1;
-            ptx::mbar_arrive_expect_tx(&pa_full, 2 * Block<KP>::SQUARE);
-            ptx::bulk_g2s(PL, Block<KP>(p, c, head).P(), 2 * Block<KP>::SQUARE, &pa_full);
-          }
+          pa_asked = m + 1;
+          ptx::mbar_arrive_expect_tx(&pa_full, 2 * Block<KP>::SQUARE);
+          ptx::bulk_g2s(PL, Block<KP>(p, c, head).P(), 2 * Block<KP>::SQUARE, &pa_full);
         }
         wait(&x_full, m);
         ptx::tc_fence_after();
@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdPar
           }
           ptx::tc_fence_before();
           __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&x_empty);
+          if (lane == 0 && ok) ptx::mbar_arrive(&x_empty);
           // the terms with h and D, and their products with q and k
           float a[2] = {}, b[2] = {}, d[2] = {};
 #pragma unroll
@@ -636,7 +636,7 @@ __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdPar
           }
         }
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&summed[m & 1]);
+        if (lane == 0 && ok) ptx::mbar_arrive(&summed[m & 1]);
       }
     }
   }
