@@ -578,6 +578,8 @@ __device__ __forceinline__ void ssm_decode_tile(const SsmDecodeParams &p, const 
   }
 }
 
+// A warp whose wait ran out leaves: it touches no stage and arrives nowhere any more, so that the
+// others' waits run out behind it and a state is the call's, or as it was.
 template <typename S, int LPR, int PP, int TM>
 __global__ void __launch_bounds__(SD_THREADS, sd_blocks(TM))
 ssm_decode_ring_kernel(SsmDecodeParams p, int items) {
@@ -585,6 +587,7 @@ ssm_decode_ring_kernel(SsmDecodeParams p, int items) {
   __shared__ uint64_t full[SD_STAGES], ready[SD_STAGES], done[SD_STAGES], empty[SD_STAGES];
   constexpr int WARP_ROWS = SD_ROWS * 32 / LPR;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int role = warp < SD_WARPS ? 0 : warp < SD_WARPS + SD_PREP ? 1 : warp - SD_WARPS - SD_PREP + 2;
   const int coef_bytes = SdCoef(p.K, p.rows, p.T).bytes();
   if (tid == 0) {
     for (int s = 0; s < SD_STAGES; ++s) {
@@ -602,7 +605,7 @@ ssm_decode_ring_kernel(SsmDecodeParams p, int items) {
     return;
   bool ok = true;
   auto wait = [&](uint64_t *bar, int use) {
-    ok = ptx::mbar_wait_bounded(bar, (uint32_t)(use & 1), ok ? 1u << 22 : 1u) && ok;
+    ok = ptx::mbar_wait_bounded(bar, (uint32_t)(use & 1), ok ? ptx::role_polls(role) : 1u) && ok;
   };
   auto item_at = [&](int i) {
     SdItem it;
@@ -631,6 +634,7 @@ ssm_decode_ring_kernel(SsmDecodeParams p, int items) {
       const SdItem it = item_at(i);
       wait(&ready[s], n / SD_STAGES);
       wait(&full[s], n / SD_STAGES);
+      if (!__all_sync(~0u, ok)) break;
       if (good(it)) {
         if (warp * WARP_ROWS < p.rows)
           ssm_decode_tile<S, LPR, PP, TM>(p, it, warp * WARP_ROWS,
@@ -656,6 +660,7 @@ ssm_decode_ring_kernel(SsmDecodeParams p, int items) {
       const int s = n % SD_STAGES;
       const SdItem it = item_at(i);
       if (n >= SD_STAGES) wait(&done[s], n / SD_STAGES - 1);
+      if (!__all_sync(~0u, ok)) break;
       ssm_decode_prepare<TM>(p, it, coef(s));
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&ready[s]);
@@ -685,8 +690,9 @@ ssm_decode_ring_kernel(SsmDecodeParams p, int items) {
       const int s = n % SD_STAGES;
       const SdItem it = item_at(i);
       wait(&done[s], n / SD_STAGES);
+      if (!__all_sync(~0u, ok)) break;
       if (lane == 0) {
-        if (good(it) && ok) ptx::bulk_s2g(tile_of(it), ring + s * SD_TILE, bytes_of(it));
+        if (good(it)) ptx::bulk_s2g(tile_of(it), ring + s * SD_TILE, bytes_of(it));
         ptx::bulk_commit();
         if (n > 0) {  // the store before has read its tile
           ptx::bulk_wait_read<1>();

@@ -232,6 +232,33 @@ def test_kda_tokens_whose_waits_run_out_leave_states_whole(role, waiting_out):
     run_waiting_out(KDA_WAITS, role, waiting_out)
 
 
+SSM_WAITS = r"""
+from _mixer import ssm_inputs
+d = cuda(ssm_inputs(5, 400, 2, 16, 2, 64, 128, BF16, h0=False))
+g = torch.Generator(device="cuda").manual_seed(1)
+before = torch.randn(400, 16, 64, 128, device="cuda", generator=g).bfloat16()
+
+
+def tokens(state):
+    gdn.ssm_decode(d["x"], d["dt"], d["A_log"], d["Bm"], d["Cm"], state, dt_bias=d["dt_bias"])
+    return state
+
+
+after = call(release, lambda: tokens(before.clone()), Status.OK)
+mid = call(other, lambda: tokens(before.clone()), Status.TIMEOUT)
+same, done = ((mid == x).all(-1) for x in (before, after))
+assert (same | done).all(), int((~(same | done)).sum())
+if role in (0, 3):
+    assert same.all()
+assert torch.equal(call(release, lambda: tokens(before.clone()), Status.OK), after)
+"""
+
+
+@pytest.mark.parametrize("role", [0, 1, 2, 3])
+def test_state_space_tokens_whose_waits_run_out_leave_states_whole(role, waiting_out):
+    run_waiting_out(SSM_WAITS, role, waiting_out)
+
+
 DELTA_WAITS = r"""
 import ctypes
 from gated_delta_rule_kk_gb300._lib import GdnChunkBwdArgs
