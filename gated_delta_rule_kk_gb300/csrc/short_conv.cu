@@ -480,7 +480,8 @@ conv_ring_kernel(const __grid_constant__ CUtensorMap tm_x,
   __syncthreads();
   bool ok = true;
   auto wait = [&](uint64_t *bar, int use) {
-    ok = ptx::mbar_wait_bounded(bar, (uint32_t)(use & 1), ok ? 1u << 22 : 1u) && ok;
+    const int role = tid < R::THREADS ? 0 : 2;  // taking rows, loading
+    ok = ptx::mbar_wait_bounded(bar, (uint32_t)(use & 1), ok ? ptx::role_polls(role) : 1u) && ok;
   };
   if (tid >= R::THREADS) {
     const int boxes = p.D - c0 > CR_BOX ? R::BOXES : 1;
@@ -662,7 +663,9 @@ conv_ring_kernel(const __grid_constant__ CUtensorMap tm_x,
       }
     }
   };
-  // (every stage is waited for, also past the end: none is left on its way)
+  // (every stage is waited for, also past the end: none is left on its way; behind a wait that
+  // ran out a warp arrives nowhere any more, so that no stage is asked for before its copy has
+  // landed)
 #pragma unroll 1
   for (int u0 = lo, r = 0; u0 < stop; u0 += 4, r += 4) {
     const int s = r / CR_STAGE % S;
@@ -677,7 +680,7 @@ conv_ring_kernel(const __grid_constant__ CUtensorMap tm_x,
       rows4(u0, rows, std::false_type());
     if ((r + 4) % CR_STAGE == 0) {
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&empty[s]);
+      if (lane == 0 && ok) ptx::mbar_arrive(&empty[s]);
     }
   }
   if (BWD && open && eos == stop) {  // the slot that row `stop` would have had

@@ -259,6 +259,28 @@ def test_state_space_tokens_whose_waits_run_out_leave_states_whole(role, waiting
     run_waiting_out(SSM_WAITS, role, waiting_out)
 
 
+CONV_WAITS = r"""
+from _mixer import conv_inputs
+d = cuda(conv_inputs(5, 2, 4096, 6144, 4, BF16))
+
+
+def rows():
+    y, _ = gdn.short_conv_fwd(d["x"], d["weight"], d["bias"])
+    return y, *gdn.short_conv_bwd(d["dy"], d["x"], d["weight"], d["bias"])[:3]
+
+
+want = call(release, rows, Status.OK)
+call(other, rows, Status.TIMEOUT)
+for a, b in zip(want, call(release, rows, Status.OK)):
+    assert torch.equal(a, b)
+"""
+
+
+@pytest.mark.parametrize("role", [0, 2])
+def test_convolution_whose_waits_run_out_ends(role, waiting_out):
+    run_waiting_out(CONV_WAITS, role, waiting_out)
+
+
 DELTA_WAITS = r"""
 import ctypes
 from gated_delta_rule_kk_gb300._lib import GdnChunkBwdArgs
