@@ -46,7 +46,7 @@ constexpr int KD_WARPS = 8, KD_ROWS = 4;
 // The ring: two blocks an SM (three would leave a thread 48 registers, and its rows would
 // spill), each with as many stages as its half of the shared memory holds, up to KD_STAGES.
 // (A preparing warp skips the others' items; it may not skip a use of a barrier, so no more
-// of them work than there are stages: 256 channels and four tokens have three.)
+// of them work than there are stages: 256 channels, one token or two, have five.)
 constexpr int KD_STAGES = 6, KD_PREP = 4, KD_PER_SM = 2;
 constexpr uint32_t KD_TILE = 16384;
 // Shared memory of a ring, at most (the kernels' limit is this, whatever a call takes: calls
@@ -350,7 +350,7 @@ __device__ __forceinline__ void kd_refuse(const KdParams &p, const KdItem &it, i
     for (int r = it.v + tid; r < it.end; r += n) kd_put(p, it, t, r, 0.f);
 }
 
-// Few states: one block a tile.  The rows are on their way while the coefficients form.
+// Few states, or several tokens: one block a tile.  The rows are on their way while the coefficients form.
 template <typename S, int LPR, int PP, int TM>
 __global__ void __launch_bounds__(32 * KD_WARPS) kda_decode_kernel(KdParams p) {
   extern __shared__ __align__(128) float coef[];
@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(32 * KD_WARPS) kda_decode_kernel(KdParams p) {
   rows.template take<TM>(p, it, tile, warp * WARP_ROWS, coef);
 }
 
-// Many states stream through a ring of bulk copies: `stages` tiles, each with its item's
+// Many states of one token (float32 ones of two) stream through a ring of bulk copies: `stages` tiles, each with its item's
 // coefficients beside it.  Warps: KD_WARPS that take the tiles in place, KD_PREP that form
 // the coefficients (every KD_PREP-th item each), one that loads and one that stores tiles.
 // Every wait is bounded.  A warp whose wait ran out leaves: it touches no stage and arrives
@@ -398,7 +398,7 @@ kda_decode_ring_kernel(KdParams p, int items) {
     ptx::fence_mbar_init();
   }
   __syncthreads();
-  if (!bounds_ok(stages >= 1 && stages <= KD_STAGES && p.rows > 0 &&
+  if (!bounds_ok(stages >= KD_PREP && stages <= KD_STAGES && p.rows > 0 &&
                      p.rows <= KD_WARPS * WARP_ROWS &&
                      p.rows * p.K * (int)sizeof(S) <= (int)KD_TILE,
                  p.err))
@@ -437,9 +437,8 @@ kda_decode_ring_kernel(KdParams p, int items) {
       if (lane == 0) ptx::mbar_arrive(&done[s]);
     }
   } else if (warp < KD_WARPS + KD_PREP) {
-    const int preps = min(KD_PREP, stages);
     for (int i = blockIdx.x; i < items; i += gridDim.x, ++n, walk.next(p)) {
-      if (n % preps != warp - KD_WARPS) continue;
+      if (n % KD_PREP != warp - KD_WARPS) continue;
       const int s = n % stages;
       const KdItem it = walk.item(p);
       KdToken<S, LPR, PP> token;
@@ -495,6 +494,20 @@ kda_decode_ring_kernel(KdParams p, int items) {
   if (!ok && lane == 0) record_error(p.err, GDN_ERR_TIMEOUT);
 }
 
+// Tiles a block of the ring from where it is the faster one; 0: nowhere.  Its warps form tokens'
+// coefficients for several tiles in turn and are what a call of several tokens waits for; the
+// direct kernel has a warp a token.  Requests of 32 heads of 128 x 128, ring / direct, us:
+//   bf16 states  1 token: 8 requests (1.7 tiles a block) 7.5 / 7.0, 16 9.9 / 10.7, 64 27.8 / 33.9,
+//                256 97.6 / 138.8; 2 tokens: 16 14.2 / 12.3, 256 161.6 / 161.0;
+//                4 tokens: 2 12.0 / 4.9, 256 285 / 214
+//   float32      1 token: 8 (3.4) 8.5 / 7.6, 16 (6.7) 12.6 / 13.3, 256 169.5 / 197;
+//                2 tokens: 16 17.5 / 15.8, 64 (27) 57.7 / 61.4, 256 205.8 / 228.8;
+//                4 tokens: 3 12.3 / 6.2, 256 363 / 302
+template <typename S, int TM>
+constexpr int kd_ring_from() {
+  return TM == 1 ? 4 : TM == 2 && sizeof(S) == 4 ? 16 : 0;
+}
+
 template <typename S, int LPR, int PP, int TM>
 cudaError_t launch_kda(KdParams &p, cudaStream_t stream) {
   constexpr int ROWS = KD_WARPS * KD_ROWS * 32 / LPR;
@@ -503,18 +516,20 @@ cudaError_t launch_kda(KdParams &p, cudaStream_t stream) {
   p.vblocks = (p.V + rows - 1) / rows;
   p.rows = (p.V + p.vblocks - 1) / p.vblocks;
   const int coef = KdCoef(p.K, p.rows, p.T).bytes();
-  p.stages = std::min(KD_STAGES, KD_RING / ((int)KD_TILE + coef));
-  const int smem = p.stages * ((int)KD_TILE + coef);
-  const int blocks = KD_PER_SM * sm_count();
   const int64_t items = bh * p.vblocks;
-  if (items >= blocks && items <= 0x7fff0000) {
-    const cudaError_t e = cudaFuncSetAttribute(kda_decode_ring_kernel<S, LPR, PP, TM>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, KD_RING);
-    if (e != cudaSuccess) return e;
-    kda_decode_ring_kernel<S, LPR, PP, TM><<<blocks, KD_THREADS, smem, stream>>>(p, (int)items);
-  } else {
-    kda_decode_kernel<S, LPR, PP, TM><<<(unsigned)items, 32 * KD_WARPS, coef, stream>>>(p);
+  if constexpr (kd_ring_from<S, TM>() > 0) {
+    const int blocks = KD_PER_SM * sm_count();
+    if (items >= kd_ring_from<S, TM>() * blocks && items <= 0x7fff0000) {
+      p.stages = std::min(KD_STAGES, KD_RING / ((int)KD_TILE + coef));
+      const int smem = p.stages * ((int)KD_TILE + coef);
+      const cudaError_t e = cudaFuncSetAttribute(kda_decode_ring_kernel<S, LPR, PP, TM>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, KD_RING);
+      if (e != cudaSuccess) return e;
+      kda_decode_ring_kernel<S, LPR, PP, TM><<<blocks, KD_THREADS, smem, stream>>>(p, (int)items);
+      return cudaGetLastError();
+    }
   }
+  kda_decode_kernel<S, LPR, PP, TM><<<(unsigned)items, 32 * KD_WARPS, coef, stream>>>(p);
   return cudaGetLastError();
 }
 

@@ -24,7 +24,7 @@ from gated_delta_rule_kk_gb300 import Status, _lib, build_lib
 from gated_delta_rule_kk_gb300._lib import GdnChunkBwdArgs
 from oracle import layer as L
 
-from _layer import delta_inputs
+from _layer import delta_inputs, kda_inputs
 from _mixer import assert_each_close, cuda
 from _util import TOL_F32, _np
 from test_layer_gpu import PIECES, run_delta
@@ -206,7 +206,7 @@ def call(lib, f, status):
 """
 
 KDA_WAITS = r"""
-d = cuda(kda_inputs(5, 300, 2, 2, 4, 128, 128, BF16, BF16))
+d = cuda(kda_inputs(5, 400, 1 + role % 2, 2, 4, 128, 128, BF16, F32 if role % 2 else BF16))
 before = d["state"].clone()
 
 
@@ -321,3 +321,27 @@ def test_delta_gradient_whose_waits_run_out_ends(role, waiting_out):
     """Warps that carry (finish), hand on (multiply), load or store (count): the call ends with
     an error, nothing is written elsewhere and the next call is right."""
     run_waiting_out(DELTA_WAITS, role, waiting_out)
+
+
+# ---------------------------------------------------------------- KDA's tokens, both kernels
+
+@pytest.mark.parametrize("T,state", [(1, BF16), (1, F32), (2, BF16), (2, F32), (3, F32), (4, BF16)])
+@pytest.mark.parametrize("K,V", [(128, 128), (256, 72), (40, 24)])
+def test_kda_tokens_of_many_requests_are_those_of_few(T, state, K, V):
+    """A call whose states stream and calls of a few requests each: the same to the bit (the
+    kernels share the arithmetic of a tile), other slots untouched."""
+    B = 600
+    d = cuda(kda_inputs(9, B, T, 2, 4, K, V, BF16, state))
+    before, few = d["state"].clone(), d["state"].clone()
+
+    def tokens(pool, lo, hi):
+        return gdn.kda_decode(*(d[n][lo:hi] for n in ("q", "k", "v", "a", "b")), d["A_log"],
+                              d["dt_bias"], pool, slot_indices=d["slots"][lo:hi].contiguous())
+
+    o = tokens(d["state"], 0, B)
+    parts = torch.cat([tokens(few, lo, lo + 40) for lo in range(0, B, 40)])
+    ok()
+    assert torch.equal(o, parts) and torch.equal(d["state"], few)
+    others = torch.ones(len(before), dtype=torch.bool, device="cuda")
+    others[d["slots"].long()] = False
+    assert torch.equal(d["state"][others], before[others])
