@@ -4,7 +4,7 @@
 //
 // A chunk and head reads 290 KB and writes 32 (K = V = 128), and multiplies
 //   do h^T, dr h^T, n D^T [64][K] and do n^T, dr n^T [64][64],
-// each over the V value columns, with h, D, n and dr as two bfloat16 pieces: 43 of the 58
+// each over the V value columns, with h, D, n and dr as two bfloat16 pieces: 11.5 of the 14.2
 // million multiplications of a chunk.  These five go to tcgen05, whose accumulators take all
 // of tensor memory, while the warps finish the chunk before: they take over the accumulators
 // (as fragments, which is how tcgen05.ld's 16x256b form gives them), apply gates and masks,
@@ -15,7 +15,7 @@
 // bounded; a warp whose wait ran out asks for nothing and arrives nowhere any more (a stage would
 // be asked for before its copies have landed, which its barrier does not bear), so that the
 // others' waits run out behind it.
-// At 2 x 4096 tokens, 16 heads of 128, 129 us: 628 MB at 4.9 TB/s (72% of the copy rate), the
+// At 2 x 4096 tokens, 16 heads of 128, 130 us: 628 MB at 4.8 TB/s (71% of the copy rate), the
 // tensor pipes busy 47% of the time; the finishing warps' phases, which wait for each other,
 // set the pace.  (All on warp-level instructions, 16 warps a chunk, phase after phase: 245 us,
 // of which the products took 6 of 18 us a chunk and waiting for loads 5.)

@@ -8,8 +8,8 @@
 // latency of the products that wait for one another along a walk, half of it instructions: the
 // next 32 steps' operands are on their way in registers while 32 are multiplied, and every
 // load is of a place that exists, with the value chosen behind it, so that no load waits for
-// another.  (Three sequences of 261 to 376 tokens, 12 heads of 48 x 40, float32: 320 us; a
-// thread summing all steps, 256 of them, 353; with 16 steps a tile, two barriers each, and loads
+// another.  (Three sequences of 261 to 376 tokens, 12 heads of 48 x 40, float32: 323 us; a
+// thread summing all steps, 256 of them, 353 (then 320); with 16 steps a tile, two barriers each, and loads
 // inside branches 502.  A walk's rows and state kept in shared memory instead of the workspace
 // changed nothing.)
 #include "delta_bwd.h"

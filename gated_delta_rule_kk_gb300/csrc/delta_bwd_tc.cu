@@ -12,7 +12,8 @@ namespace {
 // block, T_(b+d, b) = -T_(b+d, b+d) sum_m A_(b+d, m) T_(m, b), as products of pairs of
 // bfloat16 pieces: transposed, so that the sum's accumulators are the left operand of the
 // product behind it.  (As float32 sums from shared memory, two loads a multiplication, they
-// took a third of the kernel's instructions: 80 us at 2 x 4096 tokens, 16 heads of 128; now 53.)
+// took a third of the kernel's instructions: 80 us at 2 x 4096 tokens, 16 heads of 128; then 53.
+// Now 55: the sums' rests.)
 // Barriers between the phases are what a warp waits for most: four blocks an SM, T in the place
 // of the images before it (three blocks: 59 us).
 constexpr int PREP = 256;
@@ -198,6 +199,10 @@ cudaError_t launch(const DeltaBwdParams &p, cudaStream_t stream) {
 
 }  // namespace
 
+// (2 x 4096 tokens, 16 heads, K x V, tensor cores / CUDA cores, us: 128 x 128 465 / 5170,
+// 120 x 128 471 / 5090; on CUDA cores 127 x 128 5190, 128 x 136 5090, 128 x 256 5960.  Rows of K
+// and V that are no multiples of 8 do not begin on the 16 bytes that the copies want; that V ends
+// at 128 is a limit of what was tried, as value tiles do not depend on one another.)
 bool delta_bwd_tc_supported(const DeltaBwdParams &p, bool bf16) {
   return bf16 && p.K % 8 == 0 && p.V % 8 == 0 && p.K <= 128 && p.V <= 128;
 }

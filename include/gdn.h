@@ -80,7 +80,13 @@ typedef enum gdn_dtype {
  *                                     g_is_cumsum = 1 it is instead the
  *                                     inclusive cumulative sum inside each
  *                                     64-token chunk (chunks counted from
- *                                     each sequence's first token)
+ *                                     each sequence's first token).  The
+ *                                     sums are held in float32: a gate of
+ *                                     -1e4 costs the tokens behind it in
+ *                                     its chunk 5e-3 of o, -80 3e-5, and
+ *                                     -infinity or the lowest float leaves
+ *                                     NaN; -104 forgets as much as those
+ *                                     (e^-104 is zero in float32)
  *   beta   [B, T, H]      float32
  *   h0     [N, H, K, V]   float32     initial state h = S^T, NULL = zeros
  *   ht     [N, H, K, V]   float32     final state, NULL = not returned
@@ -301,8 +307,8 @@ gdn_status_t gdn_chunk_host_workspace_size(const gdn_chunk_args *args, size_t *b
  *                                          zeros / zeros / not returned
  *   cu_seqlens    [N + 1]         int32    as gdn_chunk_fwd; with bad offsets nothing is
  *                                          written
- * A per-token gate may be anything up to -infinity (the state is forgotten: e^g is zero below
- * -104); a chunk-local sum has to be finite.
+ * A per-token gate may be anything down to -infinity (the state is forgotten: e^g is zero below
+ * -104), although gdn_chunk_fwd wants it above some -1e2; a chunk-local sum has to be finite.
  * A NaN or an infinity in v or do may reach every token of its chunk and, of its sequence,
  * those that its state or the state's gradient reaches; other sequences and heads (but for dq
  * and dk of its key head) are as without it.
@@ -724,6 +730,8 @@ gdn_status_t group_norm_bwd(const group_norm_bwd_args *args, gdn_stream_t stream
  *   slot_indices [B]        int32    as gdn_decode
  * Token tensors are strided as in ssm_chunk_fwd: column ranges of wider buffers, so that q,
  * k and v may be columns of the short convolution's output.  Outputs must not overlap inputs.
+ * A call that ends with GDN_ERR_TIMEOUT in the device error word leaves every row of the states
+ * as the call's, or as it was.
  * Limits: 8 <= K <= 256, K % 8 == 0, HV % H == 0, HV at most 65535.  scale <= 0 selects
  * 1/sqrt(K); eps < 0 selects 1e-6.
  */

@@ -23,6 +23,7 @@ import gated_delta_rule_kk_gb300 as gdn
 from gated_delta_rule_kk_gb300 import Status, _lib, build_lib
 from gated_delta_rule_kk_gb300._lib import GdnChunkBwdArgs
 from oracle import layer as L
+from oracle import mixer as M
 
 from _layer import delta_inputs, kda_inputs
 from _mixer import assert_each_close, cuda
@@ -345,3 +346,53 @@ def test_kda_tokens_of_many_requests_are_those_of_few(T, state, K, V):
     others = torch.ones(len(before), dtype=torch.bool, device="cuda")
     others[d["slots"].long()] = False
     assert torch.equal(d["state"][others], before[others])
+
+
+# ---------------------------------------------------------------- a layer that serves
+
+def test_a_layer_serves():
+    """A KDA layer: two prompts through convolution, recurrence and gated norm into pooled
+    states, then 1, 2, 4 and 1 tokens of each through the same three, against the whole in 64
+    bits.  (Tokens and prompts are within 1e-5 of o's RMS; the norm divides by a head's own
+    size, and where that is a thirtieth of the RMS an error is thirty times as large.)"""
+    B, T, H, K, V, W = 2, 70, 2, 64, 32, 4
+    g = torch.Generator().manual_seed(8)
+
+    def normal(*shape, std=1.0):
+        return torch.randn(*shape, generator=g) * std
+
+    D, whole = H * (2 * K + V), T + 8
+    x, z, a = normal(B, whole, D), normal(B, whole, H * V), normal(B, whole, H, K)
+    b, cw, nw = normal(B, whole, H), normal(D, W, std=0.5), torch.rand(V, generator=g) + 0.5
+    A_log, dt_bias = torch.log(torch.rand(H, generator=g) * 15 + 1), normal(H, K) - 3
+    how = dict(center=False, activation="silu")
+
+    def heads(u):
+        return (t.unflatten(2, (H, -1)) for t in u.split([H * K, H * K, H * V], 2))
+
+    u = torch.from_numpy(M.short_conv(x, cw, None)[0])
+    o, _ = L.kda_decode(*heads(u), a, b, A_log, dt_bias, torch.zeros(B, H, V, K))
+    want = L.group_norm(o.reshape(B, whole, -1), H, nw, z=z, **how)
+
+    c = [t.cuda() for t in (x, z, a, b, cw, nw, A_log, dt_bias)]
+    x, z, a, b, cw, nw, A_log, dt_bias = c
+    slots = torch.tensor([3, 0], dtype=torch.int32, device="cuda")
+    rows, states = torch.zeros(4, W - 1, D, device="cuda"), torch.zeros(4, H, V, K, device="cuda")
+    u, last = gdn.short_conv_fwd(x[:, :T], cw)
+    q, k, v = (t.contiguous() for t in heads(u))
+    q, k = (t / (t.square().sum(-1, keepdim=True) + 1e-6).sqrt() for t in (q, k))
+    gate = -torch.exp(A_log)[:, None] * torch.nn.functional.softplus(a[:, :T] + dt_bias)
+    o, ht = gdn.kda_chunk_fwd(q, k, v, gate.contiguous(), torch.sigmoid(b[:, :T]).contiguous(),
+                              g_is_cumsum=False, state_v_first=True)
+    rows[slots.long()], states[slots.long()] = last, ht
+    got = [gdn.group_norm_fwd(o.flatten(2), H, nw, z=z[:, :T], **how)]
+    at = T
+    for n in (1, 2, 4, 1):
+        here = slice(at, at + n)
+        u = gdn.short_conv_decode(x[:, here], cw, rows, slot_indices=slots)
+        o = gdn.kda_decode(*heads(u), a[:, here], b[:, here], A_log, dt_bias, states, slot_indices=slots)
+        got.append(gdn.group_norm_fwd(o.flatten(2), H, nw, z=z[:, here], **how))
+        at += n
+    ok()
+    assert_each_close(torch.cat(got, 1), want, "y", 3e-4)
+    assert not states[1:3].any() and not rows[1:3].any()
