@@ -70,7 +70,15 @@ constexpr int NORM_WARPS = 32;
 // want the registers of half the threads).
 constexpr int norm_threads(int elements) { return elements > 8 ? 512 : 1024; }
 // Threads of an ordinary block; tokens whose rows are on their way and blocks an SM, by the
-// words that a thread's part of a row takes (some 48 KB of an SM's are on their way).
+// words that a thread's part of a row takes (some 48 KB of an SM's are on their way).  Above 8
+// channels a thread, us at 52 million values, weights of one group, the choice / the other one:
+//   forward, two blocks / three: bf16 with a gate, 512 channels 50 / 56, 1024 68 / 89, 4096 68 / 92;
+//     float32, 512 95 / 103, 1024 with a gate 99 / 104, without 81 / 69, 384 141 / 132, 125 / 97;
+//     one token ahead / two: float32, 1024 99 / 101
+//   backward, one block / two: bf16 with a gate, 512 90 / 100, 1024 174 / 212, float32, 1024
+//     190 / 291; without a gate two would be faster: bf16, 512 81 / 62, 1024 152 / 119, float32,
+//     1024 163 / 138 (512, whose ring takes an SM, 117 / 127); one token ahead / two: float32,
+//     1024 190 / 243, bf16 174 / 176
 constexpr int NORM_THREADS = 256;
 constexpr int norm_words(int elt, int vec, int pieces) {
   return pieces * (vec * elt >= 4 ? vec * elt / 4 : 1);
