@@ -15,6 +15,9 @@
 //   dG = rowsum(M) - colsum(M) + q.dq_h + k.dk_h - k.dk_s,   M = dA A + dP P,
 //   dG_L += e^(G_L) <h, D> + sum k.dk_s,
 // where dq_h, dk_h and dk_s are the terms with h and D; dg is dG summed from the chunk's end.
+// (There k.dk_s is what the tokens before add up to, and M's diagonal cancels: neither is summed
+// and taken off again, so that next to a gate that forgets, whose dg is as small as e^g, nothing
+// of order one has to cancel.)
 // (dA = -dr n^T holds as n solves (I + A) n = r: neither the gradient of T nor w = T beta e^G k
 // is formed.)  Four launches (five with packed sequences): T and P of every chunk; the states forward; their gradients
 // backward; everything else, every chunk by itself.
@@ -121,6 +124,23 @@ __device__ __forceinline__ float delta_gap(float Gi, float rest_i, float Gj, flo
 }
 __device__ __forceinline__ float delta_gap(float2 Gi, float2 Gj) {
   return delta_gap(Gi.x, Gi.y, Gj.x, Gj.y);
+}
+
+// Of x at a lane's tokens l and l + 32 the sums over the tokens before them; one warp.
+__device__ __forceinline__ void delta_before(float (&x)[2]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const float y = __shfl_up_sync(~0u, x[e], o);
+      if (lane >= o) x[e] += y;
+    }
+  }
+  const float half = __shfl_sync(~0u, x[0], 31);
+  const float a = __shfl_up_sync(~0u, x[0], 1), b = __shfl_up_sync(~0u, x[1], 1);
+  x[0] = lane > 0 ? a : 0.f;
+  x[1] = lane > 0 ? half + b : half;
 }
 
 // Whether the offsets were good (the table kernel marks bad ones).

@@ -388,14 +388,15 @@ __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdPar
         const float *qd = sums, *kh = qd + 4 * Q, *kD = kh + 4 * Q, *rM = kD + 4 * Q, *rB = rM + 4 * Q;
         const float *cM = rB + 4 * Q, *rn = cM + 4 * Q, *beta = rn + 3 * Q, *eG = beta + Q;
         const float state = hD[m & 3];
-        float d[2], db[2], all = 0.f;
+        float d[2], db[2], kds[2], all = 0.f;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int i = lane + 32 * e;
           auto all_of = [&](const float *x) { return (x[i] + x[Q + i]) + (x[2 * Q + i] + x[3 * Q + i]); };
           const float kd = all_of(kD), khi = all_of(kh);
-          d[e] = all_of(rM) - all_of(cM) + all_of(qd) + beta[i] * khi - kd;
-          all += kd;
+          d[e] = all_of(rM) - all_of(cM) + all_of(qd) + beta[i] * khi;
+          kds[e] = kd;
+          if (p.g_is_cumsum) d[e] -= kd, all += kd;
           // dbeta = dr.n / beta, as n is beta times what it does not depend on it by (of a beta
           // next to nothing the products of dr's and n's pieces could fall below float32)
           const bool none = fabsf(beta[i]) < 1e-12f;
@@ -423,6 +424,9 @@ __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdPar
             }
           }
           d[0] += __shfl_sync(~0u, d[1], 0);
+          delta_before(kds);
+          d[0] += kds[0];
+          d[1] += kds[1];
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e)
@@ -556,7 +560,7 @@ __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdPar
                 pl[u] = in ? L * p.scale * own : 0.f;
                 al[u] = below ? -be * L * raw : 0.f;
                 const float B = below ? -raw * (u ? Ah.y + Al.y : Ah.x + Al.x) : 0.f;
-                const float M = fmaf(in ? own : 0.f, u ? Ph.y + Pl.y : Ph.x + Pl.x, be * B);
+                const float M = fmaf(below ? own : 0.f, u ? Ph.y + Pl.y : Ph.x + Pl.x, be * B);
                 ms[e] += M;
                 bs[e] += B;
                 cols[j][u] += M;

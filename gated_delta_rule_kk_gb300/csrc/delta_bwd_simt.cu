@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(THREADS) simt_inputs_kernel(DeltaBwdParams p) 
     product<STEPS, STEPS>(Q, Q, V, s.tiles, go, nt, [&](int i, int j, float x) {
       const bool in = i >= j && i < ch.len;
       const float L = in ? p.scale * expf(delta_gap(G[i], rest[i], G[j], rest[j])) : 0.f;
-      s.M[i * SIDE + j] = L * x * s.P[i * SIDE + j];
+      s.M[i * SIDE + j] = i > j ? L * x * s.P[i * SIDE + j] : 0.f;
       s.P[i * SIDE + j] = L * x;
     });
     product<STEPS, STEPS>(Q, Q, K, s.tiles, k, kt, [&](int i, int j, float x) { s.A[i * SIDE + j] = x; });
@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(THREADS) simt_inputs_kernel(DeltaBwdParams p) 
     m = row_sum(m);
     b = row_sum(b);
     if (tid % EACH_ROW == 0) {
-      dG[row] = m + qd[row] + f.beta[row] * kh[row] - kD[row];
+      dG[row] = m + qd[row] + f.beta[row] * kh[row];
       if (row < ch.len) p.dbeta[(ch.token + row) * p.H + head] = sum + kh[row] + b;
     }
     // <h, D>
@@ -501,7 +501,8 @@ __global__ void __launch_bounds__(THREADS) simt_inputs_kernel(DeltaBwdParams p) 
     if (tid % 32 == 0) part[tid / 32] = sum;
     __syncthreads();
     if (tid < 32) {  // dG's sums from the end, two tokens a lane
-      float hD = 0.f, all = kD[tid] + kD[tid + 32];  // (kD is zero past the end)
+      float kds[2] = {kD[tid], kD[tid + 32]};  // (zero past the end)
+      float hD = 0.f, all = p.g_is_cumsum ? kds[0] + kds[1] : 0.f;
       for (int i = 0; i < THREADS / 32; ++i) hD += part[i];
       for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(~0u, all, o);
       float d[2];
@@ -509,6 +510,7 @@ __global__ void __launch_bounds__(THREADS) simt_inputs_kernel(DeltaBwdParams p) 
       for (int e = 0; e < 2; ++e) {
         const int i = tid + 32 * e;
         d[e] = i < ch.len ? dG[i] + (i == ch.len - 1 ? fmaf(keep, hD, all) : 0.f) : 0.f;
+        if (p.g_is_cumsum) d[e] -= kds[e];
       }
       if (!p.g_is_cumsum) {
 #pragma unroll
@@ -519,6 +521,9 @@ __global__ void __launch_bounds__(THREADS) simt_inputs_kernel(DeltaBwdParams p) 
             if (tid + o < 32) d[e] += x;
           }
         d[0] += __shfl_sync(~0u, d[1], 0);
+        delta_before(kds);
+        d[0] += kds[0];
+        d[1] += kds[1];
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e)

@@ -41,19 +41,24 @@ def ok():
 
 def check_norms(got, i, reach=64, **kw):
     """Every result element for element, the float32 ones within 1e-5 of their norm; ``reach``
-    tokens of a sequence reach its initial state."""
+    tokens of a sequence reach its initial state.  The norm's bound for pieces is that of many
+    independent errors (2^-19 of a value each, in quadrature): below 200 values of dg it says
+    nothing, as what is left of a sum whose terms cancel may be all there is (dg of two tokens and
+    heads is four such sums, of terms up to four times as large), and 3e-3 element for element,
+    which counts every term with its largest error, is the bound."""
     ref = L.gdn_grad(i["do"], i["q"], i["k"], i["v"], i["g"], i["beta"], i["scale"], i["h0"],
                      i["dht"], i["cu"], **kw)
-    pieces = i["q"].dtype is BF16
+    K, V = i["q"].shape[3], i["v"].shape[3]
+    pieces = i["q"].dtype is BF16 and K % 8 == 0 and V % 8 == 0 and V <= 128
     step = reach * 2 * 2.0 ** -134 * np.sqrt(ref[5].size / ref[5].shape[2]) if pieces else 0.0
     off = {}
     for name, x, r in zip(("dq", "dk", "dv", "dg", "dbeta", "dh0"), got, ref):
         if name != "dh0" or not pieces or np.abs(r).max() > 2.0 ** -100:
             assert_each_close(x, r, name, PIECES if pieces else TOL_F32)
-        if x.dtype is F32:
+        if x.dtype is F32 and (not pieces or ref[3].size >= 200):
             room = 1e-5 * np.linalg.norm(r) + (step if name == "dh0" else 0.0)
             off[name] = np.linalg.norm(_np(x) - r) / max(room, 1e-300)
-    assert max(off.values()) <= 1.0, {k: f"{v:.2f} times the allowed error" for k, v in off.items()}
+    assert max(off.values(), default=0) <= 1.0, {k: f"{v:.2f} times the allowed error" for k, v in off.items()}
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
@@ -67,6 +72,18 @@ def test_delta_gradient_of_many_gates_that_forget(dtype, every, gate):
     got = run_delta(cuda(i))
     ok()
     check_norms(got, i, reach=every)
+
+
+@pytest.mark.parametrize("dtype,K,V", [(BF16, 64, 64), (F32, 64, 64), (BF16, 20, 30)])
+@pytest.mark.parametrize("T", [1, 2, 63, 130])
+@pytest.mark.parametrize("gate", [-30.0, -15.0])
+def test_delta_gradient_where_every_gate_forgets(dtype, K, V, T, gate):
+    """dg is as small as e^g, and right to its own size: nothing of order one cancels in it."""
+    i = delta_inputs(T, 1, T, 2, 1, K, V, dtype)
+    i["g"][:] = gate
+    got = run_delta(cuda(i))
+    ok()
+    check_norms(got, i)
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
