@@ -4,7 +4,7 @@
 //
 // A chunk and head reads 290 KB and writes 32 (K = V = 128), and multiplies
 //   do h^T, dr h^T, n D^T [64][K] and do n^T, dr n^T [64][64],
-// each over the V value columns, with h, D, n and dr as two bfloat16 pieces: 11.5 of the 14.2
+// each over the V value columns, with h, D, n and dr as two bfloat16 pieces: 12.6 of the 15.2
 // million multiplications of a chunk.  These five go to tcgen05, whose accumulators take all
 // of tensor memory, while the warps finish the chunk before: they take over the accumulators
 // (as fragments, which is how tcgen05.ld's 16x256b form gives them), apply gates and masks,
@@ -15,7 +15,7 @@
 // bounded; a warp whose wait ran out asks for nothing and arrives nowhere any more (a stage would
 // be asked for before its copies have landed, which its barrier does not bear), so that the
 // others' waits run out behind it.
-// At 2 x 4096 tokens, 16 heads of 128, 130 us: 628 MB at 4.8 TB/s (71% of the copy rate), the
+// At 2 x 4096 tokens, 16 heads of 128, 135 us: 628 MB at 4.7 TB/s (69% of the copy rate), the
 // tensor pipes busy 47% of the time; the finishing warps' phases, which wait for each other,
 // set the pace.  (All on warp-level instructions, 16 warps a chunk, phase after phase: 245 us,
 // of which the products took 6 of 18 us a chunk and waiting for loads 5.)
@@ -296,6 +296,9 @@ __global__ void __launch_bounds__(32 * IN_WARPS, 1) tc_inputs_kernel(DeltaBwdPar
               ptx::mma_bf16(tmem + DA, dr, nl, square_t, 1);
               ptx::mma_bf16(tmem + XK, dl, h, wide_t, 1);
               ptx::mma_bf16(tmem + XS, nl, D, wide_t, 1);
+              // (dg adds its products with k up over the chunk: without this 1.3e-5 off where V
+              // is 8 or tokens are few, with it 6e-6; 2 us of 467)
+              ptx::mma_bf16(tmem + XS, nl, Dl, wide_t, 1);
               ptx::mma_bf16(tmem + DA, dl, n, square_t, 1);
               // (its diagonal gives dbeta, of terms that cancel: without this 6.4e-6 off)
               ptx::mma_bf16(tmem + DA, dl, nl, square_t, 1);

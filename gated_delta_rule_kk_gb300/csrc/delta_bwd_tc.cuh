@@ -7,8 +7,8 @@
 // registers (warp-level matrix instructions) instead of passing through tensor memory between
 // each two of them; what is plain contraction runs on tcgen05.  q, k, v and do are bfloat16 and
 // exact; what is float32 (T, P, the states h and their gradients D, the corrected values n and
-// dr) enters as a pair of bfloat16 pieces, hi + lo, with the products hi hi + hi lo + lo hi:
-// off by 2^-17 of each value at most, so that the float32 results (dg, dbeta, dh0) are not
+// dr) enters as a pair of bfloat16 pieces, hi + lo, with the products hi hi + hi lo + lo hi (lo lo
+// where dbeta and dg add many of them up): off by 2^-17 of each value at most, so that the float32 results (dg, dbeta, dh0) are not
 // bound by bfloat16.  Accumulation is float32.
 //
 // Images lie in shared memory as rows of 64, 128 or 256 bytes whose 16-byte pieces are

@@ -319,9 +319,9 @@ gdn_status_t gdn_chunk_host_workspace_size(const gdn_chunk_args *args, size_t *b
  * multiples of 8 and V <= 128 the products run on the tensor cores, whose operands carry
  * float32 values (states, their gradients, corrected values, T and P) as two bfloat16 pieces:
  * each is off by up to 2^-17 of itself (below 6e-36 by 2^-134), sums are float32, and dq, dk
- * and dv are rounded once (float32 results of some hundred tokens and heads are within 1e-5 of
- * their norm, 2e-5 with V = 8, those of a few tokens, whose errors do not average out, within
- * 3e-5; gates that forget, as many as there are, included).
+ * and dv are rounded once (float32 results are within 1e-5 of their norm, those of a few tokens,
+ * whose errors do not average out, within 3e-5; gates that forget, as many as there are,
+ * included).
  * Limits: as gdn_chunk_fwd, and V <= 2^20.  scale <= 0 selects 1/sqrt(K).
  * Workspace: gdn_chunk_bwd_workspace_size() bytes, device memory, 256-byte aligned: for every
  * chunk of 64 tokens and value head A, T, P, the corrected values and their gradients, the
